@@ -33,7 +33,9 @@ EXPORTS = ("dmtp_workspace_size", "dmtp_init", "dmtp_round", "dmtp_round_host",
            "dmtp_gate_result", "dmtp_gate_pick", "dmtp_gate_pick_p", "dmtp_gate_read",
            "dmtp_gate_free", "dmtp_vocab_create", "dmtp_vocab_begin_request",
            "dmtp_vocab_picked", "dmtp_vocab_ids", "dmtp_vocab_mask", "dmtp_vocab_counts",
-           "dmtp_vocab_stats_read", "dmtp_vocab_free")
+           "dmtp_vocab_stats_read", "dmtp_vocab_free",
+           "dmtp_paged_write", "dmtp_paged_read", "dmtp_paged_attention_workspace",
+           "dmtp_paged_attention", "dmtp_add_rmsnorm_e4m3", "dmtp_sample_rows")
 
 DMTP_GATE_MAX_DRAFTS = 32
 DMTP_GATE_MAX_ROWS = 64
@@ -103,6 +105,45 @@ class dmtp_profile(C.Structure):
                 ("round_ms", C.c_double), ("graph", C.c_int)]
 
 
+class dmtp_paged_kv(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("k_scale", C.c_void_p),
+                ("v_scale", C.c_void_p), ("table", C.c_void_p), ("page_stride", C.c_int64),
+                ("scale_stride", C.c_int64), ("table_stride", C.c_int64), ("n_pages", C.c_int),
+                ("page_size", C.c_int), ("n_kv_heads", C.c_int), ("head_dim", C.c_int),
+                ("n_seqs", C.c_int), ("max_blocks", C.c_int), ("dtype", C.c_int),
+                ("e4m3", C.c_int)]
+
+
+class dmtp_paged_rows(C.Structure):
+    _fields_ = ([(f, C.c_void_p) for f in ("q", "k", "v", "q_out")]
+                + [(f, C.c_int64) for f in ("q_row", "q_head", "k_row", "k_head", "v_row",
+                                            "v_head", "qo_row", "qo_head")]
+                + [("seq", C.c_void_p), ("pos", C.c_void_p), ("n_rows", C.c_int),
+                   ("n_heads", C.c_int), ("rope_theta", C.c_float)])
+
+
+class dmtp_paged_query(C.Structure):
+    _fields_ = ([("q", C.c_void_p), ("out", C.c_void_p)]
+                + [(f, C.c_int64) for f in ("q_seq", "q_row", "q_head", "o_seq", "o_row",
+                                            "o_head")]
+                + [("kv_len", C.c_void_p), ("rows", C.c_int), ("n_heads", C.c_int),
+                   ("window", C.c_int), ("scale", C.c_float)])
+
+
+class dmtp_norm_args(C.Structure):
+    _fields_ = ([(f, C.c_void_p) for f in ("x", "y", "gain", "x_out", "q", "scale")]
+                + [(f, C.c_int64) for f in ("x_row", "y_row", "xo_row", "q_row")]
+                + [(f, C.c_int) for f in ("rows", "d", "x_dtype", "y_dtype", "gain_dtype")]
+                + [("eps", C.c_float)])
+
+
+class dmtp_sample_args(C.Structure):
+    _fields_ = ([("logits", C.c_void_p), ("ld", C.c_int64), ("rows", C.c_int),
+                 ("vocab", C.c_int), ("dtype", C.c_int)]
+                + [(f, C.c_void_p) for f in ("u", "temperature", "top_k", "top_p", "min_p",
+                                             "ids", "kept")])
+
+
 _lib = None
 
 
@@ -169,6 +210,17 @@ def load_library(path: str = LIB_PATH):
         getattr(lib, "dmtp_vocab_" + f).restype = C.c_int
     lib.dmtp_vocab_free.argtypes = [P]
     lib.dmtp_vocab_free.restype = None
+    KV = C.POINTER(dmtp_paged_kv)
+    lib.dmtp_paged_write.argtypes = [KV, C.POINTER(dmtp_paged_rows), P, P]
+    lib.dmtp_paged_read.argtypes = [KV, P, P, C.c_int, P, P, P, P]
+    lib.dmtp_paged_attention_workspace.argtypes = [KV, C.POINTER(dmtp_paged_query),
+                                                   C.POINTER(C.c_size_t)]
+    lib.dmtp_paged_attention.argtypes = [KV, C.POINTER(dmtp_paged_query), P, C.c_size_t, P, P]
+    lib.dmtp_add_rmsnorm_e4m3.argtypes = [C.POINTER(dmtp_norm_args), P]
+    lib.dmtp_sample_rows.argtypes = [C.POINTER(dmtp_sample_args), P]
+    for f in ("paged_write", "paged_read", "paged_attention_workspace", "paged_attention",
+              "add_rmsnorm_e4m3", "sample_rows"):
+        getattr(lib, "dmtp_" + f).restype = C.c_int
     _lib = lib
     return lib
 

@@ -1,0 +1,144 @@
+// dmtp_paged_attention: argument checks, the plan (which kernel, how many CTAs, the
+// workspace) and the merge of split units.
+#include "paged_attn.cuh"
+
+using namespace dmtp;
+
+namespace {
+
+// The merge of one unit's pieces (paged_attn.cuh), one warp per query: with M the largest of
+// the pieces' maxima, out = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c, pieces in CTA
+// order. Units that one CTA wrote are left alone; units without a tile get zeros. Reads the
+// partial rows once: G x 2 x qn x (head_dim + 2) floats at most.
+template <typename T>
+__global__ void __launch_bounds__(128) k_paged_merge(const PagedAttn p, int ctas) {
+  pdl_wait();
+  const int b = blockIdx.y, unit = blockIdx.x, hd = p.m.head_dim;
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const long long total = p.prefix[p.m.n_seqs];
+  const int G = busy_ctas(total, ctas);
+  const int lo = p.prefix[b], n = (p.prefix[b + 1] - lo) / p.units;
+  const long long s0 = lo + (long long)unit * n;
+  int c0 = 0, c1 = -1;
+  if (n > 0) {
+    c0 = (int)(((s0 + 1) * G - 1) / total);
+    c1 = (int)(((s0 + n) * G - 1) / total);
+    if (c0 == c1) return;
+  }
+  const int nq = queries_of(p, unit);
+  for (int t = blockIdx.z * 4 + wid; t < nq; t += gridDim.z * 4) {
+    int head, row;
+    query_of(p, unit, t, &head, &row);
+    T* out = (T*)p.a.out + (int64_t)b * p.a.o_seq + (int64_t)row * p.a.o_row + (int64_t)head * p.a.o_head;
+    float M = -INFINITY, L = 0.f;
+    for (int c = c0 + lane; c <= c1; c += 32)
+      M = fmaxf(M, p.part_ml[(c * 2 + (c == c0)) * p.qn + t].x);
+    M = warp_max(M);
+    const float ref = M == -INFINITY ? 0.f : M;
+    for (int c = c0 + lane; c <= c1; c += 32) {
+      const float2 ml = p.part_ml[(c * 2 + (c == c0)) * p.qn + t];
+      L += ml.y * ex2(ml.x - ref);
+    }
+    L = warp_sum(L);
+    const float inv = L != 0.f ? 1.f / L : 0.f;
+    for (int d = 4 * lane; d < hd; d += 128) {
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int c = c0; c <= c1; ++c) {
+        const int at = (c * 2 + (c == c0)) * p.qn + t;
+        const float w = ex2(p.part_ml[at].x - ref);
+        const float4 v = *reinterpret_cast<const float4*>(p.part_o + (int64_t)at * hd + d);
+        o = make_float4(fmaf(w, v.x, o.x), fmaf(w, v.y, o.y), fmaf(w, v.z, o.z), fmaf(w, v.w, o.w));
+      }
+      store_act4(out + d, 0, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+    }
+  }
+}
+
+size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+int check_query(const dmtp_paged_kv* c, const dmtp_paged_query* a) {
+  const int e = check_cache(c);
+  if (e) return e;
+  if (!a || a->rows < 1 || a->rows > DMTP_OPS_MAX_ROWS || a->n_heads < 1 || a->n_heads > 4096 ||
+      a->n_heads % c->n_kv_heads || a->window < 0 || c->n_seqs > 65535)
+    return DMTP_EINVAL;
+  return DMTP_OK;
+}
+
+int plan(const dmtp_paged_kv* c, const dmtp_paged_query* a, PagedPlan* pl) {
+  const int nq = a->rows * (a->n_heads / c->n_kv_heads), hd = c->head_dim;
+  pl->tc = false;
+  pl->qn = 8;
+  pl->tk = 64;
+  pl->grid = paged_simt_grid(hd, c->dtype, c->e4m3 != 0);
+  pl->chunks = (nq + pl->qn - 1) / pl->qn;
+  const int64_t reach = (int64_t)c->max_blocks * c->page_size;
+  const int64_t most = (reach + pl->tk - 1) / pl->tk * c->n_seqs * c->n_kv_heads * pl->chunks;
+  if (most >= (1ll << 31)) return DMTP_EINVAL;
+  const size_t parts = (size_t)pl->grid * 2 * pl->qn;
+  pl->part_o = 0;
+  pl->part_ml = up256(parts * hd * 4);
+  pl->prefix = pl->part_ml + up256(parts * 8);
+  pl->bytes = pl->prefix + up256(((size_t)c->n_seqs + 1) * 4);
+  return DMTP_OK;
+}
+
+}  // namespace
+
+extern "C" int dmtp_paged_attention_workspace(const dmtp_paged_kv* c, const dmtp_paged_query* a,
+                                              size_t* bytes) {
+  const int e = check_query(c, a);
+  if (e) return e;
+  if (!bytes) return DMTP_EINVAL;
+  PagedPlan pl;
+  const int r = plan(c, a, &pl);
+  if (r) return r;
+  *bytes = pl.bytes;
+  return DMTP_OK;
+}
+
+extern "C" int dmtp_paged_attention(const dmtp_paged_kv* c, const dmtp_paged_query* a, void* workspace,
+                                    size_t ws_bytes, uint32_t* err, void* stream) {
+  const int e = check_query(c, a);
+  if (e) return e;
+  const int es = c->dtype ? 2 : 4, hd = c->head_dim;
+  if (!a->q || !a->out || !a->kv_len || !workspace) return DMTP_EINVAL;
+  if (!aligned_to(a->q, 16) || !aligned_to(a->out, 16) || !aligned_to(a->kv_len, 4) ||
+      !aligned_to(workspace, 256) || (err && !aligned_to(err, 4)))
+    return DMTP_EINVAL;
+  const int64_t strides[6] = {a->q_seq, a->q_row, a->q_head, a->o_seq, a->o_row, a->o_head};
+  for (int64_t s : strides)
+    if (s < 0 || !mult(s * es, 16)) return DMTP_EINVAL;
+  if (a->o_head < hd || !(a->scale > -3.4e38f && a->scale < 3.4e38f)) return DMTP_EINVAL;
+  PagedPlan pl;
+  const int r = plan(c, a, &pl);
+  if (r) return r;
+  if (ws_bytes < pl.bytes) return DMTP_ENOMEM;
+  if (cudaPeekAtLastError() != cudaSuccess) return DMTP_ECUDA;
+  PagedAttn p;
+  p.m = page_map(*c);
+  p.k = c->k;
+  p.v = c->v;
+  p.ks = c->k_scale;
+  p.vs = c->v_scale;
+  p.a = *a;
+  p.err = err;
+  p.group = a->n_heads / c->n_kv_heads;
+  p.nq = a->rows * p.group;
+  p.qn = pl.qn;
+  p.chunks = pl.chunks;
+  p.units = c->n_kv_heads * pl.chunks;
+  p.part_o = (float*)((char*)workspace + pl.part_o);
+  p.part_ml = (float2*)((char*)workspace + pl.part_ml);
+  p.prefix = (int*)((char*)workspace + pl.prefix);
+  p.scale2 = a->scale * 1.4426950408889634f;
+  cudaStream_t st = (cudaStream_t)stream;
+  cudaError_t le = paged_attn_simt(p, pl, c->dtype, c->e4m3 != 0, st);
+  if (le == cudaSuccess) {
+    const dim3 grid(p.units, c->n_seqs, (pl.qn + 3) / 4);
+    le = c->dtype ? launch_op(k_paged_merge<bf16>, grid, 128, 0, st, true, 1, p, pl.grid)
+                  : launch_op(k_paged_merge<float>, grid, 128, 0, st, true, 1, p, pl.grid);
+  }
+  return le == cudaSuccess ? DMTP_OK : (cudaGetLastError(), DMTP_ECUDA);
+}

@@ -52,7 +52,7 @@ extern "C" {
  * head_dim values: k + p * page_stride is [n_kv_heads][page_size][head_dim] (elements),
  * likewise v. e4m3 = 0: values of `dtype`, k_scale and v_scale unused. e4m3 = 1: E4M3
  * values, and k_scale + p * scale_stride is [n_kv_heads][page_size] fp32 scales of the
- * rows (positive and finite; dmtp_paged_write makes powers of two), likewise v_scale.
+ * rows (positive normal numbers below 2^127; dmtp_paged_write makes powers of two), likewise v_scale.
  * Position j of sequence s lies in page table[s * table_stride + j / page_size], row
  * j % page_size; 0 <= j < max_blocks * page_size. Entries past a sequence's length are not
  * read. Several entries may name one page (a shared prefix).

@@ -19,7 +19,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libdmtp.so")
 
 SOURCES = ["dmtp.cu", "elementwise.cu", "attention.cu", "gemm_simt.cu", "gemm_tc.cu", "gdn.cu", "noalloc.cu", "attention_tc.cu", "head_tc.cu", "gate.cpp", "vocab.cpp",
-           "paged_kv.cu", "paged_attn.cu", "paged_attn_simt.cu", "norm_e4m3.cu", "sample.cu"]
+           "paged_kv.cu", "paged_attn.cu", "paged_attn_simt.cu", "paged_attn_tc.cu",
+           "norm_e4m3.cu", "sample.cu"]
 # host-only units whose double arithmetic must round the same on every host: no fused
 # multiply-adds (aarch64 compilers contract them by default)
 EXTRA = {"gate.cpp": ["-Xcompiler", "-ffp-contract=off"]}

@@ -68,13 +68,17 @@ int check_query(const dmtp_paged_kv* c, const dmtp_paged_query* a) {
 
 int plan(const dmtp_paged_kv* c, const dmtp_paged_query* a, PagedPlan* pl) {
   const int nq = a->rows * (a->n_heads / c->n_kv_heads), hd = c->head_dim;
-  pl->tc = false;
-  pl->qn = 8;
-  pl->tk = 64;
-  pl->grid = paged_simt_grid(hd, c->dtype, c->e4m3 != 0);
+  pl->tc = c->dtype == 1 && (hd == 64 || hd == 128);
+  if (pl->tc) {
+    pl->qn = nq <= 8 ? 8 : nq <= 16 ? 16 : nq <= 32 ? 32 : 64;
+    pl->grid = 2 * 152;  // two CTAs an SM
+  } else {
+    pl->qn = 8;
+    pl->grid = paged_simt_grid(hd, c->dtype, c->e4m3 != 0);
+  }
   pl->chunks = (nq + pl->qn - 1) / pl->qn;
   const int64_t reach = (int64_t)c->max_blocks * c->page_size;
-  const int64_t most = (reach + pl->tk - 1) / pl->tk * c->n_seqs * c->n_kv_heads * pl->chunks;
+  const int64_t most = (reach + 63) / 64 * c->n_seqs * c->n_kv_heads * pl->chunks;
   if (most >= (1ll << 31)) return DMTP_EINVAL;
   const size_t parts = (size_t)pl->grid * 2 * pl->qn;
   pl->part_o = 0;
@@ -134,7 +138,8 @@ extern "C" int dmtp_paged_attention(const dmtp_paged_kv* c, const dmtp_paged_que
   p.prefix = (int*)((char*)workspace + pl.prefix);
   p.scale2 = a->scale * 1.4426950408889634f;
   cudaStream_t st = (cudaStream_t)stream;
-  cudaError_t le = paged_attn_simt(p, pl, c->dtype, c->e4m3 != 0, st);
+  cudaError_t le = pl.tc ? paged_attn_tc(p, pl, c->e4m3 != 0, st)
+                         : paged_attn_simt(p, pl, c->dtype, c->e4m3 != 0, st);
   if (le == cudaSuccess) {
     const dim3 grid(p.units, c->n_seqs, (pl.qn + 3) / 4);
     le = c->dtype ? launch_op(k_paged_merge<bf16>, grid, 128, 0, st, true, 1, p, pl.grid)

@@ -130,13 +130,14 @@ __device__ __forceinline__ int queries_of(const PagedAttn& p, int unit) {
   return left < p.qn ? left : p.qn;
 }
 
-// attention over a cache of rows of either type on the CUDA cores (paged_attn_simt.cu), and
-// on the tensor cores (paged_attn_tc.cu). simt_grid/tc_grid: CTAs of the launch.
+// Which kernel takes a call: the tensor cores (paged_attn_tc.cu) or the CUDA cores
+// (paged_attn_simt.cu), both with tiles of 64 keys.
 struct PagedPlan {
   bool tc;
-  int qn, chunks, grid, tk;
+  int qn, chunks, grid;
   size_t part_o, part_ml, prefix, bytes;  // workspace offsets
 };
+cudaError_t paged_attn_tc(const PagedAttn& p, const PagedPlan& pl, bool e8, cudaStream_t st);
 cudaError_t paged_attn_simt(const PagedAttn& p, const PagedPlan& pl, int dtype, bool e8, cudaStream_t st);
 int paged_simt_grid(int head_dim, int dtype, bool e8);
 

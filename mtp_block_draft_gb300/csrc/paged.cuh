@@ -61,16 +61,25 @@ struct PageMap {
   const int32_t* table;
   int64_t page_stride, scale_stride, table_stride;
   int n_pages, page_size, n_kv_heads, head_dim, n_seqs, reach;  // reach: max_blocks page_size
+  uint32_t div_mul;
+  int div_shift;  // pos / page_size = pos div_mul >> div_shift
 };
 inline PageMap page_map(const dmtp_paged_kv& c) {
-  return PageMap{c.table,      c.page_stride, c.scale_stride, c.table_stride, c.n_pages,
-                 c.page_size,  c.n_kv_heads,  c.head_dim,     c.n_seqs,
-                 c.max_blocks * c.page_size};
+  // with 2^s >= page_size and m = ceil(2^(31 + s) / page_size), m page_size exceeds 2^(31 + s)
+  // by less than 2^s, so pos m >> (31 + s) is exact for pos < 2^31
+  int s = 0;
+  while ((1 << s) < c.page_size) ++s;
+  const uint64_t m = ((1ull << (31 + s)) + c.page_size - 1) / c.page_size;
+  return PageMap{c.table,      c.page_stride, c.scale_stride, c.table_stride,
+                 c.n_pages,    c.page_size,   c.n_kv_heads,   c.head_dim,
+                 c.n_seqs,     c.max_blocks * c.page_size,    (uint32_t)m, 31 + s};
 }
-// Page of position pos of sequence seq (pos already inside the table's reach), or -1 and
-// the page bit of the error word.
-__device__ __forceinline__ int page_of(const PageMap& m, int seq, int pos, unsigned* err) {
-  const int p = __ldg(m.table + (int64_t)seq * m.table_stride + (unsigned)pos / (unsigned)m.page_size);
+// Page and row in it (off) of position pos of sequence seq (pos already inside the table's
+// reach); -1 and the page bit of the error word for a page that is none.
+__device__ __forceinline__ int page_of(const PageMap& m, int seq, int pos, int& off, unsigned* err) {
+  const int q = (int)((unsigned long long)(unsigned)pos * m.div_mul >> m.div_shift);
+  off = pos - q * m.page_size;
+  const int p = __ldg(m.table + (int64_t)seq * m.table_stride + q);
   if ((unsigned)p < (unsigned)m.n_pages) return p;
   set_err(err, DMTP_OPS_ERR_PAGE);
   return -1;

@@ -6,18 +6,21 @@ using namespace dmtp;
 
 namespace {
 
-// The merge of one unit's pieces (paged_attn.cuh), one warp per query: with M the largest of
-// the pieces' maxima, out = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c, pieces in CTA
-// order. Units that one CTA wrote are left alone; units without a tile get zeros. Reads the
-// partial rows once: G x 2 x qn x (head_dim + 2) floats at most.
+// The merge of one unit's pieces (paged_attn.cuh), one CTA per query: with M the largest of
+// the pieces' maxima, out = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c. Warp w takes every
+// fourth piece, and the four sums are added in order. Units that one CTA wrote are left alone;
+// units without a tile get zeros. It is all latency (a few hundred KB from L2), so the pieces'
+// rows are asked for eight at a time.
 template <typename T>
 __global__ void __launch_bounds__(128) k_paged_merge(const PagedAttn p, int ctas) {
+  __shared__ __align__(16) float part[3][DMTP_OPS_MAX_HEAD_DIM];
   pdl_wait();
-  const int b = blockIdx.y, unit = blockIdx.x, hd = p.m.head_dim;
+  const int b = blockIdx.y, unit = blockIdx.x, t = blockIdx.z, hd = p.m.head_dim;
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  if (t >= queries_of(p, unit)) return;
   const long long total = p.prefix[p.m.n_seqs];
-  const int G = busy_ctas(total, ctas);
   const int lo = p.prefix[b], n = (p.prefix[b + 1] - lo) / p.units;
+  const int G = busy_ctas(total, ctas);
   const long long s0 = lo + (long long)unit * n;
   int c0 = 0, c1 = -1;
   if (n > 0) {
@@ -25,30 +28,38 @@ __global__ void __launch_bounds__(128) k_paged_merge(const PagedAttn p, int ctas
     c1 = (int)(((s0 + n) * G - 1) / total);
     if (c0 == c1) return;
   }
-  const int nq = queries_of(p, unit);
-  for (int t = blockIdx.z * 4 + wid; t < nq; t += gridDim.z * 4) {
-    int head, row;
-    query_of(p, unit, t, &head, &row);
-    T* out = (T*)p.a.out + (int64_t)b * p.a.o_seq + (int64_t)row * p.a.o_row + (int64_t)head * p.a.o_head;
-    float M = -INFINITY, L = 0.f;
-    for (int c = c0 + lane; c <= c1; c += 32)
-      M = fmaxf(M, p.part_ml[(c * 2 + (c == c0)) * p.qn + t].x);
-    M = warp_max(M);
-    const float ref = M == -INFINITY ? 0.f : M;
-    for (int c = c0 + lane; c <= c1; c += 32) {
-      const float2 ml = p.part_ml[(c * 2 + (c == c0)) * p.qn + t];
-      L += ml.y * ex2(ml.x - ref);
-    }
-    L = warp_sum(L);
-    const float inv = L != 0.f ? 1.f / L : 0.f;
-    for (int d = 4 * lane; d < hd; d += 128) {
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-      for (int c = c0; c <= c1; ++c) {
+  float M = -INFINITY, L = 0.f;
+  for (int c = c0 + lane; c <= c1; c += 32)
+    M = fmaxf(M, p.part_ml[(c * 2 + (c == c0)) * p.qn + t].x);
+  M = warp_max(M);
+  const float ref = M == -INFINITY ? 0.f : M;
+  for (int c = c0 + lane; c <= c1; c += 32) {
+    const float2 ml = p.part_ml[(c * 2 + (c == c0)) * p.qn + t];
+    L += ml.y * ex2(ml.x - ref);
+  }
+  L = warp_sum(L);
+  const float inv = L != 0.f ? 1.f / L : 0.f;
+  int head, row;
+  query_of(p, unit, t, &head, &row);
+  T* out = (T*)p.a.out + (int64_t)b * p.a.o_seq + (int64_t)row * p.a.o_row + (int64_t)head * p.a.o_head;
+  for (int d = 4 * lane; d < (hd + 127) / 128 * 128; d += 128) {
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (d < hd) {
+#pragma unroll 8
+      for (int c = c0 + wid; c <= c1; c += 4) {
         const int at = (c * 2 + (c == c0)) * p.qn + t;
         const float w = ex2(p.part_ml[at].x - ref);
         const float4 v = *reinterpret_cast<const float4*>(p.part_o + (int64_t)at * hd + d);
         o = make_float4(fmaf(w, v.x, o.x), fmaf(w, v.y, o.y), fmaf(w, v.z, o.z), fmaf(w, v.w, o.w));
+      }
+      if (wid) *reinterpret_cast<float4*>(&part[wid - 1][d]) = o;
+    }
+    __syncthreads();
+    if (wid == 0 && d < hd) {
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        const float4 v = *reinterpret_cast<const float4*>(&part[i][d]);
+        o = make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w);
       }
       store_act4(out + d, 0, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
     }
@@ -71,7 +82,7 @@ int plan(const dmtp_paged_kv* c, const dmtp_paged_query* a, PagedPlan* pl) {
   pl->tc = c->dtype == 1 && (hd == 64 || hd == 128);
   if (pl->tc) {
     pl->qn = nq <= 8 ? 8 : nq <= 16 ? 16 : nq <= 32 ? 32 : 64;
-    pl->grid = 2 * 152;  // two CTAs an SM
+    pl->grid = paged_tc_grid(hd, c->e4m3 != 0, pl->qn);
   } else {
     pl->qn = 8;
     pl->grid = paged_simt_grid(hd, c->dtype, c->e4m3 != 0);
@@ -141,7 +152,7 @@ extern "C" int dmtp_paged_attention(const dmtp_paged_kv* c, const dmtp_paged_que
   cudaError_t le = pl.tc ? paged_attn_tc(p, pl, c->e4m3 != 0, st)
                          : paged_attn_simt(p, pl, c->dtype, c->e4m3 != 0, st);
   if (le == cudaSuccess) {
-    const dim3 grid(p.units, c->n_seqs, (pl.qn + 3) / 4);
+    const dim3 grid(p.units, c->n_seqs, p.nq < pl.qn ? p.nq : pl.qn);
     le = c->dtype ? launch_op(k_paged_merge<bf16>, grid, 128, 0, st, true, 1, p, pl.grid)
                   : launch_op(k_paged_merge<float>, grid, 128, 0, st, true, 1, p, pl.grid);
   }

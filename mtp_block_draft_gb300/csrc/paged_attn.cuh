@@ -1,7 +1,7 @@
 // Attention over a paged cache: what its kernels share - the arguments, how the key tiles
 // of all sequences are dealt out to the CTAs, and the partial results.
 //
-// Work. Sequence b's visible positions [first_b, len_b) are n_b tiles of TK keys. A unit is
+// Work. Sequence b's positions [first_b, len_b) that a row can see (first_b rounded down) are n_b tiles of TK keys. A unit is
 // one (sequence, kv head, chunk of at most QN queries); a sequence has U = n_kv_heads x
 // chunks of them. All units' tiles laid end to end (T in all) are dealt to the G CTAs in
 // equal contiguous ranges (G at most T), CTA c taking tiles [c T / G, (c + 1) T / G): every CTA streams
@@ -34,11 +34,11 @@ __device__ __forceinline__ int seq_len(const PagedAttn& p, int b) {
   const int n = __ldg(p.a.kv_len + b);
   return n < 0 ? 0 : n > p.m.reach ? p.m.reach : n;
 }
-// First position that any row sees.
+// First position of sequence b's tiles: that any row sees, down to a whole 64.
 __device__ __forceinline__ int seq_first(const PagedAttn& p, int len) {
   if (p.a.window <= 0) return 0;
   const int f = len - p.a.rows + 1 - p.a.window;
-  return f > 0 ? f : 0;
+  return f > 0 ? f & ~63 : 0;
 }
 template <int TK>
 __device__ __forceinline__ int seq_tiles(const PagedAttn& p, int len) {
@@ -131,7 +131,7 @@ __device__ __forceinline__ int queries_of(const PagedAttn& p, int unit) {
 }
 
 // Which kernel takes a call: the tensor cores (paged_attn_tc.cu) or the CUDA cores
-// (paged_attn_simt.cu), both with tiles of 64 keys.
+// (paged_attn_simt.cu), with tiles of 64 or 128 keys.
 struct PagedPlan {
   bool tc;
   int qn, chunks, grid;
@@ -139,6 +139,7 @@ struct PagedPlan {
 };
 cudaError_t paged_attn_tc(const PagedAttn& p, const PagedPlan& pl, bool e8, cudaStream_t st);
 cudaError_t paged_attn_simt(const PagedAttn& p, const PagedPlan& pl, int dtype, bool e8, cudaStream_t st);
+int paged_tc_grid(int head_dim, bool e8, int qn);
 int paged_simt_grid(int head_dim, int dtype, bool e8);
 
 }  // namespace dmtp

@@ -149,8 +149,9 @@ __global__ void __launch_bounds__(kThreads) k_paged_attn_simt(const PagedAttn p)
         const int j = j0 + tid;
         int64_t at = -1, line = 0;
         if (j < len) {
-          const int page = page_of(p.m, w.b, j, p.err);
-          line = (int64_t)kvh * p.m.page_size + j % p.m.page_size;
+          int off;
+          const int page = page_of(p.m, w.b, j, off, p.err);
+          line = (int64_t)kvh * p.m.page_size + off;
           if (page >= 0) {
             at = (int64_t)page * p.m.page_stride + line * hd;
             line += (int64_t)page * p.m.scale_stride;

@@ -2,27 +2,25 @@
 // cache in bf16 or E4M3.
 //
 // One pass over the cached rows bounds it: each byte of K and V feeds at most 64 queries of
-// its kv head (rows x query heads), a few hundred operations. So the CTA (four warps, two
-// CTAs an SM) keeps a ring of 64-key tiles in flight by 16-byte asynchronous copies, one
-// page lookup per row (made a tile ahead, so no copy waits for the table), and the warps
-// work on the 16-bit fragments with m16n8k16 products, which need no staging beyond the tile
-// itself and no rows padded to 128 (the tcgen05 form wants M >= 64 of its 128 lanes, mostly
-// empty at 1 to 16 queries, and the E4M3 rows would have to be converted through shared
-// memory).
+// its kv head (rows x query heads), a few hundred operations. So the warps keep rings of
+// 16-key blocks in flight by 16-byte asynchronous copies (the page of a block looked up a
+// tile ahead, so no copy waits for the table) and work on 16-bit fragments with m16n8k16
+// products that need no staging beyond the block itself. Keys are the M side and queries the N
+// side of both products (S^T = K Q^T, O^T = V^T P^T), so 8 queries fill an instruction. (The
+// tcgen05 form wants 128 rows of keys and one thread to start each product of the whole CTA;
+// a block would wait for its neighbours, and E4M3 rows would go through shared memory twice.)
 //
-//   QN queries  warps         a warp's share of a tile
-//   8, 16       4 key groups  16 keys x 16 queries
-//   32          4 key groups  16 keys x 32 queries
-//   64          2 x 2         32 keys x 32 queries
+//   QN queries    teams             a team's ring
+//   8, 16, 32     4 of one warp     16 keys a stage, no barrier but the warp's own
+//   64            2 of two warps    each warp 32 queries, 32 keys a stage
 //
-// Scores S = Q K^T (fp32 accumulators), weights 2^(S - m) with a running maximum m per row
-// that moves only when a score passes it by 2^8 (so most tiles skip the rescaling), and
-// O += P V with P as the A operand straight from the registers of S. bf16 caches: P as a
-// bf16 pair (16 bits of each weight), two products a fragment. E4M3 caches: rows become fp16
-// exactly, the queries too after a power-of-two scale per row, and P carries the value
-// row's scale: with v = 2^e c and weight w, m follows log2(w 2^e) and P = w 2^(e - m), so
-// what is rounded to fp16 is the row's contribution relative to the largest one; the sum of
-// weights undoes the exponent in fp32.
+// Weights 2^(s - m) use a running maximum m per query that moves only when a score passes it
+// by 2^8 (so most blocks skip the rescaling). bf16 caches: P as a bf16 pair (16 bits of each
+// weight), two products a fragment. E4M3 caches: rows become fp16 exactly, the queries too
+// after a power-of-two scale per query, and P carries the value row's scale: with v = 2^e c
+// and weight w, m follows log2(w 2^e) and P = w 2^(e - m), so what is rounded to fp16 is the
+// row's contribution relative to the largest one; the sum of weights undoes the exponent in
+// fp32.
 #include <cuda_fp16.h>
 
 #include "paged_attn.cuh"
@@ -31,24 +29,29 @@ using namespace dmtp;
 
 namespace {
 
-constexpr int kTK = 64, kThreads = 128;
+constexpr int kThreads = 128;
 
 template <int HD, bool E8, int QN>
 struct Shape {
-  static constexpr int MW = QN <= 16 ? 1 : 2;     // 16-query tiles of a warp
-  static constexpr int QG = QN == 64 ? 2 : 1;     // query groups of warps
-  static constexpr int KS = 4 / QG;               // key groups of warps
-  static constexpr int QR = 16 * MW * QG;         // query rows of the CTA's tiles
-  static constexpr int RB = HD * (E8 ? 1 : 2);    // bytes of a cached row
-  static constexpr int kStage = 2 * kTK * RB + (E8 ? 2 * kTK * 4 : 0);
-  static constexpr int kPitch = HD + (E8 ? 16 : 8);  // floats of a joined row: no conflicts
-  // joined rows; the queries of MW = 2 lie there while the tiles run (QR * HD * 2 bytes)
-  static constexpr int kJoin = QR * kPitch * 4 + KS * QR * 8;
-  static constexpr int kMisc = 8 * 4 * 4 + 64;    // valid rows of each stage, the walk
-  static constexpr int kRoom = 113 * 1024 - kJoin - kMisc;  // two CTAs an SM
-  static constexpr int NST = kRoom / kStage > 8 ? 8 : kRoom / kStage;
-  static constexpr int kSmem = NST * kStage + kJoin + kMisc;
-  static_assert(NST >= 2, "a ring of two tiles at least");
+  static constexpr int NT = QN >= 32 ? 4 : QN / 8;  // 8-query blocks of a warp
+  static constexpr int QG = QN == 64 ? 2 : 1;       // warps of a team
+  static constexpr int KS = 4 / QG;                 // teams
+  static constexpr int RB = HD * (E8 ? 1 : 2);      // bytes of a cached row
+  static constexpr int TK = 64;                     // keys of a tile
+  static constexpr int NSUB = TK / 16 / KS;         // 16-key blocks of a team in a tile
+  static constexpr int kBlock = 2 * 16 * RB + (E8 ? 128 : 0);
+  static constexpr int kStage = NSUB * kBlock;      // of a team
+  static constexpr int kPitch = HD + 4;             // floats of a joined row: no conflicts
+  static constexpr int kJoin = QN * kPitch * 4 + KS * QN * 8;
+  static constexpr bool QS = NT == 4;               // query fragments in shared memory (the
+                                                    // joined rows' place, until the join)
+  static constexpr int kMisc = KS * 8 * NSUB * 4 + 64;  // valid rows of the blocks, the walk
+  // CTAs of an SM: registers (128 threads x 128, 168 or 255) and a ring of two stages at least
+  static constexpr int CTAS = QN == 8 ? (RB == 256 ? 3 : 4) : QN == 16 ? (HD == 64 ? 4 : 3) : 2;
+  static constexpr int kRoom = 228 * 1024 / CTAS - 1024 - kJoin - kMisc;
+  static constexpr int NST = kRoom / (KS * kStage) > 8 ? 8 : kRoom / (KS * kStage);
+  static constexpr int kSmem = NST * KS * kStage + kJoin + kMisc;
+  static_assert(NST >= 2, "a ring of two stages at least");
 };
 
 // Byte of 16-byte step c of row r in a tile: the steps of eight consecutive rows that
@@ -94,12 +97,13 @@ __device__ __forceinline__ uint32_t finite_pair(uint32_t u) {
 }
 
 // The tiles of a CTA's range in order.
+template <int TK>
 struct Tiles {
   int pos, end, b, unit, t, n, len, first;
   __device__ __forceinline__ void seq(const PagedAttn& p) {
     len = seq_len(p, b);
     first = seq_first(p, len);
-    n = (len - first + kTK - 1) / kTK;
+    n = (len - first + TK - 1) / TK;
   }
   __device__ __forceinline__ void start(const PagedAttn& p, const Walk& w) {
     pos = w.pos;
@@ -128,61 +132,327 @@ struct Tiles {
   }
 };
 
+__device__ __forceinline__ uint32_t transpose8(uint32_t u) {  // an 8 x 8 block of 16-bit values
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(u));
+  return r;
+}
+// Four E4M3 bytes as two pairs of halves.
+__device__ __forceinline__ void e4m3_pairs(uint32_t u, uint32_t& lo, uint32_t& hi) {
+  asm("{.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;}"
+      : "=r"(lo), "=r"(hi) : "r"(u));
+}
+template <int QG>
+__device__ __forceinline__ void team_sync(int team) {
+  if (QG == 1)
+    __syncwarp();
+  else
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(32 * QG) : "memory");
+}
+
+// What a warp keeps of a piece: per 8-query block, queries 2 tq and 2 tq + 1.
+template <int HD, int NT>
+struct State {
+  float o[NT][HD / 16][4];  // O^T: [16 columns of the head] x [8 queries]
+  float m[NT][2], l[NT][2], rowf[NT][2];
+  int top[NT][2];           // last position that the query sees
+};
+
+// One 16-key block: jb its first position, `ok` its rows that hold a position of the sequence.
+// EDGE: some row is not seen by every query.
+template <int HD, bool E8, int NT, bool EDGE>
+__device__ __forceinline__ void block(const PagedAttn& p, State<HD, NT>& z,
+                                      const uint32_t (&qf)[NT == 4 ? 1 : NT][HD / 16][2], const uint4* sq,
+                                      const unsigned char* blk, int jb, unsigned ok) {
+  constexpr int RB = HD * (E8 ? 1 : 2), KK = HD / 16;
+  const int lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3, mi = lane >> 3;
+  const uint32_t sK = smem_u32(blk), sV = sK + 16 * RB;
+  const float* sS = (const float*)(blk + 32 * RB);
+  float s[NT][4];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+  {  // A fragments of K: rows (keys) 0-7 and 8-15 of two 16-byte steps. A row's steps are
+     // permuted by exclusive or, so step k2 is the first one's address with k2's bits flipped.
+    const uint32_t a0 = sK + tile_at<RB>((lane & 7) + 8 * (mi & 1), mi >> 1);
+#pragma unroll
+    for (int k2 = 0; k2 < KK; k2 += 2) {
+      uint32_t a[2][4];
+      if (E8) {  // a step holds the 16 columns of one product
+        uint32_t kr[4];
+        ldsm4(kr, a0 ^ (k2 << 4));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          e4m3_pairs(kr[2 * i], a[i][0], a[i][2]);
+          e4m3_pairs(kr[2 * i + 1], a[i][1], a[i][3]);
+        }
+      } else {
+        ldsm4(a[0], a0 ^ (2 * k2 << 4));
+        ldsm4(a[1], a0 ^ (2 * k2 + 2 << 4));
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        uint32_t q[4];
+        if (NT == 4) {
+          const uint4 u = sq[(n * KK + k2) * 16];
+          q[0] = u.x, q[1] = u.y, q[2] = u.z, q[3] = u.w;
+        } else {
+          q[0] = qf[NT == 4 ? 0 : n][k2][0], q[1] = qf[NT == 4 ? 0 : n][k2][1];
+          q[2] = qf[NT == 4 ? 0 : n][k2 + 1][0], q[3] = qf[NT == 4 ? 0 : n][k2 + 1][1];
+        }
+        mma16816<E8>(s[n], a[0], q[0], q[1]);
+        mma16816<E8>(s[n], a[1], q[2], q[3]);
+      }
+    }
+  }
+  // the thread's keys g and g + 8
+  float kf[2], ve[2], vm[2], vi[2];
+  if (E8) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      kf[h] = sS[g + 8 * h];
+      const uint32_t u = __float_as_uint(sS[16 + g + 8 * h]);  // 2^(u >> 23 - 127) times [1, 2)
+      ve[h] = __uint_as_float(0x4b000000u | u >> 23) - 8388735.f;
+      vm[h] = __uint_as_float(0x3f800000u | (u & 0x7fffffu));
+      vi[h] = pow2f(127 - (int)(u >> 23));
+    }
+  }
+  uint32_t pk[NT][2], pb[NT][2], lb[NT][2];
+  bool rise = false;
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int y = 0; y < 2; ++y)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float v = s[n][2 * h + y] * z.rowf[n][y];
+        if (E8) v = fmaf(v, kf[h], ve[h]);
+        if (EDGE) {
+          const int key = g + 8 * h, j = jb + key;
+          const bool seen = (ok >> key & 1) && j <= z.top[n][y] &&
+                            (p.a.window <= 0 || j > z.top[n][y] - p.a.window);
+          v = seen ? v : -INFINITY;
+        }
+        s[n][2 * h + y] = v;
+        rise = rise || v > z.m[n][y] + 8.f;
+      }
+  if (__any_sync(0xffffffffu, rise)) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        float mx = fmaxf(s[n][y], s[n][2 + y]);
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+        if (mx > z.m[n][y] + 8.f) {
+          const float fix = ex2(z.m[n][y] - mx);  // 0 for the first
+          z.m[n][y] = mx;
+          z.l[n][y] *= fix;
+#pragma unroll
+          for (int i = 0; i < KK; ++i) {
+            z.o[n][i][y] *= fix;
+            z.o[n][i][2 + y] *= fix;
+          }
+        }
+      }
+  }
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const float r0 = z.m[n][0] == -INFINITY ? 0.f : z.m[n][0], r1 = z.m[n][1] == -INFINITY ? 0.f : z.m[n][1];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float w0 = ex2(s[n][2 * h] - r0), w1 = ex2(s[n][2 * h + 1] - r1);
+      if (E8) {
+        z.l[n][0] = fmaf(w0, vi[h], z.l[n][0]);
+        z.l[n][1] = fmaf(w1, vi[h], z.l[n][1]);
+        pk[n][h] = pack_f16(w0 * vm[h], w1 * vm[h]);
+      } else {
+        z.l[n][0] += w0;
+        z.l[n][1] += w1;
+        pk[n][h] = pack_bf16(w0, w1);
+        lb[n][h] = transpose8(pack_bf16(w0 - __uint_as_float(pk[n][h] << 16),
+                                        w1 - __uint_as_float(pk[n][h] & 0xffff0000u)));
+      }
+      pb[n][h] = transpose8(pk[n][h]);
+    }
+  }
+  // O^T += V^T P^T: A fragments of V^T, columns of the head as rows
+  bool odd = false;  // an infinity or NaN among values that not every query sees
+  {
+    if (E8) {
+      const uint32_t v0 = sV + tile_at<RB>((lane & 7) + 8 * (mi & 1), mi >> 1);
+#pragma unroll
+      for (int c = 0; c < KK; c += 2) {
+        uint32_t v[4];  // step c: keys 0-7, 8-15; step c + 1 likewise
+        ldsm4_t(v, v0 ^ (c << 4));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          // bytes of keys 2 tq, 2 tq + 1 by column: rows g hold columns 2 g, rows g + 8 2 g + 1
+          uint32_t a[4];
+          e4m3_pairs(__byte_perm(v[2 * i], 0, 0x3120), a[0], a[1]);
+          e4m3_pairs(__byte_perm(v[2 * i + 1], 0, 0x3120), a[2], a[3]);
+          if (EDGE) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const uint32_t f = finite_pair<true>(a[x]);
+              odd = odd || f != a[x];
+              a[x] = f;
+            }
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma16816<true>(z.o[n][c + i], a, pb[n][0], pb[n][1]);
+        }
+      }
+    } else {
+      const uint32_t v0 = sV + tile_at<RB>((lane & 7) + 8 * (mi >> 1), mi & 1);
+#pragma unroll
+      for (int i = 0; i < KK; ++i) {
+        uint32_t a[4];  // keys 0-7: columns 0-7, 8-15 of the block; keys 8-15 likewise
+        ldsm4_t(a, v0 ^ (2 * i << 4));
+        if (EDGE) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const uint32_t f = finite_pair<false>(a[x]);
+            odd = odd || f != a[x];
+            a[x] = f;
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          mma16816<false>(z.o[n][i], a, pb[n][0], pb[n][1]);
+          mma16816<false>(z.o[n][i], a, lb[n][0], lb[n][1]);
+        }
+      }
+    }
+  }
+  if (EDGE && __any_sync(0xffffffffu, odd)) {
+    // give those values to the queries that do see them: weights by shuffle from the lane
+    // that holds them, values from shared memory
+    const unsigned char* vrow = blk + 16 * RB;
+#pragma unroll 1
+    for (int key = 0; key < 16; ++key) {
+      const int from = (key & 7) * 4 + tq;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const uint32_t lo = __shfl_sync(0xffffffffu, pk[n][0], from), hi = __shfl_sync(0xffffffffu, pk[n][1], from);
+        const uint32_t u = key < 8 ? lo : hi;
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const uint32_t bits = y ? u >> 16 : u & 0xffffu;
+          const float w = E8 ? h2_to_f2(bits).x : __uint_as_float(bits << 16);
+          if (w != 0.f) {
+#pragma unroll
+            for (int i = 0; i < KK; ++i)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int d = E8 ? 16 * i + 2 * g + h : 16 * i + g + 8 * h;
+                const int byte = d * (E8 ? 1 : 2);
+                const unsigned char* at = vrow + tile_at<RB>(key, byte >> 4) + (byte & 15);
+                const float val = E8 ? h2_to_f2(e4m3x2_to_h2(*at)).x : __bfloat162float(*(const bf16*)at);
+                if (!(fabsf(val) <= 3.402823466e38f)) z.o[n][i][2 * h + y] = fmaf(w, val, z.o[n][i][2 * h + y]);
+              }
+          }
+        }
+      }
+    }
+  }
+}
+
 template <int HD, bool E8, int QN>
-__global__ void __launch_bounds__(kThreads, 2) k_paged_attn_tc(const PagedAttn p) {
+__global__ void __launch_bounds__(kThreads, Shape<HD, E8, QN>::CTAS) k_paged_attn_tc(const PagedAttn p) {
   using S = Shape<HD, E8, QN>;
-  constexpr int MW = S::MW, QG = S::QG, KS = S::KS, QR = S::QR, RB = S::RB, NST = S::NST;
-  constexpr int KK = HD / 16;             // products along the head
-  constexpr bool kHalf = QN <= 8;         // rows 8..15 of the tile hold no query
+  constexpr int NT = S::NT, QG = S::QG, KS = S::KS, RB = S::RB, NST = S::NST, TK = S::TK, NSUB = S::NSUB;
+  constexpr int KK = HD / 16;
   extern __shared__ __align__(128) unsigned char smem[];
-  float* sO = (float*)(smem + NST * S::kStage);
-  float2* sML = (float2*)(sO + QR * S::kPitch);
+  float* sO = (float*)(smem + NST * KS * S::kStage);
+  float2* sML = (float2*)(sO + QN * S::kPitch);
   uint4* sQ = (uint4*)sO;
-  uint32_t* sOk = (uint32_t*)(sML + KS * QR);
-  int* sWalk = (int*)(sOk + 8 * 4);
+  uint32_t* sOk = (uint32_t*)(sML + KS * QN);
+  int* sWalk = (int*)(sOk + KS * 8 * NSUB);
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, g = lane >> 2, tq = lane & 3;
-  const int qg = wid % QG, ks = wid / QG;
+  const int team = wid / QG, qg = wid % QG;
+  unsigned char* ring = smem + team * NST * S::kStage;
+  sOk += team * 8 * NSUB;
   pdl_trigger();
-  const Walk w = deal<kTK, kThreads>(p, sWalk);
+  const Walk w = deal<TK, kThreads>(p, sWalk);
   if (w.pos >= w.end) return;
-  Tiles cons, prod;
+  Tiles<TK> cons, prod;
   cons.start(p, w);
   prod = cons;
 
-  // ---- copies: warp w brings rows 16 w .. 16 w + 15 of every tile ----
-  constexpr int CPR = RB / 16, RPI = 32 / CPR, NI = 16 / RPI;
-  int row_page = -1;  // page of this lane's row (lanes 0..15) of the next tile to bring
+  // ---- copies: a team brings the blocks team + KS i of every tile ----
+  constexpr int CPR = RB / 16, RPI = 32 * QG / CPR, NI = 16 / RPI;  // rows of one copy of the team
+  const bool paged16 = p.m.page_size % 16 == 0;  // a block lies in one page
+  int page[NSUB], off[NSUB];  // of the blocks of the next tile to bring: page, first row in it
   auto look_up = [&]() {
-    const int j = prod.first + prod.t * kTK + wid * 16 + lane;
-    row_page = -1;
-    if (prod.pos < prod.end && lane < 16 && j < prod.len) row_page = page_of(p.m, prod.b, j, p.err);
+#pragma unroll
+    for (int i = 0; i < NSUB; ++i) {
+      const int j = prod.first + prod.t * TK + (team + KS * i) * 16;
+      page[i] = -1;
+      if (paged16 && prod.pos < prod.end && j < prod.len) page[i] = page_of(p.m, prod.b, j, off[i], p.err);
+    }
   };
   int stage_in = 0;
   auto produce = [&]() {
     if (prod.pos < prod.end) {
-      unsigned char* st = smem + stage_in * S::kStage;
       const int kvh = prod.unit / p.chunks;
-      const int j = prod.first + prod.t * kTK + wid * 16 + lane;
-      const int line = kvh * p.m.page_size + (unsigned)j % (unsigned)p.m.page_size;
-      const int64_t at = row_page < 0 ? -1 : (int64_t)row_page * p.m.page_stride + (int64_t)line * HD;
-      const unsigned ok = __ballot_sync(0xffffffffu, row_page >= 0) & 0xffffu;
-      if (lane == 0) sOk[stage_in * 4 + wid] = ok;
-      if (E8 && lane < 16) {
-        const int64_t sat = row_page < 0 ? 0 : (int64_t)row_page * p.m.scale_stride + line;
-        const uint32_t d = smem_u32(st + 2 * kTK * RB) + (wid * 16 + lane) * 4;
-        cp_async4(d, p.ks + sat, row_page < 0 ? 0 : 4);
-        cp_async4(d + kTK * 4, p.vs + sat, row_page < 0 ? 0 : 4);
-      }
-      const uint32_t dst = smem_u32(st);
-      const int rin = lane / CPR, c = lane % CPR;
+      const int tl = qg * 32 + lane, rin = tl / CPR, c = tl % CPR;
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const int r = i * RPI + rin;
-        const int64_t a = __shfl_sync(0xffffffffu, at, r);
-        const int64_t src = a < 0 ? 0 : a * (E8 ? 1 : 2) + c * 16;
-        const uint32_t d = dst + tile_at<RB>(wid * 16 + r, c);
-        cp_async16(d, (const char*)p.k + src, a < 0 ? 0 : 16);
-        cp_async16(d + kTK * RB, (const char*)p.v + src, a < 0 ? 0 : 16);
+      for (int i = 0; i < NSUB; ++i) {
+        unsigned char* blk = ring + stage_in * S::kStage + i * S::kBlock;
+        const uint32_t dst = smem_u32(blk);
+        const int jb = prod.first + prod.t * TK + (team + KS * i) * 16;
+        int rows = min(16, prod.len - jb);
+        unsigned ok;
+        if (paged16) {
+          if (page[i] < 0) rows = 0;
+          ok = rows >= 16 ? 0xffffu : rows > 0 ? (1u << rows) - 1 : 0u;
+          const int64_t line = (int64_t)kvh * p.m.page_size + (rows > 0 ? off[i] : 0);
+          const int64_t pg = rows > 0 ? page[i] : 0;
+          const int64_t at = (pg * p.m.page_stride + line * HD) * (E8 ? 1 : 2) + tl * 16;
+          const char *ka = (const char*)p.k + at, *va = (const char*)p.v + at;
+#pragma unroll
+          for (int x = 0; x < NI; ++x) {
+            const int r = x * RPI + rin, bytes = r < rows ? 16 : 0;
+            const uint32_t d = dst + tile_at<RB>(r, c);
+            // (a row that is not there is not read: its address is that of one that is)
+            cp_async16(d, bytes ? ka + x * (512 * QG) : (const char*)p.k, bytes);
+            cp_async16(d + 16 * RB, bytes ? va + x * (512 * QG) : (const char*)p.v, bytes);
+          }
+          if (E8 && qg == 0) {
+            const int64_t sat = pg * p.m.scale_stride + line + (lane & 15);
+            const float* src = (lane < 16 ? p.ks : p.vs);
+            const bool there = (lane & 15) < rows;
+            cp_async4(dst + 32 * RB + lane * 4, there ? src + sat : src, there ? 4 : 0);
+          }
+        } else {
+          const int j = jb + (lane & 15);
+          int64_t at = -1;
+          int64_t sat = 0;
+          if (j < prod.len) {
+            int o;
+            const int pg = page_of(p.m, prod.b, j, o, p.err);
+            const int64_t line = (int64_t)kvh * p.m.page_size + o;
+            if (pg >= 0) {
+              at = ((int64_t)pg * p.m.page_stride + line * HD) * (E8 ? 1 : 2);
+              sat = (int64_t)pg * p.m.scale_stride + line;
+            }
+          }
+          ok = __ballot_sync(0xffffffffu, at >= 0) & 0xffffu;
+#pragma unroll
+          for (int x = 0; x < NI; ++x) {
+            const int r = x * RPI + rin;
+            const int64_t a = __shfl_sync(0xffffffffu, at, r);
+            const int bytes = a < 0 ? 0 : 16;
+            const int64_t src = a < 0 ? 0 : a + c * 16;
+            const uint32_t d = dst + tile_at<RB>(r, c);
+            cp_async16(d, (const char*)p.k + src, bytes);
+            cp_async16(d + 16 * RB, (const char*)p.v + src, bytes);
+          }
+          if (E8 && qg == 0)
+            cp_async4(dst + 32 * RB + lane * 4, (lane < 16 ? p.ks : p.vs) + sat, at < 0 ? 0 : 4);
+        }
+        if (lane == 0 && qg == 0) sOk[stage_in * NSUB + i] = ok;
       }
       prod.skip(p, 1);
       look_up();
@@ -198,366 +468,147 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attn_tc(const PagedAttn p
     // ---- one piece: tiles t0..t1 of a unit ----
     const int t0 = cons.t, t1 = min(cons.n, t0 + cons.end - cons.pos);
     const int nq = queries_of(p, cons.unit);
-    uint32_t qf[MW == 1 ? KK : 1][4];
-    float rowf[MW][2], m[MW][2], l[MW][2], o[MW][HD / 8][4];
-    int top[MW][2];
+    State<HD, NT> z;
+    uint32_t qf[S::QS ? 1 : NT][KK][2];
 #pragma unroll
-    for (int mw = 0; mw < MW; ++mw) {
-      const bf16* qp[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int t = (qg * MW + mw) * 16 + g + 8 * h;
-        m[mw][h] = -INFINITY;
-        l[mw][h] = 0.f;
-        rowf[mw][h] = p.scale2;
-        top[mw][h] = -1;
-        qp[h] = nullptr;
-        if (t < nq) {
-          int head, row;
-          query_of(p, cons.unit, t, &head, &row);
-          top[mw][h] = cons.len - p.a.rows + row;
-          qp[h] = (const bf16*)p.a.q + (int64_t)cons.b * p.a.q_seq + (int64_t)row * p.a.q_row + (int64_t)head * p.a.q_head;
-        }
+    for (int n = 0; n < NT; ++n) {
+      uint32_t f[KK][2];
+      const int q0 = (qg * NT + n) * 8;
+      const bf16* qp = nullptr;
+      int head, row;
+      if (q0 + g < nq) {
+        query_of(p, cons.unit, q0 + g, &head, &row);
+        qp = (const bf16*)p.a.q + (int64_t)cons.b * p.a.q_seq + (int64_t)row * p.a.q_row + (int64_t)head * p.a.q_head;
       }
-      // A fragments: bf16 rows in the products' own order; for an E4M3 cache a thread holds
-      // four consecutive columns, as the bytes of K come
-      uint32_t f[KK][4];
+      // B fragments of Q^T: query g, columns 2 tq.. in the products' order, or, as the bytes of
+      // an E4M3 K come, four consecutive ones
 #pragma unroll
-      for (int k = 0; k < KK; ++k)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          f[k][h] = f[k][2 + h] = 0;
-          if (qp[h]) {
-            if (E8) {
-              const uint2 u = *reinterpret_cast<const uint2*>(qp[h] + 16 * k + 4 * tq);
-              f[k][h] = u.x;
-              f[k][2 + h] = u.y;
-            } else {
-              f[k][h] = *reinterpret_cast<const uint32_t*>(qp[h] + 16 * k + 2 * tq);
-              f[k][2 + h] = *reinterpret_cast<const uint32_t*>(qp[h] + 16 * k + 8 + 2 * tq);
-            }
+      for (int k = 0; k < KK; ++k) {
+        f[k][0] = f[k][1] = 0;
+        if (qp) {
+          if (E8) {
+            const uint2 u = *reinterpret_cast<const uint2*>(qp + 16 * k + 4 * tq);
+            f[k][0] = u.x;
+            f[k][1] = u.y;
+          } else {
+            f[k][0] = *reinterpret_cast<const uint32_t*>(qp + 16 * k + 2 * tq);
+            f[k][1] = *reinterpret_cast<const uint32_t*>(qp + 16 * k + 8 + 2 * tq);
           }
         }
-      if (E8) {  // bf16 -> fp16, the row's largest magnitude brought into [2^12, 2^13)
+      }
+      float down = p.scale2;
+      if (E8) {  // bf16 -> fp16, the query's largest magnitude brought into [2^12, 2^13)
+        uint32_t big = 0;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t big = 0;
+        for (int k = 0; k < KK; ++k)
 #pragma unroll
-          for (int k = 0; k < KK; ++k)
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t a = f[k][i] << 16 & 0x7fff0000u, b = f[k][i] & 0x7fff0000u;
+            if (a < 0x7f800000u) big = max(big, a);
+            if (b < 0x7f800000u) big = max(big, b);
+          }
+        big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+        big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+        // 2^(12 - floor(log2 big)), kept inside the normal range
+        const int e = big ? min(max(12 - ((int)(big >> 23) - 127), -126), 126) : 0;
+        const float up = pow2f(e);
+        down *= pow2f(-e);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint32_t u = f[k][h + 2 * i];
-              const uint32_t a = u << 16 & 0x7fff0000u, b = u & 0x7fff0000u;
-              if (a < 0x7f800000u) big = max(big, a);
-              if (b < 0x7f800000u) big = max(big, b);
-            }
-          big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
-          big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
-          // 2^(12 - floor(log2 big)), kept inside the normal range
-          const int e = big ? min(max(12 - ((int)(big >> 23) - 127), -126), 126) : 0;
-          const float up = pow2f(e);
-          rowf[mw][h] = p.scale2 * pow2f(-e);
+        for (int k = 0; k < KK; ++k)
 #pragma unroll
-          for (int k = 0; k < KK; ++k)
+          for (int i = 0; i < 2; ++i)
+            f[k][i] = pack_f16(__uint_as_float(f[k][i] << 16) * up,
+                                   __uint_as_float(f[k][i] & 0xffff0000u) * up);
+      }
+      if (!S::QS) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint32_t u = f[k][h + 2 * i];
-              f[k][h + 2 * i] = pack_f16(__uint_as_float(u << 16) * up, __uint_as_float(u & 0xffff0000u) * up);
-            }
+        for (int k = 0; k < KK; ++k) qf[S::QS ? 0 : n][k][0] = f[k][0], qf[S::QS ? 0 : n][k][1] = f[k][1];
+      } else if (team == 0) {  // two products' fragments side by side
+#pragma unroll
+        for (int k = 0; k < KK; k += 2)
+          sQ[((qg * NT + n) * KK + k) * 16 + lane] = make_uint4(f[k][0], f[k][1], f[k + 1][0], f[k + 1][1]);
+      }
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        z.rowf[n][y] = __shfl_sync(0xffffffffu, down, (2 * tq + y) * 4);
+        z.m[n][y] = -INFINITY;
+        z.l[n][y] = 0.f;
+        z.top[n][y] = -1;
+        if (q0 + 2 * tq + y < nq) {
+          query_of(p, cons.unit, q0 + 2 * tq + y, &head, &row);
+          z.top[n][y] = cons.len - p.a.rows + row;
         }
       }
-      if (MW == 1) {
 #pragma unroll
-        for (int k = 0; k < KK; ++k)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) qf[MW == 1 ? k : 0][i] = f[k][i];
-      } else if (ks == 0) {
-#pragma unroll
-        for (int k = 0; k < KK; ++k)
-          sQ[((qg * MW + mw) * KK + k) * 32 + lane] = make_uint4(f[k][0], f[k][1], f[k][2], f[k][3]);
-      }
-#pragma unroll
-      for (int i = 0; i < HD / 8; ++i) o[mw][i][0] = o[mw][i][1] = o[mw][i][2] = o[mw][i][3] = 0.f;
+      for (int i = 0; i < KK; ++i) z.o[n][i][0] = z.o[n][i][1] = z.o[n][i][2] = z.o[n][i][3] = 0.f;
     }
+
+    if (S::QS) __syncthreads();
+    const uint4* sq = S::QS ? sQ + qg * NT * KK * 16 + lane : nullptr;
 
     for (int t = t0; t < t1; ++t) {
       cp_async_wait<NST - 2>();
-      __syncthreads();  // this tile is here for all warps; the one before has been used
+      team_sync<QG>(team);  // this stage is here; the one before has been used
       produce();
-      const unsigned char* st = smem + stage * S::kStage;
-      const uint32_t sK = smem_u32(st), sV = sK + kTK * RB;
-      const float* sS = (const float*)(st + 2 * kTK * RB);
-      const int j0 = cons.first + t * kTK;
 #pragma unroll 1
-      for (int sub = ks; sub < 4; sub += KS) {
-        const int r0 = sub * 16;  // first key of the subtile in the tile
-        const unsigned ok = sOk[stage * 4 + sub];
-        // S = Q K^T: two 8-key blocks
-        float s[MW][2][4];
-#pragma unroll
-        for (int mw = 0; mw < MW; ++mw)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) s[mw][i][0] = s[mw][i][1] = s[mw][i][2] = s[mw][i][3] = 0.f;
-        {
-          const int mi = lane >> 3, r = r0 + (lane & 7) + 8 * (mi >> 1);
-          if (E8) {
-#pragma unroll
-            for (int k2 = 0; k2 < KK; k2 += 2) {
-              uint32_t kr[4];  // keys 0-7: columns 16 k2.., 16 k2 + 16..; keys 8-15 likewise
-              ldsm4(kr, sK + tile_at<RB>(r, k2 + (mi & 1)));
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const uint32_t a0 = e4m3x2_to_h2(kr[i] & 0xffffu), a1 = e4m3x2_to_h2(kr[i] >> 16);
-                const uint32_t b0 = e4m3x2_to_h2(kr[2 + i] & 0xffffu), b1 = e4m3x2_to_h2(kr[2 + i] >> 16);
-#pragma unroll
-                for (int mw = 0; mw < MW; ++mw) {
-                  uint32_t q[4];
-                  if (MW == 1) {
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) q[x] = qf[MW == 1 ? k2 + i : 0][x];
-                  } else {
-                    const uint4 u = sQ[((qg * MW + mw) * KK + k2 + i) * 32 + lane];
-                    q[0] = u.x, q[1] = u.y, q[2] = u.z, q[3] = u.w;
-                  }
-                  mma16816<true>(s[mw][0], q, a0, a1);
-                  mma16816<true>(s[mw][1], q, b0, b1);
-                }
-              }
-            }
-          } else {
-#pragma unroll
-            for (int k = 0; k < KK; ++k) {
-              uint32_t kr[4];
-              ldsm4(kr, sK + tile_at<RB>(r, 2 * k + (mi & 1)));
-#pragma unroll
-              for (int mw = 0; mw < MW; ++mw) {
-                uint32_t q[4];
-                if (MW == 1) {
-#pragma unroll
-                  for (int x = 0; x < 4; ++x) q[x] = qf[MW == 1 ? k : 0][x];
-                } else {
-                  const uint4 u = sQ[((qg * MW + mw) * KK + k) * 32 + lane];
-                  q[0] = u.x, q[1] = u.y, q[2] = u.z, q[3] = u.w;
-                }
-                mma16816<false>(s[mw][0], q, kr[0], kr[1]);
-                mma16816<false>(s[mw][1], q, kr[2], kr[3]);
-              }
-            }
-          }
-        }
-        // the thread's four keys: 2 tq, 2 tq + 1 of each block
-        float kf[2][2], ve[2][2], vm[2][2], vi[2][2];
-        if (E8) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const int key = r0 + 8 * i + 2 * tq + x;
-              kf[i][x] = sS[key];
-              const uint32_t u = __float_as_uint(sS[kTK + key]);  // 2^(u >> 23 - 127) times [1, 2)
-              ve[i][x] = __uint_as_float(0x4b000000u | u >> 23) - 8388735.f;
-              vm[i][x] = __uint_as_float(0x3f800000u | (u & 0x7fffffu));
-              vi[i][x] = pow2f(127 - (int)(u >> 23));
-            }
-        }
-        const int jb = j0 + r0;
-        const bool edge = ok != 0xffffu || jb + 15 > cons.len - p.a.rows ||
-                          (p.a.window > 0 && jb < cons.len - p.a.window);
-        uint32_t pa[MW][4], pl[MW][4];
-#pragma unroll
-        for (int mw = 0; mw < MW; ++mw) {
-          float x[2][2][2];  // [row half][block][key]
-          bool rise = false;
-#pragma unroll
-          for (int h = 0; h < (kHalf ? 1 : 2); ++h) {
-            float mx = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                float v = s[mw][i][2 * h + y] * rowf[mw][h];
-                if (E8) v = fmaf(v, kf[i][y], ve[i][y]);
-                if (edge) {
-                  const int key = 8 * i + 2 * tq + y, j = jb + key;
-                  const bool seen = (ok >> key & 1) && j <= top[mw][h] &&
-                                    (p.a.window <= 0 || j > top[mw][h] - p.a.window);
-                  v = seen ? v : -INFINITY;
-                }
-                x[h][i][y] = v;
-                mx = fmaxf(mx, v);
-              }
-            rise = rise || mx > m[mw][h] + 8.f;
-          }
-          if (__any_sync(0xffffffffu, rise)) {
-#pragma unroll
-            for (int h = 0; h < (kHalf ? 1 : 2); ++h) {
-              float mx = fmaxf(fmaxf(x[h][0][0], x[h][0][1]), fmaxf(x[h][1][0], x[h][1][1]));
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-              if (mx > m[mw][h] + 8.f) {
-                const float fix = ex2(m[mw][h] - mx);  // 0 for the first
-                m[mw][h] = mx;
-                l[mw][h] *= fix;
-#pragma unroll
-                for (int i = 0; i < HD / 8; ++i) {
-                  o[mw][i][2 * h] *= fix;
-                  o[mw][i][2 * h + 1] *= fix;
-                }
-              }
-            }
-          }
-#pragma unroll
-          for (int h = 0; h < (kHalf ? 1 : 2); ++h) {
-            const float ref = m[mw][h] == -INFINITY ? 0.f : m[mw][h];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              float w0 = ex2(x[h][i][0] - ref), w1 = ex2(x[h][i][1] - ref);
-              if (E8) {
-                l[mw][h] = fmaf(w0, vi[i][0], fmaf(w1, vi[i][1], l[mw][h]));
-                pa[mw][2 * i + h] = pack_f16(w0 * vm[i][0], w1 * vm[i][1]);
-              } else {
-                l[mw][h] += w0 + w1;
-                const uint32_t hi = pack_bf16(w0, w1);
-                pa[mw][2 * i + h] = hi;
-                pl[mw][2 * i + h] = pack_bf16(w0 - __uint_as_float(hi << 16), w1 - __uint_as_float(hi & 0xffff0000u));
-              }
-            }
-          }
-          if (kHalf) pa[mw][1] = pa[mw][3] = pl[mw][1] = pl[mw][3] = 0;
-        }
-        // O += P V
-        const int mi = lane >> 3, vr = r0 + (lane & 7) + 8 * (mi & 1);
-        bool odd = false;  // an infinity or NaN among values that not every row sees
-#pragma unroll
-        for (int c = 0; c < CPR; c += 2) {
-          uint32_t v[4];  // two 16-byte steps of keys 0-7 and 8-15
-          ldsm4_t(v, sV + tile_at<RB>(vr, c + (mi >> 1)));
-          if (E8) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              // bytes (key, key + 1) of columns 2g, 2g + 1
-              const uint32_t lo = __byte_perm(v[2 * i], 0, 0x3120), hi = __byte_perm(v[2 * i + 1], 0, 0x3120);
-              uint32_t e0 = e4m3x2_to_h2(lo & 0xffffu), e1 = e4m3x2_to_h2(hi & 0xffffu);
-              uint32_t d0 = e4m3x2_to_h2(lo >> 16), d1 = e4m3x2_to_h2(hi >> 16);
-              if (edge) {
-                const uint32_t a = e0, b = e1, cc = d0, d = d1;
-                e0 = finite_pair<true>(e0), e1 = finite_pair<true>(e1);
-                d0 = finite_pair<true>(d0), d1 = finite_pair<true>(d1);
-                odd = odd || a != e0 || b != e1 || cc != d0 || d != d1;
-              }
-#pragma unroll
-              for (int mw = 0; mw < MW; ++mw) {
-                mma16816<true>(o[mw][2 * (c + i)], pa[mw], e0, e1);
-                mma16816<true>(o[mw][2 * (c + i) + 1], pa[mw], d0, d1);
-              }
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              uint32_t b0 = v[2 * i], b1 = v[2 * i + 1];
-              if (edge) {
-                const uint32_t a = b0, b = b1;
-                b0 = finite_pair<false>(b0), b1 = finite_pair<false>(b1);
-                odd = odd || a != b0 || b != b1;
-              }
-#pragma unroll
-              for (int mw = 0; mw < MW; ++mw) {
-                mma16816<false>(o[mw][c + i], pa[mw], b0, b1);
-                mma16816<false>(o[mw][c + i], pl[mw], b0, b1);
-              }
-            }
-          }
-        }
-        if (edge && __any_sync(0xffffffffu, odd)) {
-          // give those values to the rows that do see them: weights by shuffle from the lane
-          // that holds them, values from shared memory
-#pragma unroll 1
-          for (int key = 0; key < 16; ++key) {
-            const int from = (lane & ~3) | (key & 7) >> 1;
-#pragma unroll
-            for (int mw = 0; mw < MW; ++mw)
-#pragma unroll
-              for (int h = 0; h < (kHalf ? 1 : 2); ++h) {
-                const uint32_t a = __shfl_sync(0xffffffffu, pa[mw][h], from);
-                const uint32_t b = __shfl_sync(0xffffffffu, pa[mw][2 + h], from);
-                const uint32_t u = key < 8 ? a : b;
-                const uint32_t bits = key & 1 ? u >> 16 : u & 0xffffu;
-                const float wgt = E8 ? h2_to_f2(bits).x : __uint_as_float(bits << 16);
-                if (wgt != 0.f) {
-                  const unsigned char* row = st + kTK * RB;
-#pragma unroll
-                  for (int i = 0; i < HD / 8; ++i)
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                      const int d = E8 ? 16 * (i >> 1) + 4 * tq + 2 * y + (i & 1) : 8 * i + 2 * tq + y;
-                      const int byte = d * (E8 ? 1 : 2);
-                      const unsigned char* at = row + tile_at<RB>(r0 + key, byte >> 4) + (byte & 15);
-                      const float val = E8 ? h2_to_f2(e4m3x2_to_h2(*at)).x : __bfloat162float(*(const bf16*)at);
-                      if (!(fabsf(val) <= 3.402823466e38f)) o[mw][i][2 * h + y] = fmaf(wgt, val, o[mw][i][2 * h + y]);
-                    }
-                }
-              }
-          }
-        }
+      for (int i = 0; i < NSUB; ++i) {
+        const unsigned char* blk = ring + stage * S::kStage + i * S::kBlock;
+        const unsigned ok = sOk[stage * NSUB + i];
+        const int jb = cons.first + t * TK + (team + KS * i) * 16;
+        if (ok == 0xffffu && jb + 15 <= cons.len - p.a.rows && (p.a.window <= 0 || jb >= cons.len - p.a.window))
+          block<HD, E8, NT, false>(p, z, qf, sq, blk, jb, ok);
+        else if (ok)
+          block<HD, E8, NT, true>(p, z, qf, sq, blk, jb, ok);
       }
       stage = stage + 1 == NST ? 0 : stage + 1;
     }
 
-    // ---- join the key groups in order, and write ----
+    // ---- join the teams in order, and write ----
 #pragma unroll
-    for (int mw = 0; mw < MW; ++mw)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int h = 0; h < (kHalf ? 1 : 2); ++h) {
-        l[mw][h] += __shfl_xor_sync(0xffffffffu, l[mw][h], 1);
-        l[mw][h] += __shfl_xor_sync(0xffffffffu, l[mw][h], 2);
-        if (tq == 0) sML[ks * QR + (qg * MW + mw) * 16 + g + 8 * h] = make_float2(m[mw][h], l[mw][h]);
+      for (int y = 0; y < 2; ++y) {
+        float l = z.l[n][y];
+        l += __shfl_xor_sync(0xffffffffu, l, 4);
+        l += __shfl_xor_sync(0xffffffffu, l, 8);
+        l += __shfl_xor_sync(0xffffffffu, l, 16);
+        if (g == 0) sML[team * QN + (qg * NT + n) * 8 + 2 * tq + y] = make_float2(z.m[n][y], l);
       }
     __syncthreads();
 #pragma unroll
-    for (int mw = 0; mw < MW; ++mw)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int h = 0; h < (kHalf ? 1 : 2); ++h) {
-        const int q = (qg * MW + mw) * 16 + g + 8 * h;
+      for (int y = 0; y < 2; ++y) {
+        const int q = (qg * NT + n) * 8 + 2 * tq + y;
         float M = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < KS; ++i) M = fmaxf(M, sML[i * QR + q].x);
-        const float f = M == -INFINITY ? 0.f : ex2(m[mw][h] - M);
+        for (int i = 0; i < KS; ++i) M = fmaxf(M, sML[i * QN + q].x);
+        const float f = M == -INFINITY ? 0.f : ex2(z.m[n][y] - M);
 #pragma unroll
-        for (int i = 0; i < HD / 8; ++i) {
-          o[mw][i][2 * h] *= f;
-          o[mw][i][2 * h + 1] *= f;
+        for (int i = 0; i < KK; ++i) {
+          z.o[n][i][y] *= f;
+          z.o[n][i][2 + y] *= f;
         }
       }
 #pragma unroll
     for (int turn = 0; turn < KS; ++turn) {
-      if (turn == ks) {
+      if (turn == team) {
 #pragma unroll
-        for (int mw = 0; mw < MW; ++mw)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int h = 0; h < (kHalf ? 1 : 2); ++h) {
-            float* row = sO + ((qg * MW + mw) * 16 + g + 8 * h) * S::kPitch;
-            if (E8) {
+          for (int y = 0; y < 2; ++y) {
+            float* row = sO + ((qg * NT + n) * 8 + 2 * tq + y) * S::kPitch;
 #pragma unroll
-              for (int c = 0; c < HD / 16; ++c) {
-                float4* at = reinterpret_cast<float4*>(row + 16 * c + 4 * tq);
-                float4 v = make_float4(o[mw][2 * c][2 * h], o[mw][2 * c + 1][2 * h], o[mw][2 * c][2 * h + 1],
-                                       o[mw][2 * c + 1][2 * h + 1]);
-                if (turn) {
-                  const float4 was = *at;
-                  v = make_float4(v.x + was.x, v.y + was.y, v.z + was.z, v.w + was.w);
-                }
-                *at = v;
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < HD / 8; ++i) {
-                float2* at = reinterpret_cast<float2*>(row + 8 * i + 2 * tq);
-                float2 v = make_float2(o[mw][i][2 * h], o[mw][i][2 * h + 1]);
-                if (turn) {
-                  const float2 was = *at;
-                  v = make_float2(v.x + was.x, v.y + was.y);
-                }
-                *at = v;
+            for (int i = 0; i < KK; ++i) {
+              const float a = z.o[n][i][y], b = z.o[n][i][2 + y];
+              if (E8) {
+                float2* at = reinterpret_cast<float2*>(row + 16 * i + 2 * g);
+                const float2 was = turn ? *at : make_float2(0.f, 0.f);
+                *at = make_float2(a + was.x, b + was.y);
+              } else {
+                float* at = row + 16 * i + g;
+                at[0] = turn ? at[0] + a : a;
+                at[8] = turn ? at[8] + b : b;
               }
             }
           }
@@ -570,10 +621,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attn_tc(const PagedAttn p
       const int q = i / (HD / 4), d = (i - q * (HD / 4)) * 4;
       float M = -INFINITY, L = 0.f;
 #pragma unroll
-      for (int x = 0; x < KS; ++x) M = fmaxf(M, sML[x * QR + q].x);
+      for (int x = 0; x < KS; ++x) M = fmaxf(M, sML[x * QN + q].x);
 #pragma unroll
       for (int x = 0; x < KS; ++x) {
-        const float2 ml = sML[x * QR + q];
+        const float2 ml = sML[x * QN + q];
         L += M == -INFINITY ? 0.f : ml.y * ex2(ml.x - M);
       }
       const float4 v = *reinterpret_cast<const float4*>(sO + q * S::kPitch + d);
@@ -589,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attn_tc(const PagedAttn p
       }
     }
     cons.skip(p, t1 - t0);
-    __syncthreads();  // sO (and sQ) and sML are free again
+    __syncthreads();  // sO, sML and sQ are free again
   }
   cp_async_wait<0>();
 }
@@ -615,6 +666,15 @@ cudaError_t launch_hd(const PagedAttn& p, int grid, cudaStream_t st) {
 }  // namespace
 
 namespace dmtp {
+
+int paged_tc_grid(int head_dim, bool e8, int qn) {
+#define DMTP_CTAS(HD_, E8_)                                                           \
+  (qn == 8 ? Shape<HD_, E8_, 8>::CTAS : qn == 16 ? Shape<HD_, E8_, 16>::CTAS          \
+                                      : Shape<HD_, E8_, 32>::CTAS)
+  return 152 * (head_dim == 64 ? (e8 ? DMTP_CTAS(64, true) : DMTP_CTAS(64, false))
+                               : (e8 ? DMTP_CTAS(128, true) : DMTP_CTAS(128, false)));
+#undef DMTP_CTAS
+}
 
 cudaError_t paged_attn_tc(const PagedAttn& p, const PagedPlan& pl, bool e8, cudaStream_t st) {
   if (p.m.head_dim == 64) return e8 ? launch_hd<64, true>(p, pl.grid, st) : launch_hd<64, false>(p, pl.grid, st);

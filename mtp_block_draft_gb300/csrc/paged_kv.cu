@@ -57,7 +57,8 @@ __global__ void __launch_bounds__(256) k_paged_write(const WriteArgs a, const Tu
       set_err(a.err, seq >= a.m.n_seqs ? DMTP_OPS_ERR_SEQ : DMTP_OPS_ERR_POS);
     return;
   }
-  const int page = page_of(a.m, seq, pos, threadIdx.x == 0 ? a.err : nullptr);
+  int off;
+  const int page = page_of(a.m, seq, pos, off, threadIdx.x == 0 ? a.err : nullptr);
   if (page < 0) return;
   const bool rot = a.r.rope_theta > 0.f;
   if (rot) {
@@ -65,7 +66,6 @@ __global__ void __launch_bounds__(256) k_paged_write(const WriteArgs a, const Tu
       cs[i] = cos_sin_turns((unsigned long long)(unsigned)pos * turns.f[i]);
     __syncthreads();
   }
-  const int off = pos % a.m.page_size;
   const int nq = a.r.q ? a.r.n_heads : 0, hkv = a.m.n_kv_heads, items = nq + 2 * hkv;
   const int gl = threadIdx.x & (a.group - 1), ng = blockDim.x / a.group;
   const bool on = gl < a.lanes;
@@ -152,9 +152,10 @@ __global__ void __launch_bounds__(256) k_paged_read(const ReadArgs a) {
     if (gl == 0) set_err(a.err, seq >= a.m.n_seqs ? DMTP_OPS_ERR_SEQ : DMTP_OPS_ERR_POS);
     return;
   }
-  const int page = page_of(a.m, seq, pos, gl == 0 ? a.err : nullptr);
+  int off;
+  const int page = page_of(a.m, seq, pos, off, gl == 0 ? a.err : nullptr);
   if (page < 0) return;
-  const int64_t line = (int64_t)h * a.m.page_size + pos % a.m.page_size;
+  const int64_t line = (int64_t)h * a.m.page_size + off;
   const int64_t at = (int64_t)page * a.m.page_stride + line * hd + 8 * gl;
   T* dst = (T*)(isv ? a.vo : a.ko) + ((int64_t)row * hkv + h) * hd + 8 * gl;
   if (E8) {

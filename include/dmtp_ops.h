@@ -157,7 +157,7 @@ int dmtp_add_rmsnorm_e4m3(const dmtp_norm_args* a, void* stream);
  * equal to the largest. A row that keeps nothing gets id -1. kept[r] (optional) is the
  * number of kept tokens. temperature, top_k, top_p, min_p: device arrays [rows], each
  * optional (NULL: 1, off, off, off). u: device fp32 [rows]. Weights and their sums are
- * integers of 2^-40 relative resolution or better, so a row's result depends on nothing
+ * integers (steps of 2^-44 of the largest, computed to about 2^-39), so a row's result depends on nothing
  * but its inputs. Limits: 1 <= vocab <= DMTP_OPS_MAX_SAMPLE_VOCAB, ld >= vocab. */
 typedef struct {
   const void* logits;

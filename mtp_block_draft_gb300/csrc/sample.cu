@@ -3,20 +3,25 @@
 //
 // A cluster of CTAs takes a row: each holds a slice of it in shared memory, as keys whose
 // unsigned order is the logits' order, so the logits are read from HBM once and every later
-// step runs on chip. Counts and weights are reduced over the cluster through distributed
-// shared memory.
+// step runs on chip; a thread owns consecutive ids. Counts, weights and histograms are reduced
+// over the cluster through distributed shared memory. What bounds it is issue: a handful of
+// instructions a logit for each pass over the keys, and about fifty for a weight.
 //
-// Weights. 2^y with y = (l - max) log2(e) / T as a 64-bit integer, so that sums are exact
-// and associative: no result depends on how a row was split. The exponent is formed as a
-// pair of floats (the difference, the factor and their product with their rounding errors);
-// 2^y = 2^n 2^(j/256) e^z with a table of 2^(j/256) in 62-bit fixed point and
-// e^z - 1 = z + z^2/2 + z^3/6 + z^4/24 (|z| < 0.00136, next term 4e-17). The scale is
-// chosen per row so that the row's sum stays below 2^62; the relative error of a weight is
-// about 2^-40.
+// Weights. 2^y with y = (l - max) log2(e) / T as an integer in 2^-44 steps of the largest, so
+// that sums are exact and associative: no result depends on how a row was split. The exponent
+// is formed as a pair of floats (the difference, the factor and their product with their
+// rounding errors); 2^y = 2^n 2^(j/256) 2^r with a table of 2^(j/256) in 62-bit fixed point and
+// 2^r - 1 as a series to r^4 (|r| < 2^-9, the next term is 2^-54). The error of a weight is
+// about 2^-39 of it and half a step.
 //
-// Filters. The cut is a key and the number of its ties that stay (lowest ids first): the
-// largest key whose count from above reaches top_k, then the largest whose weight from above
-// reaches top_p of the kept weight, found a bit at a time.
+// Filters. The cut is a key and, among its ties, how many of the lowest ids stay. Keys fall
+// into bins of 1/32 octave of weight; the bin in which the count from above reaches top_k is
+// then split by key until all of a bin stays or one key is left. For top_p the bins' counts
+// give the cut's neighbourhood (their weights, taken at the bins' centres, are off by at most
+// 1.1%); one pass then sums every weight exactly - all, those above the neighbourhood, and by
+// finer bins inside it - and the bin that the goal falls into is split likewise. A goal outside
+// the neighbourhood only costs another pass. The same pass leaves each thread's kept weight
+// above the neighbourhood, so the pick needs no second one.
 #include <math.h>
 
 #include "paged.cuh"
@@ -40,7 +45,7 @@ __device__ __forceinline__ unsigned long long exp2_256th(int j) {
 
 struct RowsArgs {
   dmtp_sample_args a;
-  int slice;  // keys of a CTA, a multiple of kThreads
+  int slice;  // keys of a CTA
   bool vec;   // rows allow 16-byte loads
 };
 
@@ -75,50 +80,54 @@ __device__ __forceinline__ unsigned long long part_of(float f, unsigned long lon
   return r + (up && rest ? 1 : 0);
 }
 
+constexpr int kShift = 44;  // weight 1 is 2^44: 2^18 of them stay below 2^63
+constexpr int kBins = 2048, kFine = 512;
+
 struct Weigh {
-  float top, chi, clo;
-  int shift;  // weight 1 is 2^shift
+  float top, chi, clo, cb;
   const unsigned long long* table;
 
-  // y = (l - max) c as a pair of floats
-  __device__ __forceinline__ void exponent(float l, float& hi, float& lo) const {
-    const float d = l - top, t = d - l;
-    const float e = (l - (d - t)) + (-top - t);
-    hi = d * chi;
-    lo = fmaf(d, chi, -hi) + fmaf(d, clo, e * chi);
-  }
-  __device__ __forceinline__ float rough(uint32_t key) const {
+  // Bin of 1/32 octave below the largest logit (the nearest, so bin i is centred at 2^(-i/32));
+  // decreasing in l, the last one takes the rest.
+  __device__ __forceinline__ int bin(uint32_t key) const {
     const float l = logit_of(key);
-    const float y = (l - top) * chi;
-    return l == top ? 1.f : y > -64.f ? ex2(y) : 0.f;
+    const float x = l == top ? 0.f : fminf((top - l) * cb, (float)(kBins - 1));
+    return (int)(__float_as_uint(x + 8388608.f) & (kBins - 1));
   }
   __device__ __forceinline__ unsigned long long operator()(uint32_t key) const {
     const float l = logit_of(key);
-    if (l == top) return 1ull << shift;
-    float hi, lo;
-    exponent(l, hi, lo);
-    if (!(hi > -64.f)) return 0ull;
-    const int j = __float2int_rn(hi * 256.f);  // |j| < 2^14
-    const float r = fmaf((float)j, -0.00390625f, hi);  // exact
-    // z = (r + lo) ln 2
-    const float zh = r * 0.693147182464599609f;
-    const float zl = fmaf(r, 0.693147182464599609f, -zh) + fmaf(r, -1.90465429995776804525e-09f, lo * 0.693147182464599609f);
-    const float z2 = zh * zh;
-    const float p = zl + z2 * fmaf(zh, fmaf(zh, 0.0416666679f, 0.166666672f), 0.5f);
-    const int g = __float2int_rn(zh * 1099511627776.f) + __float2int_rn(p * 1099511627776.f);  // 2^40
-    const unsigned long long t = table[j & 255];
-    const long long w = (long long)t + (((long long)(t >> 32) * g) >> 8);  // 62 bits: Q30 Q40 2^-8
-    const int down = 62 - shift - (j >> 8);
-    if (down > 63) return 0ull;
-    return down > 0 ? ((unsigned long long)w + (1ull << (down - 1))) >> down : (unsigned long long)w;
+    if (l == top) return 1ull << kShift;
+    const float d = l - top, t = d - l;
+    const float e = (l - (d - t)) + (-top - t);
+    const float hi = d * chi;
+    if (!(hi > -45.f)) return 0ull;  // below half a step
+    const float lo = fmaf(e, chi, fmaf(d, clo, fmaf(d, chi, -hi)));
+    // (adding 1.5 2^k rounds to steps of 2^(k - 23) and leaves the step count in the low bits)
+    const float jt = hi + 49152.f;
+    const int j = __float_as_int(jt) - __float_as_int(49152.f);
+    const float s = hi - (jt - 49152.f);  // exact, |s| <= 2^-9
+    const float h = s * 0.693147182464599609f;
+    float g = fmaf(s, 0.693147182464599609f, -h);
+    g = fmaf(s, -1.90465429995776804525e-09f, fmaf(lo, 0.693147182464599609f, g));
+    const float r = s + lo;
+    g = fmaf(r * r, fmaf(r, fmaf(r, 9.618129107628477e-3f, 5.550410866482158e-2f), 0.24022650695910072f), g);
+    const float a = h + 5.859375e-3f;  // 1.5 2^-8 (|h| < 2^-9): steps of 2^-31
+    const float b = (h - (a - 5.859375e-3f)) + g + 1.1444091796875e-5f;  // 1.5 2^-17: 2^-40
+    const int q = (__float_as_int(a) - __float_as_int(5.859375e-3f)) * 512 +
+                  (__float_as_int(b) - __float_as_int(1.1444091796875e-5f));  // 2^r - 1 in 2^-40
+    const unsigned long long t62 = table[j & 255];
+    const unsigned long long w = t62 + (unsigned long long)((long long)(int)(t62 >> 32) * q >> 8);
+    const int down = 62 - kShift - (j >> 8);  // 18 .. 63
+    return (w + (1ull << (down - 1))) >> down;
   }
 };
 
 struct Shared {
+  uint32_t hist[kBins], all[kBins], coarse[kBins];
   unsigned long long slot[2][16][2];  // one (count, weight) of each CTA of the cluster, twice
   unsigned long long warp[kWarps][2];
-  unsigned long long total[2];
-  int pick;
+  unsigned long long found[4];
+  int bins[2];
 };
 
 struct Cluster {
@@ -181,35 +190,95 @@ struct Cluster {
     for (unsigned r = 0; r < size; ++r) a = a > s->slot[p][r][0] ? a : s->slot[p][r][0];
     return a;
   }
-  // Exclusive sums, in order of warps and CTAs, of one pair per warp (valid in lane 0 of each
-  // warp); also the totals.
-  __device__ __forceinline__ void scan(unsigned long long a, unsigned long long b,
-                                       unsigned long long& before_a, unsigned long long& before_b,
-                                       unsigned long long& all_a, unsigned long long& all_b) {
-    const int wid = threadIdx.x >> 5;
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) s->warp[wid][0] = a, s->warp[wid][1] = b;
-    __syncthreads();
-    unsigned long long ta = 0, tb = 0;
-    before_a = before_b = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w == wid) before_a = ta, before_b = tb;
-      ta += s->warp[w][0];
-      tb += s->warp[w][1];
-    }
-    const int p = exchange(ta, tb);
-    all_a = all_b = 0;
-    for (unsigned r = 0; r < size; ++r) {
-      if (r < rank) before_a += s->slot[p][r][0], before_b += s->slot[p][r][1];
-      all_a += s->slot[p][r][0];
-      all_b += s->slot[p][r][1];
-    }
-  }
 };
 
+// Sum the cluster's histograms: every CTA gets the whole of it in `all`, and its own is cleared.
+__device__ __forceinline__ void reduce_hist(Cluster& cl, Shared& sh) {
+  cl.sync();
+  const int per = kBins / (int)cl.size;
+  for (int i = threadIdx.x; i < per; i += kThreads) {
+    const int at = (int)cl.rank * per + i;
+    uint32_t sum = 0;
+    for (unsigned r = 0; r < cl.size; ++r) {
+      uint32_t v;
+      asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(smem_in_rank(smem_u32(&sh.hist[at]), r)) : "memory");
+      sum += v;
+    }
+    for (unsigned r = 0; r < cl.size; ++r)
+      asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(smem_in_rank(smem_u32(&sh.all[at]), r)), "r"(sum) : "memory");
+  }
+  cl.sync();
+  for (int i = threadIdx.x; i < kBins; i += kThreads) sh.hist[i] = 0;
+}
+// Exclusive sum over the CTA's threads, and the total; all threads call it.
+__device__ __forceinline__ unsigned long long block_scan(Shared& sh, unsigned long long v,
+                                                         unsigned long long& total) {
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  unsigned long long inc = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned long long u = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += u;
+  }
+  __syncthreads();
+  if (lane == 31) sh.warp[wid][0] = inc;
+  __syncthreads();
+  unsigned long long before = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < wid) before += sh.warp[w][0];
+    total += sh.warp[w][0];
+  }
+  return before + inc - v;
+}
+// The bin of `all` (counts, the largest keys first) in which the running count reaches want,
+// 1 <= want <= the total: found = {bin, count before it, its own}. All threads call it.
+__device__ __forceinline__ void find_count(Shared& sh, unsigned long long want, int& bin,
+                                           unsigned long long& before, unsigned long long& own) {
+  constexpr int E = kBins / kThreads;
+  unsigned long long n = 0, total;
+#pragma unroll
+  for (int e = 0; e < E; ++e) n += sh.all[threadIdx.x * E + e];
+  unsigned long long at = block_scan(sh, n, total);
+  if (at < want && want <= at + n) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const unsigned long long c = sh.all[threadIdx.x * E + e];
+      if (at < want && want <= at + c) sh.found[0] = threadIdx.x * E + e, sh.found[1] = at, sh.found[2] = c;
+      at += c;
+    }
+  }
+  __syncthreads();
+  bin = (int)sh.found[0];
+  before = sh.found[1];
+  own = sh.found[2];
+}
+// The smallest key <= top whose bin is at most b: every warp searches 32 places at a time.
+__device__ __forceinline__ uint32_t first_key(const Weigh& W, uint32_t top, int b) {
+  uint32_t lo = 0x007fffffu, hi = top;  // bin(lo) > b (-infinity), bin(hi) <= b
+  const int lane = threadIdx.x & 31;
+  while (hi - lo > 1) {
+    const uint32_t x = lo + (uint32_t)((unsigned long long)(hi - lo) * (lane + 1) / 33);
+    const unsigned yes = __ballot_sync(0xffffffffu, x > lo && W.bin(x) <= b);
+    const int f = yes ? __ffs(yes) - 1 : 32;
+    const uint32_t nh = __shfl_sync(0xffffffffu, x, f & 31), nl = __shfl_sync(0xffffffffu, x, (f + 31) & 31);
+    if (f < 32) hi = nh;
+    if (f > 0) lo = nl;
+  }
+  return hi;
+}
+// 2^-44 weights as three 15-bit parts and a count in bins of the histogram: 32-bit sums hold
+// the 2^15 keys a CTA has at most.
+__device__ __forceinline__ void add_fine(Shared& sh, int i, unsigned long long w) {
+  atomicAdd(&sh.hist[i], 1u);
+  atomicAdd(&sh.hist[kFine + i], (uint32_t)w & 0x7fffu);
+  atomicAdd(&sh.hist[2 * kFine + i], (uint32_t)(w >> 15) & 0x7fffu);
+  atomicAdd(&sh.hist[3 * kFine + i], (uint32_t)(w >> 30));
+}
+
 template <typename T>
-__global__ void __launch_bounds__(kThreads) k_sample_rows(const RowsArgs sa) {
+__global__ void __launch_bounds__(kThreads, 2) k_sample_rows(const RowsArgs sa) {
   extern __shared__ __align__(16) uint32_t keys[];
   __shared__ Shared sh;
   __shared__ unsigned long long table[256];
@@ -217,31 +286,32 @@ __global__ void __launch_bounds__(kThreads) k_sample_rows(const RowsArgs sa) {
   unsigned size;
   asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(size));
   Cluster cl{&sh, cluster_rank(), size, 0};
-  const int row = blockIdx.x / size, tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-  const int V = a.vocab, slice = sa.slice;
+  const int row = blockIdx.x / size, tid = threadIdx.x, lane = tid & 31;
+  const int V = a.vocab, slice = sa.slice, E = slice / kThreads;
   const int base = (int)cl.rank * slice;
   const int mine = V > base ? min(slice, V - base) : 0;
   const T* lg = (const T*)a.logits + (int64_t)row * a.ld + base;
   if (tid < 256) table[tid] = exp2_256th(tid);
+  for (int i = tid; i < kBins; i += kThreads) sh.hist[i] = 0;
   uint32_t best = 0;
   if (sa.vec) {
-    constexpr int E = 16 / sizeof(T);
-    for (int i = tid * E; i < slice; i += kThreads * E) {
-      uint32_t k[E];
-      if (i + E <= mine) {
+    constexpr int X = 16 / sizeof(T);
+    for (int i = tid * X; i < slice; i += kThreads * X) {
+      uint32_t k[X];
+      if (i + X <= mine) {
         const uint4 u = __ldcs(reinterpret_cast<const uint4*>(lg + i));
         const T* t = reinterpret_cast<const T*>(&u);
 #pragma unroll
-        for (int e = 0; e < E; ++e) k[e] = key_of(to_f32(t[e]));
+        for (int e = 0; e < X; ++e) k[e] = key_of(to_f32(t[e]));
       } else {
 #pragma unroll
-        for (int e = 0; e < E; ++e) k[e] = i + e < mine ? key_of(to_f32(lg[i + e])) : kNone;
+        for (int e = 0; e < X; ++e) k[e] = i + e < mine ? key_of(to_f32(lg[i + e])) : kNone;
       }
 #pragma unroll
-      for (int e = 0; e < E; e += 4)
+      for (int e = 0; e < X; e += 4)
         *reinterpret_cast<uint4*>(keys + i + e) = make_uint4(k[e], k[e + 1], k[e + 2], k[e + 3]);
 #pragma unroll
-      for (int e = 0; e < E; ++e) best = max(best, k[e]);
+      for (int e = 0; e < X; ++e) best = max(best, k[e]);
     }
   } else {
     for (int i = tid; i < slice; i += kThreads) {
@@ -250,12 +320,13 @@ __global__ void __launch_bounds__(kThreads) k_sample_rows(const RowsArgs sa) {
       best = max(best, k);
     }
   }
-  cl.sync();  // every CTA of the cluster runs before one writes another's memory
-  const uint32_t top = (uint32_t)cl.max(best);
   const float temp = a.temperature ? __ldg(a.temperature + row) : 1.f;
   const int k = a.top_k ? __ldg(a.top_k + row) : 0;
   const float top_p = a.top_p ? __ldg(a.top_p + row) : 1.f;
   const float min_p = a.min_p ? __ldg(a.min_p + row) : 0.f;
+  const float u = __ldg(a.u + row);
+  cl.sync();  // every CTA of the cluster runs before one writes another's memory
+  const uint32_t top = (uint32_t)cl.max(best);
   const bool greedy = !(temp > 0.f);
   if (top == kNone || greedy) {
     unsigned long long id = 0;  // of the largest logit, the lowest: 2^32 - 1 - id is maximal
@@ -275,113 +346,243 @@ __global__ void __launch_bounds__(kThreads) k_sample_rows(const RowsArgs sa) {
   // c = log2(e) / T as a pair
   W.chi = 1.44269502162933349609f / temp;
   W.clo = (fmaf(-W.chi, temp, 1.44269502162933349609f) + 1.92596299112661746887e-08f) / temp;
-  float rough = 0.f;
-  unsigned long long nvalid = 0, none = 0;
-  for (int i = tid; i < mine; i += kThreads) {
-    const uint32_t x = keys[i];
-    if (x != kNone) rough += W.rough(x), ++nvalid;
-  }
-  {  // the row's weight in 2^-20 steps, only to choose the scale
-    unsigned long long r = (unsigned long long)(rough * 1048576.f) + 1;
-    cl.sum(nvalid, r);
-    W.shift = 61 - (64 - __clzll((long long)(r + (r >> 8) + (1ull << 12))) - 20);
-  }
-  // top-k: the largest key that at least k keys reach, and how many of its ties stay
-  uint32_t cut = 1;  // the smallest key that stays
-  unsigned long long ties = ~0ull;
-  if (k > 0 && (unsigned long long)k < nvalid) {
-    cut = 0;
-    for (uint32_t bit = 0x80000000u; bit; bit >>= 1) {
-      const uint32_t c = cut | bit;
-      unsigned long long n = 0;
-      none = 0;
-      for (int i = tid; i < mine; i += kThreads) n += keys[i] >= c;
-      cl.sum(n, none);
-      if (n >= (unsigned long long)k) cut = c;
-    }
-    unsigned long long above = 0;
-    none = 0;
-    for (int i = tid; i < mine; i += kThreads) above += keys[i] > cut;
-    cl.sum(above, none);
-    ties = (unsigned long long)k - above;
-  }
-  if (top_p < 1.f) {
-    unsigned long long eq = 0, mass = 0;
-    for (int i = tid; i < mine; i += kThreads) {
-      const uint32_t x = keys[i];
-      if (x > cut) mass += W(x);
-      eq += x == cut;
-    }
-    cl.sum(eq, mass);
-    const unsigned long long cut_w = W(cut), cut_n = eq < ties ? eq : ties;
-    mass += cut_n * cut_w;
-    unsigned long long goal = part_of(fmaxf(top_p, 0.f), mass, true);
-    goal = goal ? goal : 1ull;
-    uint32_t t = 0;
-    for (uint32_t bit = 0x80000000u; bit; bit >>= 1) {
-      const uint32_t c = t | bit;
-      unsigned long long m = 0;
-      none = 0;
-      for (int i = tid; i < mine; i += kThreads) {
-        const uint32_t x = keys[i];
-        if (x >= c && x > cut) m += W(x);
-      }
-      cl.sum(none, m);
-      if (c <= cut) m += cut_n * cut_w;
-      if (m >= goal) t = c;
-    }
-    // the first ties of key t that bring the weight above it to the goal
-    unsigned long long above = 0;
-    none = 0;
-    for (int i = tid; i < mine; i += kThreads) {
-      const uint32_t x = keys[i];
-      if (x > t && x > cut) above += W(x);
-    }
-    cl.sum(none, above);
-    const unsigned long long wt = W(t);
-    const unsigned long long need = wt ? (goal - above + wt - 1) / wt : ~0ull;
-    ties = t == cut ? (need < ties ? need : ties) : need;
-    cut = t;
-  }
-  unsigned long long least = 0;
-  if (min_p > 0.f) least = min_p < 1.f ? part_of(min_p, 1ull << W.shift, true) : 1ull << W.shift;
-  // ranks of the ties of the cut in order of id, by warps that hold consecutive ids
-  const int ws = slice / kWarps, w0 = wid * ws;
-  unsigned long long eq = 0;
-  for (int i = lane; i < ws; i += 32) eq += __popc(__ballot_sync(0xffffffffu, keys[w0 + i] == cut));
-  unsigned long long rank0, zero, all, zero2;
-  cl.scan(eq, 0, rank0, zero, all, zero2);
-  unsigned long long mass = 0, cnt = 0, r = rank0;
-  for (int i = lane; i < ws; i += 32) {
-    const uint32_t x = keys[w0 + i];
-    const unsigned tie = __ballot_sync(0xffffffffu, x == cut);
-    const unsigned long long my = r + __popc(tie & ((1u << lane) - 1));
-    r += __popc(tie);
-    if (x > cut || (x == cut && my < ties)) {
-      const unsigned long long w = W(x);
-      if (w >= least) mass += w, ++cnt;
-    }
-  }
+  W.cb = fminf(W.chi * 32.f, 1e30f);
+  const uint2* own = reinterpret_cast<const uint2*>(keys + tid * E);  // this thread's ids, E even
+  const unsigned long long least =
+      min_p > 0.f ? (min_p < 1.f ? part_of(min_p, 1ull << kShift, true) : 1ull << kShift) : 0ull;
+  const bool by_p = top_p < 1.f;
+  // the smallest key that stays; `ties` of its keys stay, all of them unless `partial`
+  uint32_t cut = 1;
+  unsigned long long ties = 0;
+  bool partial = false;
+  int last_bin = kBins - 1;          // the last bin that top-k leaves
+  unsigned long long last_n = ~0ull; // and how many of its keys
+
+  if (k > 0 || by_p) {
+    // the two end bins, where flat rows and masked logits crowd, are counted by thread
+    uint32_t ends[2] = {0, 0};
+    for (int i = 0; i < E / 2; ++i) {
+      const uint2 xy = own[i];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    mass += __shfl_xor_sync(0xffffffffu, mass, o);
-    cnt += __shfl_xor_sync(0xffffffffu, cnt, o);
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t x = e ? xy.y : xy.x;
+        if (x == kNone) continue;
+        const int b = W.bin(x);
+        if (b == 0)
+          ++ends[0];
+        else if (b == kBins - 1)
+          ++ends[1];
+        else
+          atomicAdd(&sh.hist[b], 1u);
+      }
+    }
+    ends[0] = __reduce_add_sync(0xffffffffu, ends[0]);
+    ends[1] = __reduce_add_sync(0xffffffffu, ends[1]);
+    if (lane == 0 && ends[0]) atomicAdd(&sh.hist[0], ends[0]);
+    if (lane == 1 && ends[1]) atomicAdd(&sh.hist[kBins - 1], ends[1]);
+    reduce_hist(cl, sh);
+    unsigned long long n = 0, nvalid;
+    for (int i = tid; i < kBins; i += kThreads) n += sh.coarse[i] = sh.all[i];
+    block_scan(sh, n, nvalid);
+    if (k > 0 && (unsigned long long)k < nvalid) {
+      unsigned long long before, cnt, want = k;
+      find_count(sh, want, last_bin, before, cnt);
+      want -= before;
+      last_n = want;
+      uint32_t lo = first_key(W, top, last_bin), hi = last_bin ? first_key(W, top, last_bin - 1) - 1 : top;
+      while (want != cnt && lo != hi) {
+        const int sh_ = max(0, 32 - __clz((int)(hi - lo)) - 11);
+        for (int i = 0; i < E / 2; ++i) {
+          const uint2 x = own[i];
+          if (x.x >= lo && x.x <= hi) atomicAdd(&sh.hist[hi - x.x >> sh_], 1u);
+          if (x.y >= lo && x.y <= hi) atomicAdd(&sh.hist[hi - x.y >> sh_], 1u);
+        }
+        reduce_hist(cl, sh);
+        int f;
+        find_count(sh, want, f, before, cnt);
+        want -= before;
+        hi -= (uint32_t)f << sh_;
+        lo = hi - lo < (1u << sh_) ? lo : hi - ((1u << sh_) - 1);
+      }
+      cut = lo;
+      partial = want != cnt;
+      ties = want;
+    }
   }
-  unsigned long long mass0, cnt0, total, kept;
-  cl.scan(mass, cnt, mass0, cnt0, total, kept);
-  const float u = __ldg(a.u + row);
+
+  unsigned long long mass = 0, cnt = 0;  // of this thread's kept keys, so far those above `from`
+  uint32_t from = 0xffffffffu;
+  const unsigned long long tie_mass = partial ? ties * W(cut) : 0ull;
+  if (by_p) {
+    // the neighbourhood of the cut: bins whose running weight is about top_p of all
+    constexpr int BE = kBins / kThreads;
+    {
+      float m[BE], sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < BE; ++e) {
+        const int i = tid * BE + e;
+        const unsigned long long n = sh.coarse[i];
+        m[e] = i < last_bin ? (float)n : i == last_bin ? (float)(n < last_n ? n : last_n) : 0.f;
+        m[e] *= ex2(-(float)i * 0.03125f);
+        sum += m[e];
+      }
+      unsigned long long total;  // (in 2^-24: order does not matter)
+      unsigned long long at = block_scan(sh, (unsigned long long)(sum * 16777216.f), total);
+      if (tid == 0) sh.bins[0] = last_bin, sh.bins[1] = last_bin;
+      __syncthreads();
+      // a weight taken at its bin's centre is off by 1.1% at most, 0.6% in the mean square,
+      // and the errors of the many weights of a flat row average out
+      const float p = fmaxf(top_p, 0.f) * (float)total;
+      const float wide = fminf(0.023f, 0.001f + 0.03f * rsqrtf((float)total * 5.9604645e-8f));
+      float run = (float)at;
+      int lo_b = kBins, hi_b = kBins;
+#pragma unroll
+      for (int e = 0; e < BE; ++e) {
+        run += m[e] * 16777216.f;
+        if (run >= p * (1.f - wide)) lo_b = min(lo_b, tid * BE + e);
+        if (run >= p * (1.f + wide)) hi_b = min(hi_b, tid * BE + e);
+      }
+      if (lo_b <= last_bin) atomicMin(&sh.bins[0], lo_b);
+      if (hi_b <= last_bin) atomicMin(&sh.bins[1], hi_b);
+      __syncthreads();
+    }
+    uint32_t hi = sh.bins[0] ? first_key(W, top, sh.bins[0] - 1) - 1 : top;
+    const uint32_t least_key = partial ? cut + 1 : cut;  // below it, only the cut's own ties
+    uint32_t lo = max(first_key(W, top, sh.bins[1]), least_key);
+    if (hi < lo) hi = lo;
+    // every weight once: all, above the neighbourhood, and inside it by finer bins
+    unsigned long long sum = 0, above = 0;
+    int shift = max(0, 32 - __clz((int)(hi - lo)) - 9);
+    from = hi;
+    for (int i = 0; i < E / 2; ++i) {
+      const uint2 xy = own[i];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t x = e ? xy.y : xy.x;
+        if (x < cut || (partial && x == cut)) continue;
+        const unsigned long long w = W(x);
+        sum += w;
+        if (x > hi) {
+          above += w;
+          if (w >= least) mass += w, ++cnt;
+        } else if (x >= lo) {
+          add_fine(sh, hi - x >> shift, w);
+        }
+      }
+    }
+    cl.sum(sum, above);
+    sum += tie_mass;
+    unsigned long long goal = part_of(fmaxf(top_p, 0.f), sum, true);
+    goal = goal ? goal : 1ull;
+    // the first key from above at which the running weight reaches the goal
+    while (true) {
+      reduce_hist(cl, sh);
+      const uint32_t n = sh.all[tid];
+      const unsigned long long m = (unsigned long long)sh.all[kFine + tid] +
+                                   ((unsigned long long)sh.all[2 * kFine + tid] << 15) +
+                                   ((unsigned long long)sh.all[3 * kFine + tid] << 30);
+      unsigned long long total;
+      const unsigned long long at = above + block_scan(sh, m, total);
+      if (at < goal && goal <= at + m) sh.found[0] = tid, sh.found[1] = at, sh.found[2] = n, sh.found[3] = m;
+      __syncthreads();
+      if (above >= goal) {  // the goal lies above this range
+        lo = hi + 1;
+        hi = top;
+        above = 0;
+      } else if (above + total < goal) {  // or below it
+        above += total;
+        if (lo <= least_key) {  // only the cut's own ties are left
+          const unsigned long long wc = W(cut);
+          const unsigned long long need = wc ? (goal - above + wc - 1) / wc : ties;
+          ties = need < ties ? need : ties;
+          break;
+        }
+        hi = lo - 1;
+        lo = least_key;
+      } else {
+        const int f = (int)sh.found[0];
+        above = sh.found[1];
+        hi -= (uint32_t)f << shift;
+        lo = hi - lo < (1u << shift) ? lo : hi - ((1u << shift) - 1);
+        const unsigned long long c = sh.found[2];
+        if (c == 1 || lo == hi) {
+          const unsigned long long wl = c == 1 ? 0ull : sh.found[3] / c;
+          const unsigned long long need = c == 1 ? 1ull : (goal - above + wl - 1) / wl;
+          partial = need < c;
+          ties = need;
+          cut = lo;
+          break;
+        }
+      }
+      shift = max(0, 32 - __clz((int)(hi - lo)) - 9);
+      __syncthreads();  // found has been read, the histogram cleared
+      for (int i = 0; i < E / 2; ++i) {
+        const uint2 xy = own[i];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t x = e ? xy.y : xy.x;
+          if (x >= lo && x <= hi) add_fine(sh, hi - x >> shift, W(x));
+        }
+      }
+    }
+    if (cut > from) {  // the cut came out above the first neighbourhood: count again
+      from = 0xffffffffu;
+      mass = cnt = 0;
+    }
+  }
+
+  // ranks of the cut's ties in order of id
+  unsigned long long rank = 0;
+  if (partial) {
+    unsigned long long n = 0, total;
+    for (int i = 0; i < E; ++i) n += keys[tid * E + i] == cut;
+    rank = block_scan(sh, n, total);
+    const int p = cl.exchange(total, 0);
+    for (unsigned r = 0; r < cl.rank; ++r) rank += sh.slot[p][r][0];
+  }
+  {
+    unsigned long long r = rank;
+    for (int i = 0; i < E / 2; ++i) {
+      const uint2 xy = own[i];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t x = e ? xy.y : xy.x;
+        if (x < cut || x > from) continue;
+        if (partial && x == cut && r++ >= ties) continue;
+        const unsigned long long w = W(x);
+        if (w >= least) mass += w, ++cnt;
+      }
+    }
+  }
+  // the pick: the thread whose ids hold it, then its ids by a warp
+  unsigned long long total, kept, in_cta;
+  unsigned long long before = block_scan(sh, mass, in_cta);
+  {
+    unsigned long long n_cta;
+    block_scan(sh, cnt, n_cta);
+    const int p = cl.exchange(in_cta, n_cta);
+    total = kept = 0;
+    for (unsigned r = 0; r < size; ++r) {
+      if (r < cl.rank) before += sh.slot[p][r][0];
+      total += sh.slot[p][r][0];
+      kept += sh.slot[p][r][1];
+    }
+  }
   const unsigned long long goal = u >= 1.f ? total - 1 : u > 0.f ? part_of(u, total, false) : 0ull;
   if (cl.rank == 0 && tid == 0 && a.kept) a.kept[row] = (int)kept;
-  if (goal >= mass0 && goal < mass0 + mass) {  // this warp holds the pick
-    unsigned long long run = mass0;
-    r = rank0;
-    for (int i = lane; i < ws; i += 32) {
-      const uint32_t x = keys[w0 + i];
+  const unsigned holder = __ballot_sync(0xffffffffu, goal >= before && goal < before + mass);
+  if (holder) {
+    const int t = __ffs(holder) - 1;
+    unsigned long long run = __shfl_sync(0xffffffffu, before, t), r = __shfl_sync(0xffffffffu, rank, t);
+    const int first = (tid - lane + t) * E;
+    for (int i0 = 0; i0 < E; i0 += 32) {
+      const int i = i0 + lane;
+      const uint32_t x = i < E ? keys[first + i] : kNone;
       const unsigned tie = __ballot_sync(0xffffffffu, x == cut);
       const unsigned long long my = r + __popc(tie & ((1u << lane) - 1));
       r += __popc(tie);
       unsigned long long w = 0;
-      if (x > cut || (x == cut && my < ties)) {
+      if (x >= cut && !(partial && x == cut && my >= ties)) {
         w = W(x);
         if (w < least) w = 0;
       }
@@ -393,7 +594,7 @@ __global__ void __launch_bounds__(kThreads) k_sample_rows(const RowsArgs sa) {
       }
       const unsigned hit = __ballot_sync(0xffffffffu, run + inc > goal);
       if (hit) {
-        if (lane == __ffs(hit) - 1) a.ids[row] = base + w0 + i;
+        if (lane == __ffs(hit) - 1) a.ids[row] = base + first + i;
         break;
       }
       run += __shfl_sync(0xffffffffu, inc, 31);
@@ -412,7 +613,7 @@ template <typename T>
 cudaError_t launch(const RowsArgs& s, unsigned cluster, cudaStream_t st) {
   static unsigned long long done = 0;
   auto k = k_sample_rows<T>;
-  const int most = (DMTP_OPS_MAX_SAMPLE_VOCAB / 8) * 4;
+  const int most = 2 * 33 * kThreads * 4;  // of the largest vocabulary
   if (!smem_limit((const void*)k, most, &done)) return cudaErrorInvalidValue;
   return launch_op(k, (unsigned)s.a.rows * cluster, kThreads, (size_t)s.slice * 4, st, false, cluster, s);
 }
@@ -435,7 +636,10 @@ extern "C" int dmtp_sample_rows(const dmtp_sample_args* a, void* stream) {
   s.a = *a;
   const unsigned cluster = a->vocab > 8192 ? 8 : a->vocab > 2048 ? 2 : 1;
   const int per = (a->vocab + (int)cluster - 1) / (int)cluster;
-  s.slice = (per + kThreads - 1) / kThreads * kThreads;
+  // a thread's ids: an odd number of pairs, so that the threads' pairs lie in different banks
+  int pairs = (per + 2 * kThreads - 1) / (2 * kThreads);
+  pairs += 1 - pairs % 2;
+  s.slice = 2 * pairs * kThreads;
   s.vec = aligned_to(a->logits, 16) && mult(a->ld * es, 16);
   const cudaError_t e = a->dtype ? launch<bf16>(s, cluster, (cudaStream_t)stream)
                                  : launch<float>(s, cluster, (cudaStream_t)stream);

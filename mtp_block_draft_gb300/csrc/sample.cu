@@ -28,8 +28,7 @@
 
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr uint32_t kNone = 0u;            // key of a logit that is never kept
+constexpr float kMasked = -INFINITY;  // what a logit that is never kept becomes
 
 // 2^(2^-i), i = 1..8, in 62-bit fixed point: 2^(j/256) is the product of those of j's bits.
 __constant__ const unsigned long long kRoots[8] = {
@@ -45,14 +44,16 @@ __device__ __forceinline__ unsigned long long exp2_256th(int j) {
 
 struct RowsArgs {
   dmtp_sample_args a;
-  int slice;  // keys of a CTA
+  int slice;  // logits of a CTA
   bool vec;   // rows allow 16-byte loads
 };
 
+__device__ __forceinline__ float clean(float l) {  // NaN: masked; +infinity: the largest number
+  return fminf(fmaxf(l, kMasked), 3.402823466e38f);
+}
+// Unsigned keys in the order of the logits (+-0 alike), to search and split ranges.
 __device__ __forceinline__ uint32_t key_of(float l) {
-  l += 0.f;  // -0 ties with +0
-  const uint32_t u = __float_as_uint(l);
-  if (!(l > -INFINITY)) return kNone;  // NaN, -infinity
+  const uint32_t u = __float_as_uint(l + 0.f);
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 __device__ __forceinline__ float logit_of(uint32_t key) {
@@ -81,7 +82,7 @@ __device__ __forceinline__ unsigned long long part_of(float f, unsigned long lon
 }
 
 constexpr int kShift = 44;  // weight 1 is 2^44: 2^18 of them stay below 2^63
-constexpr int kBins = 2048, kFine = 512;
+constexpr int kBins = 2048, kFine = 512, kList = 1024;
 
 struct Weigh {
   float top, chi, clo, cb;
@@ -89,18 +90,15 @@ struct Weigh {
 
   // Bin of 1/32 octave below the largest logit (the nearest, so bin i is centred at 2^(-i/32));
   // decreasing in l, the last one takes the rest.
-  __device__ __forceinline__ int bin(uint32_t key) const {
-    const float l = logit_of(key);
-    const float x = l == top ? 0.f : fminf((top - l) * cb, (float)(kBins - 1));
+  __device__ __forceinline__ int bin(float l) const {
+    const float x = fminf((top - l) * cb, (float)(kBins - 1));
     return (int)(__float_as_uint(x + 8388608.f) & (kBins - 1));
   }
-  __device__ __forceinline__ unsigned long long operator()(uint32_t key) const {
-    const float l = logit_of(key);
-    if (l == top) return 1ull << kShift;
+  __device__ __forceinline__ unsigned long long operator()(float l) const {
     const float d = l - top, t = d - l;
     const float e = (l - (d - t)) + (-top - t);
     const float hi = d * chi;
-    if (!(hi > -45.f)) return 0ull;  // below half a step
+    if (!(hi > -45.f)) return 0ull;  // below half a step, or masked
     const float lo = fmaf(e, chi, fmaf(d, clo, fmaf(d, chi, -hi)));
     // (adding 1.5 2^k rounds to steps of 2^(k - 23) and leaves the step count in the low bits)
     const float jt = hi + 49152.f;
@@ -122,16 +120,27 @@ struct Weigh {
   }
 };
 
+template <int THREADS>
 struct Shared {
-  uint32_t hist[kBins], all[kBins], coarse[kBins];
-  unsigned long long slot[2][16][2];  // one (count, weight) of each CTA of the cluster, twice
+  static constexpr int kWarps = THREADS / 32;
+  uint32_t hist[kBins], all[kBins];
+  unsigned long long slot[2][16][2];  // one pair of each CTA of the cluster, twice
   unsigned long long warp[kWarps][2];
   unsigned long long found[4];
+  unsigned long long extra[THREADS];  // kept weight that the list gives a thread
+  uint32_t extra_n[THREADS];
+  float list[kList];                  // the neighbourhood's logits of this CTA, and where they are
+  uint16_t where[kList];
+  unsigned listed;
+  uint32_t edge[3];
   int bins[2];
+  unsigned long long table[256];
 };
 
+template <int THREADS>
 struct Cluster {
-  Shared* s;
+  static constexpr int kWarps = THREADS / 32;
+  Shared<THREADS>* s;
   unsigned rank, size;
   int phase;
 
@@ -172,264 +181,243 @@ struct Cluster {
     a = b = 0;
     for (unsigned r = 0; r < size; ++r) a += s->slot[p][r][0], b += s->slot[p][r][1];
   }
-  __device__ __forceinline__ unsigned long long max(unsigned long long a) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const unsigned long long v = __shfl_xor_sync(0xffffffffu, a, o);
-      a = a > v ? a : v;
-    }
+  __device__ __forceinline__ uint32_t max(uint32_t a) {
+    a = __reduce_max_sync(0xffffffffu, a);
     __syncthreads();
     if ((threadIdx.x & 31) == 0) s->warp[threadIdx.x >> 5][0] = a;
     __syncthreads();
     if (threadIdx.x < 32) {
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) a = a > s->warp[w][0] ? a : s->warp[w][0];
+      for (int w = 0; w < kWarps; ++w) a = ::max(a, (uint32_t)s->warp[w][0]);
     }
     const int p = exchange(a, 0);
     a = 0;
-    for (unsigned r = 0; r < size; ++r) a = a > s->slot[p][r][0] ? a : s->slot[p][r][0];
+    for (unsigned r = 0; r < size; ++r) a = ::max(a, (uint32_t)s->slot[p][r][0]);
     return a;
+  }
+  // Sum the cluster's histograms: every CTA gets the whole of it in `all`, and its own is
+  // cleared (a barrier of the CTA must come before the next one is begun).
+  __device__ __forceinline__ void sum_hist() {
+    sync();
+    const int per = kBins / (int)size;
+    for (int i = threadIdx.x; i < per; i += THREADS) {
+      const int at = (int)rank * per + i;
+      uint32_t n = 0;
+      for (unsigned r = 0; r < size; ++r) {
+        uint32_t v;
+        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(smem_in_rank(smem_u32(&s->hist[at]), r)) : "memory");
+        n += v;
+      }
+      for (unsigned r = 0; r < size; ++r)
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(smem_in_rank(smem_u32(&s->all[at]), r)), "r"(n) : "memory");
+    }
+    sync();
+    for (int i = threadIdx.x; i < kBins; i += THREADS) s->hist[i] = 0;
+  }
+  // Exclusive sum over the CTA's threads, and the total; all threads call it.
+  __device__ __forceinline__ unsigned long long scan(unsigned long long v, unsigned long long& total) {
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    unsigned long long inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long u = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += u;
+    }
+    __syncthreads();
+    if (lane == 31) s->warp[wid][0] = inc;
+    __syncthreads();
+    unsigned long long before = 0;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < wid) before += s->warp[w][0];
+      total += s->warp[w][0];
+    }
+    return before + inc - v;
+  }
+  // The bin of `all` (counts, the largest logits first) in which the running count reaches
+  // want, 1 <= want <= the total, the count before it and its own. All threads call it.
+  __device__ __forceinline__ void find_count(unsigned long long want, int& bin, unsigned long long& before,
+                                             unsigned long long& own) {
+    constexpr int E = kBins / THREADS;
+    unsigned long long n = 0, total;
+#pragma unroll
+    for (int e = 0; e < E; ++e) n += s->all[threadIdx.x * E + e];
+    unsigned long long at = scan(n, total);
+    if (at < want && want <= at + n) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const unsigned long long c = s->all[threadIdx.x * E + e];
+        if (at < want && want <= at + c) s->found[0] = threadIdx.x * E + e, s->found[1] = at, s->found[2] = c;
+        at += c;
+      }
+    }
+    __syncthreads();
+    bin = (int)s->found[0];
+    before = s->found[1];
+    own = s->found[2];
+  }
+  // 2^-44 weights as three 15-bit parts and a count in bins of the histogram: 32-bit sums hold
+  // the 2^16 logits a CTA has at most.
+  __device__ __forceinline__ void add_fine(int i, unsigned long long w) {
+    atomicAdd(&s->hist[i], 1u);
+    atomicAdd(&s->hist[kFine + i], (uint32_t)w & 0x7fffu);
+    atomicAdd(&s->hist[2 * kFine + i], (uint32_t)(w >> 15) & 0x7fffu);
+    atomicAdd(&s->hist[3 * kFine + i], (uint32_t)(w >> 30));
   }
 };
 
-// Sum the cluster's histograms: every CTA gets the whole of it in `all`, and its own is cleared.
-__device__ __forceinline__ void reduce_hist(Cluster& cl, Shared& sh) {
-  cl.sync();
-  const int per = kBins / (int)cl.size;
-  for (int i = threadIdx.x; i < per; i += kThreads) {
-    const int at = (int)cl.rank * per + i;
-    uint32_t sum = 0;
-    for (unsigned r = 0; r < cl.size; ++r) {
-      uint32_t v;
-      asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(smem_in_rank(smem_u32(&sh.hist[at]), r)) : "memory");
-      sum += v;
-    }
-    for (unsigned r = 0; r < cl.size; ++r)
-      asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(smem_in_rank(smem_u32(&sh.all[at]), r)), "r"(sum) : "memory");
-  }
-  cl.sync();
-  for (int i = threadIdx.x; i < kBins; i += kThreads) sh.hist[i] = 0;
-}
-// Exclusive sum over the CTA's threads, and the total; all threads call it.
-__device__ __forceinline__ unsigned long long block_scan(Shared& sh, unsigned long long v,
-                                                         unsigned long long& total) {
-  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  unsigned long long inc = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const unsigned long long u = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += u;
-  }
-  __syncthreads();
-  if (lane == 31) sh.warp[wid][0] = inc;
-  __syncthreads();
-  unsigned long long before = 0;
-  total = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < wid) before += sh.warp[w][0];
-    total += sh.warp[w][0];
-  }
-  return before + inc - v;
-}
-// The bin of `all` (counts, the largest keys first) in which the running count reaches want,
-// 1 <= want <= the total: found = {bin, count before it, its own}. All threads call it.
-__device__ __forceinline__ void find_count(Shared& sh, unsigned long long want, int& bin,
-                                           unsigned long long& before, unsigned long long& own) {
-  constexpr int E = kBins / kThreads;
-  unsigned long long n = 0, total;
-#pragma unroll
-  for (int e = 0; e < E; ++e) n += sh.all[threadIdx.x * E + e];
-  unsigned long long at = block_scan(sh, n, total);
-  if (at < want && want <= at + n) {
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const unsigned long long c = sh.all[threadIdx.x * E + e];
-      if (at < want && want <= at + c) sh.found[0] = threadIdx.x * E + e, sh.found[1] = at, sh.found[2] = c;
-      at += c;
-    }
-  }
-  __syncthreads();
-  bin = (int)sh.found[0];
-  before = sh.found[1];
-  own = sh.found[2];
-}
-// The smallest key <= top whose bin is at most b: every warp searches 32 places at a time.
-__device__ __forceinline__ uint32_t first_key(const Weigh& W, uint32_t top, int b) {
-  uint32_t lo = 0x007fffffu, hi = top;  // bin(lo) > b (-infinity), bin(hi) <= b
+// The smallest key <= top of which yes(logit) holds (it holds of top, and of every key above
+// one of which it holds); one warp searches 32 places at a time.
+template <typename F>
+__device__ __forceinline__ uint32_t first_key(uint32_t top, F yes) {
+  uint32_t lo = 0x007fffffu, hi = top;  // minus infinity
   const int lane = threadIdx.x & 31;
   while (hi - lo > 1) {
     const uint32_t x = lo + (uint32_t)((unsigned long long)(hi - lo) * (lane + 1) / 33);
-    const unsigned yes = __ballot_sync(0xffffffffu, x > lo && W.bin(x) <= b);
-    const int f = yes ? __ffs(yes) - 1 : 32;
+    const unsigned b = __ballot_sync(0xffffffffu, x > lo && yes(logit_of(x)));
+    const int f = b ? __ffs(b) - 1 : 32;
     const uint32_t nh = __shfl_sync(0xffffffffu, x, f & 31), nl = __shfl_sync(0xffffffffu, x, (f + 31) & 31);
     if (f < 32) hi = nh;
     if (f > 0) lo = nl;
   }
   return hi;
 }
-// 2^-44 weights as three 15-bit parts and a count in bins of the histogram: 32-bit sums hold
-// the 2^15 keys a CTA has at most.
-__device__ __forceinline__ void add_fine(Shared& sh, int i, unsigned long long w) {
-  atomicAdd(&sh.hist[i], 1u);
-  atomicAdd(&sh.hist[kFine + i], (uint32_t)w & 0x7fffu);
-  atomicAdd(&sh.hist[2 * kFine + i], (uint32_t)(w >> 15) & 0x7fffu);
-  atomicAdd(&sh.hist[3 * kFine + i], (uint32_t)(w >> 30));
-}
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) k_sample_rows(const RowsArgs sa) {
-  extern __shared__ __align__(16) uint32_t keys[];
-  __shared__ Shared sh;
-  __shared__ unsigned long long table[256];
+template <typename T, int THREADS>
+__global__ void __launch_bounds__(THREADS) k_sample_rows(const RowsArgs sa) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  Shared<THREADS>& sh = *reinterpret_cast<Shared<THREADS>*>(smem);
+  float* vals = reinterpret_cast<float*>(smem + (sizeof(Shared<THREADS>) + 15) / 16 * 16);
   const dmtp_sample_args& a = sa.a;
   unsigned size;
   asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(size));
-  Cluster cl{&sh, cluster_rank(), size, 0};
-  const int row = blockIdx.x / size, tid = threadIdx.x, lane = tid & 31;
-  const int V = a.vocab, slice = sa.slice, E = slice / kThreads;
+  Cluster<THREADS> cl{&sh, cluster_rank(), size, 0};
+  const int row = blockIdx.x / size, tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const int V = a.vocab, slice = sa.slice, E = slice / THREADS;
   const int base = (int)cl.rank * slice;
   const int mine = V > base ? min(slice, V - base) : 0;
   const T* lg = (const T*)a.logits + (int64_t)row * a.ld + base;
-  if (tid < 256) table[tid] = exp2_256th(tid);
-  for (int i = tid; i < kBins; i += kThreads) sh.hist[i] = 0;
-  uint32_t best = 0;
+  float best = kMasked;
   if (sa.vec) {
     constexpr int X = 16 / sizeof(T);
-    for (int i = tid * X; i < slice; i += kThreads * X) {
-      uint32_t k[X];
+#pragma unroll 4
+    for (int i = tid * X; i < slice; i += THREADS * X) {
+      float f[X];
       if (i + X <= mine) {
         const uint4 u = __ldcs(reinterpret_cast<const uint4*>(lg + i));
         const T* t = reinterpret_cast<const T*>(&u);
 #pragma unroll
-        for (int e = 0; e < X; ++e) k[e] = key_of(to_f32(t[e]));
+        for (int e = 0; e < X; ++e) f[e] = clean(to_f32(t[e]));
       } else {
 #pragma unroll
-        for (int e = 0; e < X; ++e) k[e] = i + e < mine ? key_of(to_f32(lg[i + e])) : kNone;
+        for (int e = 0; e < X; ++e) f[e] = i + e < mine ? clean(to_f32(lg[i + e])) : kMasked;
       }
 #pragma unroll
       for (int e = 0; e < X; e += 4)
-        *reinterpret_cast<uint4*>(keys + i + e) = make_uint4(k[e], k[e + 1], k[e + 2], k[e + 3]);
+        *reinterpret_cast<float4*>(vals + i + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
 #pragma unroll
-      for (int e = 0; e < X; ++e) best = max(best, k[e]);
+      for (int e = 0; e < X; ++e) best = fmaxf(best, f[e]);
     }
   } else {
-    for (int i = tid; i < slice; i += kThreads) {
-      const uint32_t k = i < mine ? key_of(to_f32(lg[i])) : kNone;
-      keys[i] = k;
-      best = max(best, k);
+#pragma unroll 4
+    for (int i = tid; i < slice; i += THREADS) {
+      const float f = i < mine ? clean(to_f32(lg[i])) : kMasked;
+      vals[i] = f;
+      best = fmaxf(best, f);
     }
   }
+  for (int i = tid; i < 256; i += THREADS) sh.table[i] = exp2_256th(i);
+  for (int i = tid; i < kBins; i += THREADS) sh.hist[i] = 0;
+  sh.extra[tid] = 0;
+  sh.extra_n[tid] = 0;
+  if (tid == 0) sh.listed = 0;
   const float temp = a.temperature ? __ldg(a.temperature + row) : 1.f;
   const int k = a.top_k ? __ldg(a.top_k + row) : 0;
   const float top_p = a.top_p ? __ldg(a.top_p + row) : 1.f;
   const float min_p = a.min_p ? __ldg(a.min_p + row) : 0.f;
   const float u = __ldg(a.u + row);
   cl.sync();  // every CTA of the cluster runs before one writes another's memory
-  const uint32_t top = (uint32_t)cl.max(best);
-  const bool greedy = !(temp > 0.f);
-  if (top == kNone || greedy) {
-    unsigned long long id = 0;  // of the largest logit, the lowest: 2^32 - 1 - id is maximal
-    for (int i = tid; i < mine; i += kThreads)
-      if (keys[i] == top && top != kNone) id = max(id, (unsigned long long)(0xffffffffu - (unsigned)(base + i)));
+  const uint32_t top = cl.max(key_of(best));
+  const bool none = top == key_of(kMasked);
+  if (none || !(temp > 0.f)) {
+    uint32_t id = 0;  // of the largest logit, the lowest: 2^32 - 1 - id is maximal
+    const float t = logit_of(top);
+    for (int i = tid; i < mine; i += THREADS)
+      if (vals[i] == t && !none) id = max(id, 0xffffffffu - (unsigned)(base + i));
     id = cl.max(id);
     if (cl.rank == 0 && tid == 0) {
-      a.ids[row] = top == kNone ? -1 : (int)(0xffffffffu - (unsigned)id);
-      if (a.kept) a.kept[row] = top == kNone ? 0 : 1;
+      a.ids[row] = none ? -1 : (int)(0xffffffffu - id);
+      if (a.kept) a.kept[row] = none ? 0 : 1;
     }
     cl.sync();  // no CTA leaves while another may still write its slots
     return;
   }
   Weigh W;
   W.top = logit_of(top);
-  W.table = table;
+  W.table = sh.table;
   // c = log2(e) / T as a pair
-  W.chi = 1.44269502162933349609f / temp;
-  W.clo = (fmaf(-W.chi, temp, 1.44269502162933349609f) + 1.92596299112661746887e-08f) / temp;
-  W.cb = fminf(W.chi * 32.f, 1e30f);
-  const uint2* own = reinterpret_cast<const uint2*>(keys + tid * E);  // this thread's ids, E even
-  const unsigned long long least =
-      min_p > 0.f ? (min_p < 1.f ? part_of(min_p, 1ull << kShift, true) : 1ull << kShift) : 0ull;
+  const float tt = fmaxf(temp, 1e-30f);
+  W.chi = 1.44269502162933349609f / tt;
+  W.clo = (fmaf(-W.chi, tt, 1.44269502162933349609f) + 1.92596299112661746887e-08f) / tt;
+  W.cb = W.chi * 32.f;
+  const float2* own = reinterpret_cast<const float2*>(vals + tid * E);  // this thread's ids, E even
   const bool by_p = top_p < 1.f;
-  // the smallest key that stays; `ties` of its keys stay, all of them unless `partial`
-  uint32_t cut = 1;
+  // the smallest logit that stays, as a key; `ties` of its ids stay, all of them unless `partial`
+  uint32_t cut = 0x00800000u;
   unsigned long long ties = 0;
   bool partial = false;
-  int last_bin = kBins - 1;          // the last bin that top-k leaves
-  unsigned long long last_n = ~0ull; // and how many of its keys
+  bool by_k = false;
 
   if (k > 0 || by_p) {
     // the two end bins, where flat rows and masked logits crowd, are counted by thread
     uint32_t ends[2] = {0, 0};
+#pragma unroll 2
     for (int i = 0; i < E / 2; ++i) {
-      const uint2 xy = own[i];
+      const float2 xy = own[i];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const uint32_t x = e ? xy.y : xy.x;
-        if (x == kNone) continue;
+        const float x = e ? xy.y : xy.x;
         const int b = W.bin(x);
-        if (b == 0)
-          ++ends[0];
-        else if (b == kBins - 1)
-          ++ends[1];
-        else
+        if (b > 0 && b < kBins - 1)
           atomicAdd(&sh.hist[b], 1u);
+        else if (b == 0)
+          ++ends[0];
+        else
+          ends[1] += x > kMasked;
       }
     }
     ends[0] = __reduce_add_sync(0xffffffffu, ends[0]);
     ends[1] = __reduce_add_sync(0xffffffffu, ends[1]);
     if (lane == 0 && ends[0]) atomicAdd(&sh.hist[0], ends[0]);
     if (lane == 1 && ends[1]) atomicAdd(&sh.hist[kBins - 1], ends[1]);
-    reduce_hist(cl, sh);
-    unsigned long long n = 0, nvalid;
-    for (int i = tid; i < kBins; i += kThreads) n += sh.coarse[i] = sh.all[i];
-    block_scan(sh, n, nvalid);
-    if (k > 0 && (unsigned long long)k < nvalid) {
-      unsigned long long before, cnt, want = k;
-      find_count(sh, want, last_bin, before, cnt);
+    cl.sum_hist();
+    unsigned long long n = 0, nvalid, before, cnt, want = k;
+    for (int i = tid; i < kBins; i += THREADS) n += sh.all[i];
+    cl.scan(n, nvalid);
+    by_k = k > 0 && (unsigned long long)k < nvalid;
+    int last_bin = kBins - 1;           // the last bin that top-k leaves
+    unsigned long long last_n = ~0ull;  // and how many of its logits
+    if (by_k) {
+      cl.find_count(want, last_bin, before, cnt);
       want -= before;
       last_n = want;
-      uint32_t lo = first_key(W, top, last_bin), hi = last_bin ? first_key(W, top, last_bin - 1) - 1 : top;
-      while (want != cnt && lo != hi) {
-        const int sh_ = max(0, 32 - __clz((int)(hi - lo)) - 11);
-        for (int i = 0; i < E / 2; ++i) {
-          const uint2 x = own[i];
-          if (x.x >= lo && x.x <= hi) atomicAdd(&sh.hist[hi - x.x >> sh_], 1u);
-          if (x.y >= lo && x.y <= hi) atomicAdd(&sh.hist[hi - x.y >> sh_], 1u);
-        }
-        reduce_hist(cl, sh);
-        int f;
-        find_count(sh, want, f, before, cnt);
-        want -= before;
-        hi -= (uint32_t)f << sh_;
-        lo = hi - lo < (1u << sh_) ? lo : hi - ((1u << sh_) - 1);
-      }
-      cut = lo;
-      partial = want != cnt;
-      ties = want;
     }
-  }
-
-  unsigned long long mass = 0, cnt = 0;  // of this thread's kept keys, so far those above `from`
-  uint32_t from = 0xffffffffu;
-  const unsigned long long tie_mass = partial ? ties * W(cut) : 0ull;
-  if (by_p) {
-    // the neighbourhood of the cut: bins whose running weight is about top_p of all
-    constexpr int BE = kBins / kThreads;
-    {
+    if (by_p) {
+      // the neighbourhood of top-p's cut: bins whose running weight is about top_p of all
+      constexpr int BE = kBins / THREADS;
       float m[BE], sum = 0.f;
 #pragma unroll
       for (int e = 0; e < BE; ++e) {
         const int i = tid * BE + e;
-        const unsigned long long n = sh.coarse[i];
-        m[e] = i < last_bin ? (float)n : i == last_bin ? (float)(n < last_n ? n : last_n) : 0.f;
+        const unsigned long long c = sh.all[i];
+        m[e] = i < last_bin ? (float)c : i == last_bin ? (float)(c < last_n ? c : last_n) : 0.f;
         m[e] *= ex2(-(float)i * 0.03125f);
         sum += m[e];
       }
-      unsigned long long total;  // (in 2^-24: order does not matter)
-      unsigned long long at = block_scan(sh, (unsigned long long)(sum * 16777216.f), total);
-      if (tid == 0) sh.bins[0] = last_bin, sh.bins[1] = last_bin;
-      __syncthreads();
+      if (tid == 0) sh.bins[0] = sh.bins[1] = last_bin;
+      unsigned long long total;  // in 2^-24
+      const unsigned long long at = cl.scan((unsigned long long)(sum * 16777216.f), total);
       // a weight taken at its bin's centre is off by 1.1% at most, 0.6% in the mean square,
       // and the errors of the many weights of a flat row average out
       const float p = fmaxf(top_p, 0.f) * (float)total;
@@ -446,27 +434,84 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample_rows(const RowsArgs sa) 
       if (hi_b <= last_bin) atomicMin(&sh.bins[1], hi_b);
       __syncthreads();
     }
-    uint32_t hi = sh.bins[0] ? first_key(W, top, sh.bins[0] - 1) - 1 : top;
+    if (by_k) {
+      if (wid < 2) {
+        const int b = wid ? last_bin - 1 : last_bin;
+        const uint32_t f = b < 0 ? top + 1 : first_key(top, [&](float x) { return W.bin(x) <= b; });
+        if (lane == 0) sh.edge[wid] = wid ? f - 1 : f;
+      }
+      __syncthreads();
+      uint32_t lo = sh.edge[0], hi = sh.edge[1];
+      while (want != cnt && lo != hi) {
+        const int shift = max(0, 32 - __clz((int)(hi - lo)) - 11);
+        const float lf = logit_of(lo), hf = logit_of(hi);
+        for (int i = 0; i < E / 2; ++i) {
+          const float2 x = own[i];
+          if (x.x >= lf && x.x <= hf) atomicAdd(&sh.hist[hi - key_of(x.x) >> shift], 1u);
+          if (x.y >= lf && x.y <= hf) atomicAdd(&sh.hist[hi - key_of(x.y) >> shift], 1u);
+        }
+        cl.sum_hist();
+        int f;
+        cl.find_count(want, f, before, cnt);
+        want -= before;
+        hi -= (uint32_t)f << shift;
+        lo = hi - lo < (1u << shift) ? lo : hi - ((1u << shift) - 1);
+      }
+      cut = lo;
+      partial = want != cnt;
+      ties = want;
+    }
+  }
+  const unsigned long long tie_mass = partial ? ties * W(logit_of(cut)) : 0ull;
+  // min_p as a key
+  uint32_t min_key = 0;
+  if (min_p > 0.f && wid == 0) {
+    const unsigned long long least = min_p < 1.f ? part_of(min_p, 1ull << kShift, true) : 1ull << kShift;
+    const uint32_t f = first_key(top, [&](float x) { return W(x) >= least; });
+    if (lane == 0) sh.edge[2] = f;
+  }
+
+  unsigned long long mass = 0;  // of this thread's kept logits, so far of those above `from`
+  uint32_t cnt = 0, from = 0xffffffffu;
+  bool listed = false;          // the others are in the list
+  if (by_p) {
+    {
+      if (wid < 2) {
+        const int b = wid ? sh.bins[0] - 1 : sh.bins[1];
+        const uint32_t f = b < 0 ? top + 1 : first_key(top, [&](float x) { return W.bin(x) <= b; });
+        if (lane == 0) sh.edge[wid] = wid ? f - 1 : f;
+      }
+      __syncthreads();
+    }
+    if (min_p > 0.f) min_key = sh.edge[2];
     const uint32_t least_key = partial ? cut + 1 : cut;  // below it, only the cut's own ties
-    uint32_t lo = max(first_key(W, top, sh.bins[1]), least_key);
-    if (hi < lo) hi = lo;
+    uint32_t lo = max(sh.edge[0], least_key), hi = max(sh.edge[1], lo);
     // every weight once: all, above the neighbourhood, and inside it by finer bins
     unsigned long long sum = 0, above = 0;
     int shift = max(0, 32 - __clz((int)(hi - lo)) - 9);
     from = hi;
-    for (int i = 0; i < E / 2; ++i) {
-      const uint2 xy = own[i];
+    listed = true;
+    {
+      const float lf = logit_of(lo), hf = logit_of(hi), cf = logit_of(least_key);
+      const float mf = logit_of(max(min_key, 0x007fffffu));
+#pragma unroll 1
+      for (int i = 0; i < E / 2; ++i) {
+        const float2 xy = own[i];
+        if (by_k && !(fmaxf(xy.x, xy.y) >= cf)) continue;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const uint32_t x = e ? xy.y : xy.x;
-        if (x < cut || (partial && x == cut)) continue;
-        const unsigned long long w = W(x);
-        sum += w;
-        if (x > hi) {
-          above += w;
-          if (w >= least) mass += w, ++cnt;
-        } else if (x >= lo) {
-          add_fine(sh, hi - x >> shift, w);
+        for (int e = 0; e < 2; ++e) {
+          const float x = e ? xy.y : xy.x;
+          unsigned long long w = W(x);
+          if (by_k && !(x >= cf)) w = 0;
+          sum += w;
+          if (x > hf) {
+            above += w;
+            if (x >= mf) mass += w, ++cnt;
+          } else if (x >= lf) {
+            cl.add_fine(hi - key_of(x) >> shift, w);
+            const unsigned at = atomicAdd(&sh.listed, 1u);
+            if (at < kList) sh.list[at] = x, sh.where[at] = (uint16_t)(tid * E + 2 * i + e);
+          }
         }
       }
     }
@@ -474,31 +519,43 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample_rows(const RowsArgs sa) 
     sum += tie_mass;
     unsigned long long goal = part_of(fmaxf(top_p, 0.f), sum, true);
     goal = goal ? goal : 1ull;
-    // the first key from above at which the running weight reaches the goal
+    // the first logit from above at which the running weight reaches the goal
     while (true) {
-      reduce_hist(cl, sh);
-      const uint32_t n = sh.all[tid];
-      const unsigned long long m = (unsigned long long)sh.all[kFine + tid] +
-                                   ((unsigned long long)sh.all[2 * kFine + tid] << 15) +
-                                   ((unsigned long long)sh.all[3 * kFine + tid] << 30);
-      unsigned long long total;
-      const unsigned long long at = above + block_scan(sh, m, total);
-      if (at < goal && goal <= at + m) sh.found[0] = tid, sh.found[1] = at, sh.found[2] = n, sh.found[3] = m;
+      cl.sum_hist();
+      constexpr int FE = kFine / THREADS > 1 ? kFine / THREADS : 1;
+      unsigned long long m[FE], mine_m = 0, total;
+#pragma unroll
+      for (int e = 0; e < FE; ++e) {
+        const int i = tid * FE + e;
+        m[e] = i < kFine ? (unsigned long long)sh.all[kFine + i] + ((unsigned long long)sh.all[2 * kFine + i] << 15) +
+                               ((unsigned long long)sh.all[3 * kFine + i] << 30)
+                         : 0ull;
+        mine_m += m[e];
+      }
+      unsigned long long at = above + cl.scan(mine_m, total);
+#pragma unroll
+      for (int e = 0; e < FE; ++e) {
+        if (at < goal && goal <= at + m[e])
+          sh.found[0] = tid * FE + e, sh.found[1] = at, sh.found[2] = sh.all[tid * FE + e], sh.found[3] = m[e];
+        at += m[e];
+      }
       __syncthreads();
       if (above >= goal) {  // the goal lies above this range
         lo = hi + 1;
         hi = top;
         above = 0;
+        listed = false;
       } else if (above + total < goal) {  // or below it
         above += total;
         if (lo <= least_key) {  // only the cut's own ties are left
-          const unsigned long long wc = W(cut);
+          const unsigned long long wc = W(logit_of(cut));
           const unsigned long long need = wc ? (goal - above + wc - 1) / wc : ties;
           ties = need < ties ? need : ties;
           break;
         }
         hi = lo - 1;
         lo = least_key;
+        listed = false;
       } else {
         const int f = (int)sh.found[0];
         above = sh.found[1];
@@ -516,50 +573,77 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample_rows(const RowsArgs sa) 
       }
       shift = max(0, 32 - __clz((int)(hi - lo)) - 9);
       __syncthreads();  // found has been read, the histogram cleared
-      for (int i = 0; i < E / 2; ++i) {
-        const uint2 xy = own[i];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint32_t x = e ? xy.y : xy.x;
-          if (x >= lo && x <= hi) add_fine(sh, hi - x >> shift, W(x));
+      const float lf = logit_of(lo), hf = logit_of(hi);
+      if (listed && sh.listed <= kList) {
+        for (unsigned i = tid; i < sh.listed; i += THREADS) {
+          const float x = sh.list[i];
+          if (x >= lf && x <= hf) cl.add_fine(hi - key_of(x) >> shift, W(x));
+        }
+      } else {
+        for (int i = 0; i < E / 2; ++i) {
+          const float2 xy = own[i];
+          if (xy.x >= lf && xy.x <= hf) cl.add_fine(hi - key_of(xy.x) >> shift, W(xy.x));
+          if (xy.y >= lf && xy.y <= hf) cl.add_fine(hi - key_of(xy.y) >> shift, W(xy.y));
         }
       }
     }
-    if (cut > from) {  // the cut came out above the first neighbourhood: count again
+    if (!listed) {  // the cut came out elsewhere: count again
       from = 0xffffffffu;
-      mass = cnt = 0;
+      mass = 0;
+      cnt = 0;
     }
+    listed = listed && !partial && sh.listed <= kList;
+  } else if (min_p > 0.f) {
+    __syncthreads();
+    min_key = sh.edge[2];
+  }
+  if (min_key > cut) {  // min_p cuts deeper
+    cut = min_key;
+    partial = false;
   }
 
   // ranks of the cut's ties in order of id
+  const float cf = logit_of(cut), ff = logit_of(min(from, top));
   unsigned long long rank = 0;
   if (partial) {
     unsigned long long n = 0, total;
-    for (int i = 0; i < E; ++i) n += keys[tid * E + i] == cut;
-    rank = block_scan(sh, n, total);
+    for (int i = 0; i < E; ++i) n += vals[tid * E + i] == cf;
+    rank = cl.scan(n, total);
     const int p = cl.exchange(total, 0);
     for (unsigned r = 0; r < cl.rank; ++r) rank += sh.slot[p][r][0];
   }
-  {
+  if (listed) {
+    for (unsigned i = tid; i < sh.listed; i += THREADS) {
+      const float x = sh.list[i];
+      if (x >= cf) {
+        const int t = sh.where[i] / E;
+        atomicAdd(&sh.extra[t], W(x));
+        atomicAdd(&sh.extra_n[t], 1u);
+      }
+    }
+    __syncthreads();
+    mass += sh.extra[tid];
+    cnt += sh.extra_n[tid];
+  } else if (cut <= from) {
     unsigned long long r = rank;
+#pragma unroll 1
     for (int i = 0; i < E / 2; ++i) {
-      const uint2 xy = own[i];
+      const float2 xy = own[i];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const uint32_t x = e ? xy.y : xy.x;
-        if (x < cut || x > from) continue;
-        if (partial && x == cut && r++ >= ties) continue;
-        const unsigned long long w = W(x);
-        if (w >= least) mass += w, ++cnt;
+        const float x = e ? xy.y : xy.x;
+        if (!(x >= cf && x <= ff)) continue;
+        if (partial && x == cf && r++ >= ties) continue;
+        mass += W(x);
+        ++cnt;
       }
     }
   }
   // the pick: the thread whose ids hold it, then its ids by a warp
-  unsigned long long total, kept, in_cta;
-  unsigned long long before = block_scan(sh, mass, in_cta);
+  unsigned long long total, kept, in_cta, n_cta;
+  unsigned long long before = cl.scan(mass, in_cta);
+  cl.scan(cnt, n_cta);
   {
-    unsigned long long n_cta;
-    block_scan(sh, cnt, n_cta);
     const int p = cl.exchange(in_cta, n_cta);
     total = kept = 0;
     for (unsigned r = 0; r < size; ++r) {
@@ -577,15 +661,11 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample_rows(const RowsArgs sa) 
     const int first = (tid - lane + t) * E;
     for (int i0 = 0; i0 < E; i0 += 32) {
       const int i = i0 + lane;
-      const uint32_t x = i < E ? keys[first + i] : kNone;
-      const unsigned tie = __ballot_sync(0xffffffffu, x == cut);
+      const float x = i < E ? vals[first + i] : kMasked;
+      const unsigned tie = __ballot_sync(0xffffffffu, x == cf);
       const unsigned long long my = r + __popc(tie & ((1u << lane) - 1));
       r += __popc(tie);
-      unsigned long long w = 0;
-      if (x >= cut && !(partial && x == cut && my >= ties)) {
-        w = W(x);
-        if (w < least) w = 0;
-      }
+      const unsigned long long w = x >= cf && !(partial && x == cf && my >= ties) ? W(x) : 0ull;
       unsigned long long inc = w;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -609,13 +689,31 @@ using namespace dmtp;
 
 namespace {
 
-template <typename T>
-cudaError_t launch(const RowsArgs& s, unsigned cluster, cudaStream_t st) {
+template <typename T, int THREADS>
+cudaError_t launch(const dmtp_sample_args& a, unsigned cluster, cudaStream_t st) {
   static unsigned long long done = 0;
-  auto k = k_sample_rows<T>;
-  const int most = 2 * 33 * kThreads * 4;  // of the largest vocabulary
+  auto k = k_sample_rows<T, THREADS>;
+  constexpr int kFixed = (sizeof(Shared<THREADS>) + 15) / 16 * 16;
+  // a thread's ids: an odd number of pairs, so that the threads' pairs lie in different banks
+  auto pairs_of = [](int n) {
+    const int p = (n + 2 * THREADS - 1) / (2 * THREADS);
+    return p + 1 - p % 2;
+  };
+  const int most = kFixed + 2 * pairs_of(DMTP_OPS_MAX_SAMPLE_VOCAB / 8) * THREADS * 4;
   if (!smem_limit((const void*)k, most, &done)) return cudaErrorInvalidValue;
-  return launch_op(k, (unsigned)s.a.rows * cluster, kThreads, (size_t)s.slice * 4, st, false, cluster, s);
+  RowsArgs s;
+  s.a = a;
+  s.slice = 2 * pairs_of((a.vocab + (int)cluster - 1) / (int)cluster) * THREADS;
+  const int es = sizeof(T);
+  s.vec = aligned_to(a.logits, 16) && mult(a.ld * es, 16);
+  return launch_op(k, (unsigned)a.rows * cluster, THREADS, (size_t)(kFixed + s.slice * 4), st, false, cluster, s);
+}
+template <typename T>
+cudaError_t launch_t(const dmtp_sample_args& a, cudaStream_t st) {
+  const unsigned cluster = a.vocab > 8192 ? 8 : a.vocab > 2048 ? 2 : 1;
+  // rows that one wave of the GPU holds: more threads finish a row sooner; more rows: fewer
+  // threads spend less on what every thread does once
+  return (int64_t)a.rows * cluster <= 304 ? launch<T, 512>(a, cluster, st) : launch<T, 256>(a, cluster, st);
 }
 
 }  // namespace
@@ -626,22 +724,11 @@ extern "C" int dmtp_sample_rows(const dmtp_sample_args* a, void* stream) {
   if (!a->logits || !a->u || !a->ids || (a->dtype != 0 && a->dtype != 1) || a->vocab < 1 ||
       a->vocab > DMTP_OPS_MAX_SAMPLE_VOCAB || a->ld < a->vocab || a->rows > (1 << 24))
     return DMTP_EINVAL;
-  const int es = a->dtype ? 2 : 4;
-  if (!aligned_to(a->logits, es)) return DMTP_EINVAL;
+  if (!aligned_to(a->logits, a->dtype ? 2 : 4)) return DMTP_EINVAL;
   const void* words[] = {a->u, a->temperature, a->top_k, a->top_p, a->min_p, a->ids, a->kept};
   for (const void* p : words)
     if (!aligned_to(p, 4)) return DMTP_EINVAL;
   if (cudaPeekAtLastError() != cudaSuccess) return DMTP_ECUDA;
-  RowsArgs s;
-  s.a = *a;
-  const unsigned cluster = a->vocab > 8192 ? 8 : a->vocab > 2048 ? 2 : 1;
-  const int per = (a->vocab + (int)cluster - 1) / (int)cluster;
-  // a thread's ids: an odd number of pairs, so that the threads' pairs lie in different banks
-  int pairs = (per + 2 * kThreads - 1) / (2 * kThreads);
-  pairs += 1 - pairs % 2;
-  s.slice = 2 * pairs * kThreads;
-  s.vec = aligned_to(a->logits, 16) && mult(a->ld * es, 16);
-  const cudaError_t e = a->dtype ? launch<bf16>(s, cluster, (cudaStream_t)stream)
-                                 : launch<float>(s, cluster, (cudaStream_t)stream);
+  const cudaError_t e = a->dtype ? launch_t<bf16>(*a, (cudaStream_t)stream) : launch_t<float>(*a, (cudaStream_t)stream);
   return e == cudaSuccess ? DMTP_OK : (cudaGetLastError(), DMTP_ECUDA);
 }

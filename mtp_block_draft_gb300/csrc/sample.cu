@@ -12,7 +12,7 @@
 // is formed as a pair of floats (the difference, the factor and their product with their
 // rounding errors); 2^y = 2^n 2^(j/256) 2^r with a table of 2^(j/256) in 62-bit fixed point and
 // 2^r - 1 as a series to r^4 (|r| < 2^-9, the next term is 2^-54). The error of a weight is
-// about 2^-39 of it and half a step.
+// about 2^-39 of it and a step.
 //
 // Filters. The cut is a key and, among its ties, how many of the lowest ids stay. Keys fall
 // into bins of 1/32 octave of weight; the bin in which the count from above reaches top_k is
@@ -82,7 +82,36 @@ __device__ __forceinline__ unsigned long long part_of(float f, unsigned long lon
 }
 
 constexpr int kShift = 44;  // weight 1 is 2^44: 2^18 of them stay below 2^63
-constexpr int kBins = 2048, kFine = 512, kList = 1024;
+constexpr int kBins = 2048, kFine = 512;
+
+// Two floats in one register pair: Blackwell's packed single-precision instructions.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pack(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack(f32x2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f32x2 both(float a) { return pack(a, a); }
 
 struct Weigh {
   float top, chi, clo, cb;
@@ -94,29 +123,42 @@ struct Weigh {
     const float x = fminf((top - l) * cb, (float)(kBins - 1));
     return (int)(__float_as_uint(x + 8388608.f) & (kBins - 1));
   }
-  __device__ __forceinline__ unsigned long long operator()(float l) const {
-    const float d = l - top, t = d - l;
-    const float e = (l - (d - t)) + (-top - t);
-    const float hi = d * chi;
-    if (!(hi > -45.f)) return 0ull;  // below half a step, or masked
-    const float lo = fmaf(e, chi, fmaf(d, clo, fmaf(d, chi, -hi)));
-    // (adding 1.5 2^k rounds to steps of 2^(k - 23) and leaves the step count in the low bits)
-    const float jt = hi + 49152.f;
-    const int j = __float_as_int(jt) - __float_as_int(49152.f);
-    const float s = hi - (jt - 49152.f);  // exact, |s| <= 2^-9
-    const float h = s * 0.693147182464599609f;
-    float g = fmaf(s, 0.693147182464599609f, -h);
-    g = fmaf(s, -1.90465429995776804525e-09f, fmaf(lo, 0.693147182464599609f, g));
-    const float r = s + lo;
-    g = fmaf(r * r, fmaf(r, fmaf(r, 9.618129107628477e-3f, 5.550410866482158e-2f), 0.24022650695910072f), g);
-    const float a = h + 5.859375e-3f;  // 1.5 2^-8 (|h| < 2^-9): steps of 2^-31
-    const float b = (h - (a - 5.859375e-3f)) + g + 1.1444091796875e-5f;  // 1.5 2^-17: 2^-40
-    const int q = (__float_as_int(a) - __float_as_int(5.859375e-3f)) * 512 +
-                  (__float_as_int(b) - __float_as_int(1.1444091796875e-5f));  // 2^r - 1 in 2^-40
+  // The weight from the exponent's whole and 256th part (jt, in the low bits of a sum with
+  // 1.5 2^15), and 2^r - 1 in steps of 2^-31 (a) and 2^-40 (b), kept likewise. Steps of 2^-44,
+  // rounded down: 2^18 of them lose 2^-27 of the largest weight at most.
+  __device__ __forceinline__ unsigned long long scaled(float hi, float jt, float a, float b) const {
+    const int j = __float_as_int(jt) - 0x47400000;
+    const int q = __float_as_int(a) * 512 + __float_as_int(b) - (int)(0x3bc00000u * 512u + 0x37400000u);
     const unsigned long long t62 = table[j & 255];
     const unsigned long long w = t62 + (unsigned long long)((long long)(int)(t62 >> 32) * q >> 8);
-    const int down = 62 - kShift - (j >> 8);  // 18 .. 63
-    return (w + (1ull << (down - 1))) >> down;
+    return hi > -45.f ? w >> (62 - kShift - (j >> 8)) : 0ull;  // (below: under half a step, or masked)
+  }
+  // The weights of two logits.
+  __device__ __forceinline__ void two(float2 l, unsigned long long& wx, unsigned long long& wy) const {
+    const f32x2 one = both(-1.f), x = pack(l.x, l.y), c = both(chi), nc = both(-chi), ntop = both(-top);
+    const f32x2 d = add2(x, ntop), t = fma2(x, one, d);           // l - top and what it lost, e
+    const f32x2 e = add2(fma2(fma2(t, one, d), one, x), fma2(t, one, ntop));
+    const f32x2 hi = mul2(d, c);                                  // the exponent, hi + lo; nlo = -lo
+    const f32x2 nlo = fma2(e, nc, fma2(d, both(-clo), fma2(d, nc, hi)));
+    // (adding 1.5 2^k rounds to steps of 2^(k - 23) and leaves the step count in the low bits)
+    const f32x2 jt = add2(hi, both(49152.f));
+    const f32x2 s = fma2(add2(jt, both(-49152.f)), one, hi);      // exact, |s| <= 2^-9
+    const f32x2 h = mul2(s, both(0.693147182464599609f));         // (s + lo) ln 2 = h - g so far
+    f32x2 g = fma2(s, both(-0.693147182464599609f), h);
+    g = fma2(s, both(1.90465429995776804525e-09f), fma2(nlo, both(0.693147182464599609f), g));
+    const f32x2 r = fma2(nlo, one, s);
+    g = fma2(mul2(r, r), fma2(r, fma2(r, both(-9.618129107628477e-3f), both(-5.550410866482158e-2f)),
+                              both(-0.24022650695910072f)), g);   // 2^(s + lo) - 1 = h - g
+    const f32x2 a = add2(h, both(5.859375e-3f));                  // 1.5 2^-8 (|h| < 2^-9): steps of 2^-31
+    const f32x2 b = add2(fma2(g, one, fma2(add2(a, both(-5.859375e-3f)), one, h)), both(1.1444091796875e-5f));
+    const float2 h2 = unpack(hi), j2 = unpack(jt), a2 = unpack(a), b2 = unpack(b);  // b: 1.5 2^-17
+    wx = scaled(h2.x, j2.x, a2.x, b2.x);
+    wy = scaled(h2.y, j2.y, a2.y, b2.y);
+  }
+  __device__ __forceinline__ unsigned long long operator()(float l) const {
+    unsigned long long wx, wy;
+    two(make_float2(l, l), wx, wy);
+    return wx;
   }
 };
 
@@ -127,11 +169,8 @@ struct Shared {
   unsigned long long slot[2][16][2];  // one pair of each CTA of the cluster, twice
   unsigned long long warp[kWarps][2];
   unsigned long long found[4];
-  unsigned long long extra[THREADS];  // kept weight that the list gives a thread
-  uint32_t extra_n[THREADS];
-  float list[kList];                  // the neighbourhood's logits of this CTA, and where they are
-  uint16_t where[kList];
-  unsigned listed;
+  static constexpr int kSlots = 4096 / THREADS;
+  uint8_t list[kSlots][THREADS];      // where a thread's ids in the neighbourhood are
   uint32_t edge[3];
   int bins[2];
   unsigned long long table[256];
@@ -287,8 +326,9 @@ __device__ __forceinline__ uint32_t first_key(uint32_t top, F yes) {
 template <typename T, int THREADS>
 __global__ void __launch_bounds__(THREADS) k_sample_rows(const RowsArgs sa) {
   extern __shared__ __align__(16) unsigned char smem[];
-  Shared<THREADS>& sh = *reinterpret_cast<Shared<THREADS>*>(smem);
-  float* vals = reinterpret_cast<float*>(smem + (sizeof(Shared<THREADS>) + 15) / 16 * 16);
+  using Sh = Shared<THREADS>;
+  Sh& sh = *reinterpret_cast<Sh*>(smem);
+  float* vals = reinterpret_cast<float*>(smem + (sizeof(Sh) + 15) / 16 * 16);
   const dmtp_sample_args& a = sa.a;
   unsigned size;
   asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(size));
@@ -329,9 +369,6 @@ __global__ void __launch_bounds__(THREADS) k_sample_rows(const RowsArgs sa) {
   }
   for (int i = tid; i < 256; i += THREADS) sh.table[i] = exp2_256th(i);
   for (int i = tid; i < kBins; i += THREADS) sh.hist[i] = 0;
-  sh.extra[tid] = 0;
-  sh.extra_n[tid] = 0;
-  if (tid == 0) sh.listed = 0;
   const float temp = a.temperature ? __ldg(a.temperature + row) : 1.f;
   const int k = a.top_k ? __ldg(a.top_k + row) : 0;
   const float top_p = a.top_p ? __ldg(a.top_p + row) : 1.f;
@@ -421,7 +458,7 @@ __global__ void __launch_bounds__(THREADS) k_sample_rows(const RowsArgs sa) {
       // a weight taken at its bin's centre is off by 1.1% at most, 0.6% in the mean square,
       // and the errors of the many weights of a flat row average out
       const float p = fmaxf(top_p, 0.f) * (float)total;
-      const float wide = fminf(0.023f, 0.001f + 0.03f * rsqrtf((float)total * 5.9604645e-8f));
+      const float wide = fminf(0.023f, 0.0005f + 0.025f * rsqrtf((float)total * 5.9604645e-8f));
       float run = (float)at;
       int lo_b = kBins, hi_b = kBins;
 #pragma unroll
@@ -473,7 +510,7 @@ __global__ void __launch_bounds__(THREADS) k_sample_rows(const RowsArgs sa) {
 
   unsigned long long mass = 0;  // of this thread's kept logits, so far of those above `from`
   uint32_t cnt = 0, from = 0xffffffffu;
-  bool listed = false;          // the others are in the list
+  int listed = -1;              // >= 0: the others are in this thread's list, so many
   if (by_p) {
     {
       if (wid < 2) {
@@ -490,28 +527,40 @@ __global__ void __launch_bounds__(THREADS) k_sample_rows(const RowsArgs sa) {
     unsigned long long sum = 0, above = 0;
     int shift = max(0, 32 - __clz((int)(hi - lo)) - 9);
     from = hi;
-    listed = true;
+    listed = 0;
     {
       const float lf = logit_of(lo), hf = logit_of(hi), cf = logit_of(least_key);
-      const float mf = logit_of(max(min_key, 0x007fffffu));
-#pragma unroll 1
+      const bool deep = min_key > hi + 1;  // min_p cuts above the neighbourhood
+      const float mf = logit_of(deep ? min_key : hi + 1);
+#pragma unroll 2
       for (int i = 0; i < E / 2; ++i) {
         const float2 xy = own[i];
         if (by_k && !(fmaxf(xy.x, xy.y) >= cf)) continue;
+        unsigned long long w2[2];
+        W.two(xy, w2[0], w2[1]);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float x = e ? xy.y : xy.x;
-          unsigned long long w = W(x);
-          if (by_k && !(x >= cf)) w = 0;
+          const unsigned long long w = by_k && !(x >= cf) ? 0ull : w2[e];
           sum += w;
-          if (x > hf) {
-            above += w;
-            if (x >= mf) mass += w, ++cnt;
-          } else if (x >= lf) {
-            cl.add_fine(hi - key_of(x) >> shift, w);
-            const unsigned at = atomicAdd(&sh.listed, 1u);
-            if (at < kList) sh.list[at] = x, sh.where[at] = (uint16_t)(tid * E + 2 * i + e);
+          if (x >= mf) mass += w, ++cnt;
+          if (deep && x > hf) above += w;
+          if (x >= lf && x <= hf) {
+            if (listed < Sh::kSlots) sh.list[listed][tid] = (uint8_t)(2 * i + e);
+            ++listed;
           }
+        }
+      }
+      if (!deep) above = mass;
+      if (listed <= Sh::kSlots) {
+        for (int i = 0; i < listed; ++i) {
+          const float x = vals[tid * E + sh.list[i][tid]];
+          cl.add_fine(hi - key_of(x) >> shift, W(x));
+        }
+      } else {
+        for (int i = 0; i < E; ++i) {
+          const float x = vals[tid * E + i];
+          if (x >= lf && x <= hf) cl.add_fine(hi - key_of(x) >> shift, W(x));
         }
       }
     }
@@ -520,6 +569,7 @@ __global__ void __launch_bounds__(THREADS) k_sample_rows(const RowsArgs sa) {
     unsigned long long goal = part_of(fmaxf(top_p, 0.f), sum, true);
     goal = goal ? goal : 1ull;
     // the first logit from above at which the running weight reaches the goal
+    bool moved = false;  // out of the neighbourhood
     while (true) {
       cl.sum_hist();
       constexpr int FE = kFine / THREADS > 1 ? kFine / THREADS : 1;
@@ -544,7 +594,7 @@ __global__ void __launch_bounds__(THREADS) k_sample_rows(const RowsArgs sa) {
         lo = hi + 1;
         hi = top;
         above = 0;
-        listed = false;
+        moved = true;
       } else if (above + total < goal) {  // or below it
         above += total;
         if (lo <= least_key) {  // only the cut's own ties are left
@@ -555,7 +605,7 @@ __global__ void __launch_bounds__(THREADS) k_sample_rows(const RowsArgs sa) {
         }
         hi = lo - 1;
         lo = least_key;
-        listed = false;
+        moved = true;
       } else {
         const int f = (int)sh.found[0];
         above = sh.found[1];
@@ -574,9 +624,9 @@ __global__ void __launch_bounds__(THREADS) k_sample_rows(const RowsArgs sa) {
       shift = max(0, 32 - __clz((int)(hi - lo)) - 9);
       __syncthreads();  // found has been read, the histogram cleared
       const float lf = logit_of(lo), hf = logit_of(hi);
-      if (listed && sh.listed <= kList) {
-        for (unsigned i = tid; i < sh.listed; i += THREADS) {
-          const float x = sh.list[i];
+      if (!moved && listed <= Sh::kSlots) {
+        for (int i = 0; i < listed; ++i) {
+          const float x = vals[tid * E + sh.list[i][tid]];
           if (x >= lf && x <= hf) cl.add_fine(hi - key_of(x) >> shift, W(x));
         }
       } else {
@@ -587,12 +637,12 @@ __global__ void __launch_bounds__(THREADS) k_sample_rows(const RowsArgs sa) {
         }
       }
     }
-    if (!listed) {  // the cut came out elsewhere: count again
+    if (moved) {  // the cut came out elsewhere: count again
       from = 0xffffffffu;
       mass = 0;
       cnt = 0;
     }
-    listed = listed && !partial && sh.listed <= kList;
+    if (moved || partial || listed > Sh::kSlots) listed = -1;
   } else if (min_p > 0.f) {
     __syncthreads();
     min_key = sh.edge[2];
@@ -612,29 +662,25 @@ __global__ void __launch_bounds__(THREADS) k_sample_rows(const RowsArgs sa) {
     const int p = cl.exchange(total, 0);
     for (unsigned r = 0; r < cl.rank; ++r) rank += sh.slot[p][r][0];
   }
-  if (listed) {
-    for (unsigned i = tid; i < sh.listed; i += THREADS) {
-      const float x = sh.list[i];
-      if (x >= cf) {
-        const int t = sh.where[i] / E;
-        atomicAdd(&sh.extra[t], W(x));
-        atomicAdd(&sh.extra_n[t], 1u);
-      }
+  if (listed >= 0) {
+    for (int i = 0; i < listed; ++i) {
+      const float x = vals[tid * E + sh.list[i][tid]];
+      if (x >= cf) mass += W(x), ++cnt;
     }
-    __syncthreads();
-    mass += sh.extra[tid];
-    cnt += sh.extra_n[tid];
   } else if (cut <= from) {
     unsigned long long r = rank;
 #pragma unroll 1
     for (int i = 0; i < E / 2; ++i) {
       const float2 xy = own[i];
+      if (!(fmaxf(xy.x, xy.y) >= cf)) continue;
+      unsigned long long w2[2];
+      W.two(xy, w2[0], w2[1]);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const float x = e ? xy.y : xy.x;
         if (!(x >= cf && x <= ff)) continue;
         if (partial && x == cf && r++ >= ties) continue;
-        mass += W(x);
+        mass += w2[e];
         ++cnt;
       }
     }
@@ -711,9 +757,7 @@ cudaError_t launch(const dmtp_sample_args& a, unsigned cluster, cudaStream_t st)
 template <typename T>
 cudaError_t launch_t(const dmtp_sample_args& a, cudaStream_t st) {
   const unsigned cluster = a.vocab > 8192 ? 8 : a.vocab > 2048 ? 2 : 1;
-  // rows that one wave of the GPU holds: more threads finish a row sooner; more rows: fewer
-  // threads spend less on what every thread does once
-  return (int64_t)a.rows * cluster <= 304 ? launch<T, 512>(a, cluster, st) : launch<T, 256>(a, cluster, st);
+  return launch<T, 512>(a, cluster, st);
 }
 
 }  // namespace

@@ -6,28 +6,21 @@ using namespace dmtp;
 
 namespace {
 
-// The merge of one unit's pieces (paged_attn.cuh), one CTA per query: with M the largest of
-// the pieces' maxima, out = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c. Warp w takes every
-// fourth piece, and the four sums are added in order. Units that one CTA wrote are left alone;
-// units without a tile get zeros. It is all latency (a few hundred KB from L2), so the pieces'
-// rows are asked for eight at a time.
-template <typename T>
-__global__ void __launch_bounds__(128) k_paged_merge(const PagedAttn p, int ctas) {
+// The merge of the unit that CTA blockIdx.x began and did not end (paged_attn.cuh): with M the
+// largest of the pieces' maxima, out = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c. A CTA takes
+// PER queries: four of them, one a warp, or one, with every fourth piece a warp's and the four
+// sums added in order. It is all latency (the pieces lie in L2), so their rows are asked for
+// eight at a time.
+template <typename T, int PER>
+__global__ void __launch_bounds__(128) k_paged_merge(const PagedAttn p) {
   __shared__ __align__(16) float part[3][DMTP_OPS_MAX_HEAD_DIM];
   pdl_wait();
-  const int b = blockIdx.y, unit = blockIdx.x, t = blockIdx.z, hd = p.m.head_dim;
-  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  if (t >= queries_of(p, unit)) return;
-  const long long total = p.prefix[p.m.n_seqs];
-  const int lo = p.prefix[b], n = (p.prefix[b + 1] - lo) / p.units;
-  const int G = busy_ctas(total, ctas);
-  const long long s0 = lo + (long long)unit * n;
-  int c0 = 0, c1 = -1;
-  if (n > 0) {
-    c0 = (int)(((s0 + 1) * G - 1) / total);
-    c1 = (int)(((s0 + n) * G - 1) / total);
-    if (c0 == c1) return;
-  }
+  const int c0 = blockIdx.x, hd = p.m.head_dim, lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const PagedNote note = p.note[c0];
+  if (note.b < 0) return;
+  const int t = PER == 4 ? blockIdx.y * 4 + wid : blockIdx.y;
+  if (t >= queries_of(p, note.unit)) return;
+  const int c1 = note.last;
   float M = -INFINITY, L = 0.f;
   for (int c = c0 + lane; c <= c1; c += 32)
     M = fmaxf(M, p.part_ml[(c * 2 + (c == c0)) * p.qn + t].x);
@@ -40,29 +33,32 @@ __global__ void __launch_bounds__(128) k_paged_merge(const PagedAttn p, int ctas
   L = warp_sum(L);
   const float inv = L != 0.f ? 1.f / L : 0.f;
   int head, row;
-  query_of(p, unit, t, &head, &row);
-  T* out = (T*)p.a.out + (int64_t)b * p.a.o_seq + (int64_t)row * p.a.o_row + (int64_t)head * p.a.o_head;
+  query_of(p, note.unit, t, &head, &row);
+  T* out = (T*)p.a.out + (int64_t)note.b * p.a.o_seq + (int64_t)row * p.a.o_row + (int64_t)head * p.a.o_head;
   for (int d = 4 * lane; d < (hd + 127) / 128 * 128; d += 128) {
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     if (d < hd) {
 #pragma unroll 8
-      for (int c = c0 + wid; c <= c1; c += 4) {
+      for (int c = c0 + (PER == 4 ? 0 : wid); c <= c1; c += (PER == 4 ? 1 : 4)) {
         const int at = (c * 2 + (c == c0)) * p.qn + t;
         const float w = ex2(p.part_ml[at].x - ref);
         const float4 v = *reinterpret_cast<const float4*>(p.part_o + (int64_t)at * hd + d);
         o = make_float4(fmaf(w, v.x, o.x), fmaf(w, v.y, o.y), fmaf(w, v.z, o.z), fmaf(w, v.w, o.w));
       }
-      if (wid) *reinterpret_cast<float4*>(&part[wid - 1][d]) = o;
     }
-    __syncthreads();
-    if (wid == 0 && d < hd) {
+    if (PER == 1) {
+      if (wid && d < hd) *reinterpret_cast<float4*>(&part[wid - 1][d]) = o;
+      __syncthreads();
+      if (wid) continue;
+      if (d < hd) {
 #pragma unroll
-      for (int i = 0; i < 3; ++i) {
-        const float4 v = *reinterpret_cast<const float4*>(&part[i][d]);
-        o = make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w);
+        for (int i = 0; i < 3; ++i) {
+          const float4 v = *reinterpret_cast<const float4*>(&part[i][d]);
+          o = make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w);
+        }
       }
-      store_act4(out + d, 0, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
     }
+    if (d < hd) store_act4(out + d, 0, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
   }
 }
 
@@ -89,13 +85,19 @@ int plan(const dmtp_paged_kv* c, const dmtp_paged_query* a, PagedPlan* pl) {
   }
   pl->chunks = (nq + pl->qn - 1) / pl->qn;
   const int64_t reach = (int64_t)c->max_blocks * c->page_size;
-  const int64_t most = (reach + 63) / 64 * c->n_seqs * c->n_kv_heads * pl->chunks;
-  if (most >= (1ll << 31)) return DMTP_EINVAL;
+  const int64_t units = (int64_t)c->n_seqs * c->n_kv_heads * pl->chunks;
+  if ((reach + 63) / 64 * units >= (1ll << 31)) return DMTP_EINVAL;
+  pl->whole = reach <= kWholeReach;
+  if (pl->whole) {
+    pl->grid = (int)units;
+    pl->part_o = pl->part_ml = pl->note = pl->bytes = 0;
+    return DMTP_OK;
+  }
   const size_t parts = (size_t)pl->grid * 2 * pl->qn;
   pl->part_o = 0;
   pl->part_ml = up256(parts * hd * 4);
-  pl->prefix = pl->part_ml + up256(parts * 8);
-  pl->bytes = pl->prefix + up256(((size_t)c->n_seqs + 1) * 4);
+  pl->note = pl->part_ml + up256(parts * 8);
+  pl->bytes = pl->note + up256((size_t)pl->grid * sizeof(PagedNote));
   return DMTP_OK;
 }
 
@@ -118,7 +120,7 @@ extern "C" int dmtp_paged_attention(const dmtp_paged_kv* c, const dmtp_paged_que
   const int e = check_query(c, a);
   if (e) return e;
   const int es = c->dtype ? 2 : 4, hd = c->head_dim;
-  if (!a->q || !a->out || !a->kv_len || !workspace) return DMTP_EINVAL;
+  if (!a->q || !a->out || !a->kv_len) return DMTP_EINVAL;
   if (!aligned_to(a->q, 16) || !aligned_to(a->out, 16) || !aligned_to(a->kv_len, 4) ||
       !aligned_to(workspace, 256) || (err && !aligned_to(err, 4)))
     return DMTP_EINVAL;
@@ -129,6 +131,7 @@ extern "C" int dmtp_paged_attention(const dmtp_paged_kv* c, const dmtp_paged_que
   PagedPlan pl;
   const int r = plan(c, a, &pl);
   if (r) return r;
+  if (pl.bytes && !workspace) return DMTP_EINVAL;
   if (ws_bytes < pl.bytes) return DMTP_ENOMEM;
   if (cudaPeekAtLastError() != cudaSuccess) return DMTP_ECUDA;
   PagedAttn p;
@@ -146,15 +149,18 @@ extern "C" int dmtp_paged_attention(const dmtp_paged_kv* c, const dmtp_paged_que
   p.units = c->n_kv_heads * pl.chunks;
   p.part_o = (float*)((char*)workspace + pl.part_o);
   p.part_ml = (float2*)((char*)workspace + pl.part_ml);
-  p.prefix = (int*)((char*)workspace + pl.prefix);
+  p.note = pl.whole ? nullptr : (PagedNote*)((char*)workspace + pl.note);
   p.scale2 = a->scale * 1.4426950408889634f;
   cudaStream_t st = (cudaStream_t)stream;
   cudaError_t le = pl.tc ? paged_attn_tc(p, pl, c->e4m3 != 0, st)
                          : paged_attn_simt(p, pl, c->dtype, c->e4m3 != 0, st);
-  if (le == cudaSuccess) {
-    const dim3 grid(p.units, c->n_seqs, p.nq < pl.qn ? p.nq : pl.qn);
-    le = c->dtype ? launch_op(k_paged_merge<bf16>, grid, 128, 0, st, true, 1, p, pl.grid)
-                  : launch_op(k_paged_merge<float>, grid, 128, 0, st, true, 1, p, pl.grid);
+  if (le == cudaSuccess && !pl.whole) {
+    const int nq = p.nq < pl.qn ? p.nq : pl.qn;
+    const bool four = nq > 8;
+    const dim3 grid(pl.grid, four ? (nq + 3) / 4 : nq);
+    auto k = c->dtype ? (four ? k_paged_merge<bf16, 4> : k_paged_merge<bf16, 1>)
+                      : (four ? k_paged_merge<float, 4> : k_paged_merge<float, 1>);
+    le = launch_op(k, grid, 128, 0, st, true, 1, p);
   }
   return le == cudaSuccess ? DMTP_OK : (cudaGetLastError(), DMTP_ECUDA);
 }

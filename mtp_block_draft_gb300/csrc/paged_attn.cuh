@@ -1,20 +1,34 @@
 // Attention over a paged cache: what its kernels share - the arguments, how the key tiles
 // of all sequences are dealt out to the CTAs, and the partial results.
 //
-// Work. Sequence b's positions [first_b, len_b) that a row can see (first_b rounded down) are n_b tiles of TK keys. A unit is
-// one (sequence, kv head, chunk of at most QN queries); a sequence has U = n_kv_heads x
-// chunks of them. All units' tiles laid end to end (T in all) are dealt to the G CTAs in
-// equal contiguous ranges (G at most T), CTA c taking tiles [c T / G, (c + 1) T / G): every CTA streams
-// the same number of tiles whatever the lengths, which only the device knows, and the grid
-// is fixed, so a call can be captured. A CTA's part of one unit is a piece. A piece that is
-// a whole unit writes its output rows; any other leaves (max, sum, O) in the workspace, in
-// slot 0 of its CTA if an earlier CTA began the unit, else in slot 1 (the unit is then the
-// CTA's last), and the merge kernel joins a unit's pieces in order.
+// Work. Sequence b's positions [first_b, len_b) that a row can see (first_b rounded down) are
+// n_b tiles of 64 keys. A unit is one (sequence, kv head, chunk of at most QN queries); a
+// sequence has U = n_kv_heads x chunks of them.
+//
+// Whole units (tables that reach no further than kWholeReach positions): CTA c takes unit c, and
+// one launch is all; nothing about the lengths has to be known before.
+//
+// Split units: all units' tiles laid end to end (T in all) are dealt to the G CTAs (G at most
+// T) in contiguous ranges of T / G tiles, the first T % G of them one more: every CTA streams
+// the same number of tiles whatever the lengths, which only the device knows, and the grid is
+// fixed, so a call can be captured. A CTA's part of one unit is a piece. A piece that is a whole
+// unit writes its output rows; any other leaves (max, sum, O) in the workspace, in slot 0 of its
+// CTA if an earlier CTA began the unit, else in slot 1 (the unit is then the CTA's last), with a
+// note of the unit and its last CTA; the merge kernel joins each noted unit's pieces in order.
+// Sequences without a tile get their zeros from CTA b % G.
 #pragma once
 
 #include "paged.cuh"
 
 namespace dmtp {
+
+// Table reach up to which units are not split. Measured with one sequence of that length, 4 kv
+// heads of 128 (32 query heads), us in a captured graph: see paged_attn.cu.
+constexpr int kWholeReach = 1024;
+
+struct PagedNote {
+  int b, unit, last, pad;  // a split unit that begins in this CTA, and its last CTA; b < 0: none
+};
 
 struct PagedAttn {
   PageMap m;
@@ -25,7 +39,7 @@ struct PagedAttn {
   int group, nq, qn, chunks, units;  // queries per kv head; of a unit; units of a sequence
   float* part_o;                     // [G][2][qn][head_dim]
   float2* part_ml;                   // [G][2][qn] (max in base 2, sum)
-  int* prefix;                       // [n_seqs + 1] tiles before sequence b
+  PagedNote* note;                   // [G]; null: whole units
   float scale2;                      // scale log2(e)
 };
 
@@ -40,83 +54,117 @@ __device__ __forceinline__ int seq_first(const PagedAttn& p, int len) {
   const int f = len - p.a.rows + 1 - p.a.window;
   return f > 0 ? f & ~63 : 0;
 }
-template <int TK>
 __device__ __forceinline__ int seq_tiles(const PagedAttn& p, int len) {
-  return (len - seq_first(p, len) + TK - 1) / TK;
+  return (len - seq_first(p, len) + 63) / 64;
 }
 
-// CTAs that take tiles: with fewer tiles than CTAs, as many as there are tiles, so that
-// every one of them has a piece of each unit it lies in.
-__device__ __forceinline__ int busy_ctas(long long total, int G) {
-  return total < G ? (int)total : G;
-}
-
-struct Walk {
-  long long total;  // T
-  int pos, end;     // this CTA's tiles
-  int b, base;      // the sequence of tile pos, tiles before it
+// The tiles of a CTA in order: [pos, end) of all, pos lying in tile t of a unit of sequence b.
+struct Tiles {
+  int pos, end, b, unit, t, n, len, first;
+  __device__ __forceinline__ void seq(const PagedAttn& p) {
+    len = seq_len(p, b);
+    first = seq_first(p, len);
+    n = (len - first + 63) / 64;
+  }
+  __device__ __forceinline__ void skip(const PagedAttn& p, int tiles) {  // to the next unit at most
+    pos += tiles;
+    t += tiles;
+    if (t == n && pos < end) {
+      t = 0;
+      if (++unit == p.units) {
+        unit = 0;
+        do {
+          ++b;
+          seq(p);
+        } while (n == 0);
+      }
+    }
+  }
+};
+struct Deal {
+  int each, more;  // tiles of a CTA, and how many CTAs have one more
+  __device__ __forceinline__ int begin(int c) const { return c * each + min(c, more); }
+  __device__ __forceinline__ int owner(int tile) const {
+    const int big = more * (each + 1);
+    return tile < big ? tile / (each + 1) : more + (tile - big) / each;
+  }
 };
 
-// This CTA's range and where it starts, by all THREADS threads of the CTA. `sh`: THREADS / 32
-// + 4 ints of shared memory. CTA 0 also leaves the prefix sums for the merge kernel.
-template <int TK, int THREADS>
-__device__ __forceinline__ Walk deal(const PagedAttn& p, int* sh) {
-  constexpr int W = THREADS / 32;
-  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, n = p.m.n_seqs;
-  Walk w;
-  int sum = 0;
-  for (int b = threadIdx.x; b < n; b += THREADS) sum += seq_tiles<TK>(p, seq_len(p, b));
+// This CTA's tiles. Every warp finds them for itself. Also zeros the output of sequences that
+// have none, and reports lengths past the table's reach. All threads call it.
+template <typename T>
+__device__ __forceinline__ Tiles my_tiles(const PagedAttn& p, Deal& d, int threads) {
+  const int lane = threadIdx.x & 31, n = p.m.n_seqs, G = gridDim.x, c = blockIdx.x;
+  Tiles w;
+  d.each = 1;
+  d.more = 0;
+  int zero_b, zero_step;  // sequences to look at
+  if (!p.note) {
+    w.b = c / p.units;
+    w.unit = c - w.b * p.units;
+    w.t = 0;
+    w.seq(p);
+    w.pos = 0;
+    w.end = w.n;
+    zero_b = w.unit == 0 ? w.b : n;
+    zero_step = n;
+  } else {
+    int total = 0;
+    for (int b = lane; b < n; b += 32) total += seq_tiles(p, seq_len(p, b));
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) sh[wid] = sum;
-  __syncthreads();
-  int total = 0;
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    total *= p.units;
+    const int busy = min(total, G);
+    d.each = busy ? total / busy : 1;
+    d.more = busy ? total - d.each * busy : 0;
+    w.pos = c < busy ? d.begin(c) : 0;
+    w.end = c < busy ? d.begin(c + 1) : 0;
+    w.b = w.unit = w.t = w.n = w.len = w.first = 0;
+    if (w.pos < w.end) {
+      int before = 0;  // tiles of the sequences before this round
+      for (int b0 = 0; b0 < n; b0 += 32) {
+        const int t = b0 + lane < n ? seq_tiles(p, seq_len(p, b0 + lane)) * p.units : 0;
+        int inc = t;
 #pragma unroll
-  for (int i = 0; i < W; ++i) total += sh[i];
-  w.total = (long long)total * p.units;
-  const int G = busy_ctas(w.total, gridDim.x), c = min((int)blockIdx.x, G);
-  w.pos = G ? (int)(w.total * c / G) : 0;
-  w.end = G ? (int)(w.total * min(c + 1, G) / G) : 0;
-  w.b = 0;
-  w.base = 0;
-  int before = 0;  // tiles of one unit before this round of sequences
-  for (int b0 = 0; b0 < n; b0 += THREADS) {
-    const int b = b0 + threadIdx.x;
-    const int len = b < n ? seq_len(p, b) : 0;
-    if (blockIdx.x == 0 && b < n && __ldg(p.a.kv_len + b) > p.m.reach) set_err(p.err, DMTP_OPS_ERR_POS);
-    const int t = b < n ? seq_tiles<TK>(p, len) : 0;
-    int inc = t;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += v;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += v;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, before + inc > w.pos);
+        if (past) {
+          const int l = __ffs(past) - 1;
+          w.b = b0 + l;
+          const int in = w.pos - (before + __shfl_sync(0xffffffffu, inc - t, l));
+          w.seq(p);
+          w.unit = in / w.n;
+          w.t = in - w.unit * w.n;
+          break;
+        }
+        before += __shfl_sync(0xffffffffu, inc, 31);
+      }
     }
-    __syncthreads();  // sh of the total (or the last round) has been read
-    if (lane == 31) sh[wid] = inc;
-    __syncthreads();
-    int off = before, all = 0;
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-      if (i < wid) off += sh[i];
-      all += sh[i];
-    }
-    const int lo = (off + inc - t) * p.units, hi = (off + inc) * p.units;
-    if (blockIdx.x == 0 && b < n) {
-      p.prefix[b] = lo;
-      if (b == n - 1) p.prefix[n] = hi;
-    }
-    if (t > 0 && w.pos >= lo && w.pos < hi) {
-      sh[W] = b;
-      sh[W + 1] = lo;
-    }
-    before += all;
+    zero_b = c;
+    zero_step = G;
   }
-  __syncthreads();
-  if (w.pos < w.end) {
-    w.b = sh[W];
-    w.base = sh[W + 1];
+  for (int b = zero_b; b < n; b += zero_step) {
+    const int raw = __ldg(p.a.kv_len + b);
+    if (raw > p.m.reach && threadIdx.x == 0) set_err(p.err, DMTP_OPS_ERR_POS);
+    if (raw > 0) continue;
+    const int hd = p.m.head_dim;
+    for (int i = threadIdx.x; i < p.a.rows * p.a.n_heads * hd; i += threads) {
+      const int rh = i / hd, row = rh / p.a.n_heads;
+      ((T*)p.a.out)[(int64_t)b * p.a.o_seq + (int64_t)row * p.a.o_row +
+                    (int64_t)(rh - row * p.a.n_heads) * p.a.o_head + (i - rh * hd)] = from_f32<T>(0.f);
+    }
   }
   return w;
+}
+// Once per CTA of a split call: the unit that it begins and does not end. pos: the unit's first
+// tile among all; one thread.
+__device__ __forceinline__ void leave_note(const PagedAttn& p, const Deal& d, const Tiles& w, bool some) {
+  PagedNote n = {-1, 0, 0, 0};
+  if (some) n = {w.b, w.unit, d.owner(w.pos + w.n - 1), 0};
+  p.note[blockIdx.x] = n;
 }
 
 // Output row of query t of a unit: query head and row.
@@ -131,11 +179,11 @@ __device__ __forceinline__ int queries_of(const PagedAttn& p, int unit) {
 }
 
 // Which kernel takes a call: the tensor cores (paged_attn_tc.cu) or the CUDA cores
-// (paged_attn_simt.cu), with tiles of 64 or 128 keys.
+// (paged_attn_simt.cu), with tiles of 64 keys.
 struct PagedPlan {
-  bool tc;
+  bool tc, whole;
   int qn, chunks, grid;
-  size_t part_o, part_ml, prefix, bytes;  // workspace offsets
+  size_t part_o, part_ml, note, bytes;  // workspace offsets
 };
 cudaError_t paged_attn_tc(const PagedAttn& p, const PagedPlan& pl, bool e8, cudaStream_t st);
 cudaError_t paged_attn_simt(const PagedAttn& p, const PagedPlan& pl, int dtype, bool e8, cudaStream_t st);

@@ -29,7 +29,7 @@ __host__ __device__ inline int smem_of(int hd, int es) {
          + 2 * kQ * 32 * 4            // P of each warp
          + kQ * hd * 4                // joining the warps
          + 2 * kTK * 4                // scales
-         + kTK * 8 + 256;             // row offsets, warps' statistics, the walk
+         + kTK * 8 + kQ * 8;          // row offsets, warps' statistics
 }
 
 template <typename S> struct Chunk;  // values of a 16-byte step
@@ -105,18 +105,13 @@ __global__ void __launch_bounds__(kThreads) k_paged_attn_simt(const PagedAttn p)
   float* sS = sP + 2 * kQ * 32;
   int64_t* sRow = (int64_t*)(sS + 2 * kTK);
   float2* sML = (float2*)(sRow + kTK);
-  int* sW = (int*)(sML + kQ);
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-  Walk w = deal<kTK, kThreads>(p, sW);
+  Deal deal;
+  Tiles w = my_tiles<T>(p, deal, kThreads);
+  bool noted = false;
 
   while (w.pos < w.end) {
-    const int len = seq_len(p, w.b), first = seq_first(p, len), n = seq_tiles<kTK>(p, len);
-    if (w.pos >= w.base + n * p.units) {  // on to the next sequence
-      w.base += n * p.units;
-      ++w.b;
-      continue;
-    }
-    const int unit = (w.pos - w.base) / n, t0 = w.pos - w.base - unit * n;
+    const int len = w.len, first = w.first, n = w.n, unit = w.unit, t0 = w.t;
     const int t1 = min(n, t0 + w.end - w.pos);
     const int kvh = unit / p.chunks, nq = queries_of(p, unit);
     for (int i = tid; i < kQ * hd; i += kThreads) {
@@ -259,9 +254,14 @@ __global__ void __launch_bounds__(kThreads) k_paged_attn_simt(const PagedAttn p)
         }
       }
     }
-    w.pos += t1 - t0;
+    if (t0 == 0 && t1 < n) {
+      noted = true;
+      if (tid == 0) leave_note(p, deal, w, true);
+    }
+    w.skip(p, t1 - t0);
     __syncthreads();
   }
+  if (p.note && !noted && tid == 0) leave_note(p, deal, w, false);
 }
 
 template <typename T, typename S, int NI>

@@ -37,15 +37,14 @@ struct Shape {
   static constexpr int QG = QN == 64 ? 2 : 1;       // warps of a team
   static constexpr int KS = 4 / QG;                 // teams
   static constexpr int RB = HD * (E8 ? 1 : 2);      // bytes of a cached row
-  static constexpr int TK = 64;                     // keys of a tile
-  static constexpr int NSUB = TK / 16 / KS;         // 16-key blocks of a team in a tile
+  static constexpr int NSUB = 4 / KS;         // 16-key blocks of a team in a tile
   static constexpr int kBlock = 2 * 16 * RB + (E8 ? 128 : 0);
   static constexpr int kStage = NSUB * kBlock;      // of a team
   static constexpr int kPitch = HD + 4;             // floats of a joined row: no conflicts
   static constexpr int kJoin = QN * kPitch * 4 + KS * QN * 8;
   static constexpr bool QS = NT == 4;               // query fragments in shared memory (the
                                                     // joined rows' place, until the join)
-  static constexpr int kMisc = KS * 8 * NSUB * 4 + 64;  // valid rows of the blocks, the walk
+  static constexpr int kMisc = KS * 8 * NSUB * 4;   // valid rows of the blocks
   // CTAs of an SM: registers (128 threads x 128, 168 or 255) and a ring of two stages at least
   static constexpr int CTAS = QN == 8 ? (RB == 256 ? 3 : 4) : QN == 16 ? (HD == 64 ? 4 : 3) : 2;
   static constexpr int kRoom = 228 * 1024 / CTAS - 1024 - kJoin - kMisc;
@@ -95,42 +94,6 @@ __device__ __forceinline__ uint32_t finite_pair(uint32_t u) {
   if ((u >> 16 & e) == e) u &= 0x0000ffffu;
   return u;
 }
-
-// The tiles of a CTA's range in order.
-template <int TK>
-struct Tiles {
-  int pos, end, b, unit, t, n, len, first;
-  __device__ __forceinline__ void seq(const PagedAttn& p) {
-    len = seq_len(p, b);
-    first = seq_first(p, len);
-    n = (len - first + TK - 1) / TK;
-  }
-  __device__ __forceinline__ void start(const PagedAttn& p, const Walk& w) {
-    pos = w.pos;
-    end = w.end;
-    b = w.b;
-    unit = t = n = len = first = 0;
-    if (pos < end) {
-      seq(p);
-      unit = (pos - w.base) / n;
-      t = pos - w.base - unit * n;
-    }
-  }
-  __device__ __forceinline__ void skip(const PagedAttn& p, int tiles) {  // to the next unit at most
-    pos += tiles;
-    t += tiles;
-    if (t == n && pos < end) {
-      t = 0;
-      if (++unit == p.units) {
-        unit = 0;
-        do {
-          ++b;
-          seq(p);
-        } while (n == 0);
-      }
-    }
-  }
-};
 
 __device__ __forceinline__ uint32_t transpose8(uint32_t u) {  // an 8 x 8 block of 16-bit values
   uint32_t r;
@@ -361,24 +324,26 @@ __device__ __forceinline__ void block(const PagedAttn& p, State<HD, NT>& z,
 template <int HD, bool E8, int QN>
 __global__ void __launch_bounds__(kThreads, Shape<HD, E8, QN>::CTAS) k_paged_attn_tc(const PagedAttn p) {
   using S = Shape<HD, E8, QN>;
-  constexpr int NT = S::NT, QG = S::QG, KS = S::KS, RB = S::RB, NST = S::NST, TK = S::TK, NSUB = S::NSUB;
+  constexpr int NT = S::NT, QG = S::QG, KS = S::KS, RB = S::RB, NST = S::NST, NSUB = S::NSUB;
   constexpr int KK = HD / 16;
   extern __shared__ __align__(128) unsigned char smem[];
   float* sO = (float*)(smem + NST * KS * S::kStage);
   float2* sML = (float2*)(sO + QN * S::kPitch);
   uint4* sQ = (uint4*)sO;
   uint32_t* sOk = (uint32_t*)(sML + KS * QN);
-  int* sWalk = (int*)(sOk + KS * 8 * NSUB);
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, g = lane >> 2, tq = lane & 3;
   const int team = wid / QG, qg = wid % QG;
   unsigned char* ring = smem + team * NST * S::kStage;
   sOk += team * 8 * NSUB;
   pdl_trigger();
-  const Walk w = deal<TK, kThreads>(p, sWalk);
-  if (w.pos >= w.end) return;
-  Tiles<TK> cons, prod;
-  cons.start(p, w);
-  prod = cons;
+  Deal deal;
+  Tiles cons = my_tiles<bf16>(p, deal, kThreads);
+  bool noted = false;
+  if (cons.pos >= cons.end) {
+    if (p.note && tid == 0) leave_note(p, deal, cons, false);
+    return;
+  }
+  Tiles prod = cons;
 
   // ---- copies: a team brings the blocks team + KS i of every tile ----
   constexpr int CPR = RB / 16, RPI = 32 * QG / CPR, NI = 16 / RPI;  // rows of one copy of the team
@@ -387,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, E8, QN>::CTAS) k_paged_att
   auto look_up = [&]() {
 #pragma unroll
     for (int i = 0; i < NSUB; ++i) {
-      const int j = prod.first + prod.t * TK + (team + KS * i) * 16;
+      const int j = prod.first + prod.t * 64 + (team + KS * i) * 16;
       page[i] = -1;
       if (paged16 && prod.pos < prod.end && j < prod.len) page[i] = page_of(p.m, prod.b, j, off[i], p.err);
     }
@@ -401,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, E8, QN>::CTAS) k_paged_att
       for (int i = 0; i < NSUB; ++i) {
         unsigned char* blk = ring + stage_in * S::kStage + i * S::kBlock;
         const uint32_t dst = smem_u32(blk);
-        const int jb = prod.first + prod.t * TK + (team + KS * i) * 16;
+        const int jb = prod.first + prod.t * 64 + (team + KS * i) * 16;
         int rows = min(16, prod.len - jb);
         unsigned ok;
         if (paged16) {
@@ -554,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, E8, QN>::CTAS) k_paged_att
       for (int i = 0; i < NSUB; ++i) {
         const unsigned char* blk = ring + stage * S::kStage + i * S::kBlock;
         const unsigned ok = sOk[stage * NSUB + i];
-        const int jb = cons.first + t * TK + (team + KS * i) * 16;
+        const int jb = cons.first + t * 64 + (team + KS * i) * 16;
         if (ok == 0xffffu && jb + 15 <= cons.len - p.a.rows && (p.a.window <= 0 || jb >= cons.len - p.a.window))
           block<HD, E8, NT, false>(p, z, qf, sq, blk, jb, ok);
         else if (ok)
@@ -639,9 +604,14 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, E8, QN>::CTAS) k_paged_att
         if (d == 0) p.part_ml[slot + q] = make_float2(M, L);
       }
     }
+    if (!whole && t0 == 0) {
+      noted = true;
+      if (tid == 0) leave_note(p, deal, cons, true);
+    }
     cons.skip(p, t1 - t0);
     __syncthreads();  // sO, sML and sQ are free again
   }
+  if (p.note && !noted && tid == 0) leave_note(p, deal, cons, false);
   cp_async_wait<0>();
 }
 

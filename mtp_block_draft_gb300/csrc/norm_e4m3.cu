@@ -1,6 +1,6 @@
 // dmtp_add_rmsnorm_e4m3: residual addition, RMS norm and E4M3 rows in one pass.
 //
-// One CTA per row; the row stays in registers between the sum of squares, the row maximum
+// One CTA at a row; the row stays in registers between the sum of squares, the row maximum
 // and the conversion, so each input is read once and each output written once:
 // d (2 tx + ty + 1) bytes a row, which is what bounds it (a few operations a byte).
 //
@@ -23,116 +23,222 @@ __device__ __forceinline__ F2 add(F2 a, F2 b) {
   F2 s = two_sum(a.hi, b.hi);
   return F2{s.hi, s.lo + (a.lo + b.lo)};
 }
-__device__ __forceinline__ void add_square(F2& a, float x) {
-  const float p = x * x, e = fmaf(x, x, -p);
-  const F2 s = two_sum(a.hi, p);
-  a.hi = s.hi;
-  a.lo += s.lo + e;
+// Packed single precision: two of a thread's sums of squares side by side.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pack(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
 }
-__device__ __forceinline__ float4 gain4(const void* p, int dt, int i) {
-  return dt ? load4((const bf16*)p + i) : load4((const float*)p + i);
+__device__ __forceinline__ float2 unpack(f32x2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// (hi, lo) += x^2: the square with its rounding error, the addition with its own.
+__device__ __forceinline__ void add_squares(f32x2& hi, f32x2& lo, f32x2 x, f32x2 minus) {
+  const f32x2 p = fma2(x, x, 0ull), e = fma2(x, x, fma2(p, minus, 0ull));
+  const f32x2 s = add2(hi, p), t = fma2(hi, minus, s);          // t = s - hi
+  const f32x2 f = add2(fma2(fma2(t, minus, s), minus, hi), fma2(t, minus, p));
+  hi = s;
+  lo = add2(lo, add2(e, f));
+}
+// Eight values as they lie in memory (fp32: two steps of 16 bytes, bf16: one).
+template <typename T>
+struct Raw {
+  uint4 u[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ Raw<T> fetch(const T* p) {
+  Raw<T> r;
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.u[i] = __ldcs(reinterpret_cast<const uint4*>(p) + i);
+  return r;
+}
+__device__ __forceinline__ void get8(const Raw<float>& r, float (&f)[8]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    f[4 * i] = __uint_as_float(r.u[i].x);
+    f[4 * i + 1] = __uint_as_float(r.u[i].y);
+    f[4 * i + 2] = __uint_as_float(r.u[i].z);
+    f[4 * i + 3] = __uint_as_float(r.u[i].w);
+  }
+}
+__device__ __forceinline__ void get8(const Raw<bf16>& r, float (&f)[8]) {
+  const uint32_t w[4] = {r.u[0].x, r.u[0].y, r.u[0].z, r.u[0].w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void put8(float* p, const float (&f)[8]) {
+  *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+  *reinterpret_cast<float4*>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
+}
+__device__ __forceinline__ void put8(bf16* p, const float (&f)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// NV: eights of a thread. A CTA takes every gridDim.x-th row and asks for the next one's values
+// before it works on the one it has, so the reductions' barriers do not leave the memory idle.
 template <typename TX, typename TY, int NV, int THREADS>
 __global__ void __launch_bounds__(THREADS) k_add_rmsnorm_e4m3(const dmtp_norm_args a) {
-  __shared__ float2 red2[THREADS / 32];
-  __shared__ float red[THREADS / 32];
-  const int d4 = a.d >> 2, lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  const int64_t row = blockIdx.x;
-  const TX* x = (const TX*)a.x + row * a.x_row;
-  float4 v[NV];
-  F2 ss = {0.f, 0.f};
-#pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    const int i = threadIdx.x + k * THREADS;
-    v[k] = i < d4 ? load4(x + 4 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
-  }
-  if (a.y) {
-    const TY* y = (const TY*)a.y + row * a.y_row;
+  __shared__ float2 red2[2][THREADS / 32];
+  __shared__ uint32_t red[2][THREADS / 32];
+  const int d8 = a.d >> 3, lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  Raw<TX> rx[NV];
+  Raw<TY> ry[NV];
+  auto ask = [&](int64_t row) {
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int i = threadIdx.x + k * THREADS;
-      if (i < d4) {
-        const float4 w = load4(y + 4 * i);
-        v[k] = make_float4(v[k].x + w.x, v[k].y + w.y, v[k].z + w.z, v[k].w + w.w);
+      if (i < d8) {
+        rx[k] = fetch((const TX*)a.x + row * a.x_row + 8 * i);
+        if (a.y) ry[k] = fetch((const TY*)a.y + row * a.y_row + 8 * i);
       }
     }
-  }
-  if (a.x_out) {
-    TX* xo = (TX*)a.x_out + row * a.xo_row;
+  };
+  ask(blockIdx.x);
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+    float v[NV][8];
+    const f32x2 minus = pack(-1.f, -1.f);
+    f32x2 hi2 = 0ull, lo2 = 0ull;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int i = threadIdx.x + k * THREADS;
-      if (i < d4) store_act4(xo + 4 * i, 0, v[k]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[k][e] = 0.f;
+      if (i < d8) {
+        get8(rx[k], v[k]);
+        if (a.y) {
+          float w[8];
+          get8(ry[k], w);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[k][e] += w[e];
+        }
+      }
     }
-  }
+    if (row + gridDim.x < a.rows) ask(row + gridDim.x);
 #pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    add_square(ss, v[k].x);
-    add_square(ss, v[k].y);
-    add_square(ss, v[k].z);
-    add_square(ss, v[k].w);
-  }
+    for (int k = 0; k < NV; ++k) {
+      const int i = threadIdx.x + k * THREADS;
+      if (a.x_out && i < d8) put8((TX*)a.x_out + row * a.xo_row + 8 * i, v[k]);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    ss = add(ss, F2{__shfl_xor_sync(0xffffffffu, ss.hi, o), __shfl_xor_sync(0xffffffffu, ss.lo, o)});
-  if (lane == 0) red2[wid] = make_float2(ss.hi, ss.lo);
-  __syncthreads();
-  ss = F2{red2[0].x, red2[0].y};
-#pragma unroll
-  for (int w = 1; w < THREADS / 32; ++w) ss = add(ss, F2{red2[w].x, red2[w].y});
-  // mean + eps as a pair: q = S / d, then the division's remainder
-  const float n = (float)a.d, q0 = ss.hi / n;
-  F2 ms = two_sum(q0, a.eps);
-  ms.lo += (fmaf(-q0, n, ss.hi) + ss.lo) / n;
-  // r ~ 1 / sqrt(ms), one Newton step on the pair: r + r (1 - ms r^2) / 2
-  const float r0 = rsqrtf(ms.hi);
-  const float rr = r0 * r0, rl = fmaf(r0, r0, -rr);
-  const float p = ms.hi * rr;
-  const float res = (1.f - p) - (fmaf(ms.hi, rr, -p) + ms.hi * rl + ms.lo * rr);
-  // a sum that overflowed, or no non-zero element and eps 0: the plain value
-  const float r = fabsf(res) < 0.25f ? fmaf(0.5f * r0, res, r0) : rsqrtf(ss.hi / n + a.eps);
-  float amax = 0.f;
-#pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    const int i = threadIdx.x + k * THREADS;
-    if (i < d4) {
-      const float4 g = gain4(a.gain, a.gain_dtype, 4 * i);
-      v[k] = make_float4(v[k].x * r * g.x, v[k].y * r * g.y, v[k].z * r * g.z, v[k].w * r * g.w);
-      amax = fmaxf(amax, fmaxf(fmaxf(finite_abs(v[k].x), finite_abs(v[k].y)),
-                               fmaxf(finite_abs(v[k].z), finite_abs(v[k].w))));
+      for (int e = 0; e < 8; e += 2) add_squares(hi2, lo2, pack(v[k][e], v[k][e + 1]), minus);
     }
-  }
-  amax = warp_max(amax);
-  if (lane == 0) red[wid] = amax;
-  __syncthreads();
+    const float2 h2 = unpack(hi2), l2 = unpack(lo2);
+    F2 ss = add(F2{h2.x, l2.x}, F2{h2.y, l2.y});
 #pragma unroll
-  for (int w = 0; w < THREADS / 32; ++w) amax = fmaxf(amax, red[w]);
-  const int e = e4m3_exponent(amax);
-  const float inv = pow2f(-e);
-  uint8_t* q = (uint8_t*)a.q + row * a.q_row;
+    for (int o = 16; o > 0; o >>= 1)
+      ss = add(ss, F2{__shfl_xor_sync(0xffffffffu, ss.hi, o), __shfl_xor_sync(0xffffffffu, ss.lo, o)});
+    if (THREADS > 32) {
+      if (lane == 0) red2[turn][wid] = make_float2(ss.hi, ss.lo);
+      __syncthreads();
+      ss = F2{red2[turn][0].x, red2[turn][0].y};
 #pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    const int i = threadIdx.x + k * THREADS;
-    if (i < d4)
-      *reinterpret_cast<uint32_t*>(q + 4 * i) = e4m3_row4(
-          make_float4(v[k].x * inv, v[k].y * inv, v[k].z * inv, v[k].w * inv));
+      for (int w = 1; w < THREADS / 32; ++w) ss = add(ss, F2{red2[turn][w].x, red2[turn][w].y});
+    }
+    // mean + eps as a pair: q = S / d, then the division's remainder
+    const float n = (float)a.d, q0 = ss.hi / n;
+    F2 ms = two_sum(q0, a.eps);
+    ms.lo += (fmaf(-q0, n, ss.hi) + ss.lo) / n;
+    // r ~ 1 / sqrt(ms), one Newton step on the pair: r + r (1 - ms r^2) / 2
+    const float r0 = rsqrtf(ms.hi);
+    const float rr = r0 * r0, rl = fmaf(r0, r0, -rr);
+    const float p = ms.hi * rr;
+    const float res = (1.f - p) - (fmaf(ms.hi, rr, -p) + ms.hi * rl + ms.lo * rr);
+    // a sum that overflowed, or no non-zero element and eps 0: the plain value
+    const float r = fabsf(res) < 0.25f ? fmaf(0.5f * r0, res, r0) : rsqrtf(ss.hi / n + a.eps);
+    uint32_t top = 0;  // largest magnitude, as bits: an infinity or NaN is above every number
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int i = threadIdx.x + k * THREADS;
+      if (i < d8) {
+        float g[8];
+        if (a.gain_dtype)
+          get8(Raw<bf16>{__ldg((const uint4*)a.gain + i)}, g);
+        else
+          get8(Raw<float>{__ldg((const uint4*)a.gain + 2 * i), __ldg((const uint4*)a.gain + 2 * i + 1)}, g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          v[k][e] = v[k][e] * r * g[e];
+          top = max(top, __float_as_uint(v[k][e]) & 0x7fffffffu);
+        }
+      }
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (THREADS > 32) {
+      if (lane == 0) red[turn][wid] = top;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < THREADS / 32; ++w) top = max(top, red[turn][w]);
+    }
+    const bool odd = top >= 0x7f800000u;
+    if (odd) {  // the scale goes by the finite values
+      uint32_t t = 0;
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (threadIdx.x + k * THREADS < d8) t = max(t, __float_as_uint(finite_abs(v[k][e])));
+      t = __reduce_max_sync(0xffffffffu, t);
+      __syncthreads();
+      if (lane == 0) red[turn][wid] = t;
+      __syncthreads();
+      top = 0;
+#pragma unroll
+      for (int w = 0; w < THREADS / 32; ++w) top = max(top, red[turn][w]);
+    }
+    const int e = e4m3_exponent(__uint_as_float(top));
+    const float inv = pow2f(-e);
+    uint8_t* q = (uint8_t*)a.q + row * a.q_row;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int i = threadIdx.x + k * THREADS;
+      const float (&f)[8] = v[k];
+      const float4 lo = make_float4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
+      const float4 hi = make_float4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv);
+      if (i < d8)
+        *reinterpret_cast<uint2*>(q + 8 * i) =
+            odd ? make_uint2(e4m3_row4(lo), e4m3_row4(hi)) : make_uint2(e4m3x4(lo), e4m3x4(hi));
+    }
+    if (threadIdx.x == 0) a.scale[row] = pow2f(e);
   }
-  if (threadIdx.x == 0) a.scale[row] = pow2f(e);
 }
 
 template <typename TX, typename TY>
 cudaError_t launch(const dmtp_norm_args& a, cudaStream_t st) {
   using dmtp::launch_op;
-  const int d4 = a.d / 4;
+  const int d8 = a.d / 8;
+  // 1024 threads an SM: they hold their rows and the next ones in registers
+  auto grid = [&](int threads) { return a.rows < 152 * 1024 / threads ? a.rows : 152 * 1024 / threads; };
 #define DMTP_NORM(NV_, TH_) \
-  return launch_op(k_add_rmsnorm_e4m3<TX, TY, NV_, TH_>, a.rows, TH_, 0, st, false, 1, a)
-  if (d4 <= 128) DMTP_NORM(1, 128);
-  if (d4 <= 256) DMTP_NORM(2, 128);
-  if (d4 <= 512) DMTP_NORM(2, 256);
-  if (d4 <= 1024) DMTP_NORM(4, 256);
-  if (d4 <= 2048) DMTP_NORM(4, 512);
-  DMTP_NORM(8, 512);
+  return launch_op(k_add_rmsnorm_e4m3<TX, TY, NV_, TH_>, grid(TH_), TH_, 0, st, false, 1, a)
+  if (d8 <= 32) DMTP_NORM(1, 32);
+  if (d8 <= 64) DMTP_NORM(1, 64);
+  if (d8 <= 128) DMTP_NORM(1, 128);
+  if (d8 <= 256) DMTP_NORM(1, 256);
+  if (d8 <= 512) DMTP_NORM(2, 256);
+  if (d8 <= 1024) DMTP_NORM(2, 512);
+  DMTP_NORM(4, 512);
 #undef DMTP_NORM
 }
 

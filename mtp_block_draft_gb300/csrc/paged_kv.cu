@@ -42,20 +42,35 @@ struct WriteArgs {
   bool wide;         // rows allow 16-byte accesses
 };
 
-// Eight consecutive values; `wide`: at a 16-byte boundary (else fp32 at one, bf16 at 8 bytes).
-__device__ __forceinline__ void load8(const float* p, bool wide, float (&f)[8]) {
-  const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p + 4));
-  f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+// Eight consecutive values as they lie in memory; `wide`: at a 16-byte boundary (else fp32 at
+// one, bf16 at 8 bytes).
+template <typename T>
+struct Raw {
+  uint4 u[sizeof(T) / 2];
+};
+__device__ __forceinline__ void fetch(const float* p, bool, Raw<float>& r) {
+  r.u[0] = __ldcs(reinterpret_cast<const uint4*>(p));
+  r.u[1] = __ldcs(reinterpret_cast<const uint4*>(p + 4));
 }
-__device__ __forceinline__ void load8(const bf16* p, bool wide, float (&f)[8]) {
-  uint4 u;
+__device__ __forceinline__ void fetch(const bf16* p, bool wide, Raw<bf16>& r) {
   if (wide) {
-    u = __ldcs(reinterpret_cast<const uint4*>(p));
+    r.u[0] = __ldcs(reinterpret_cast<const uint4*>(p));
   } else {
     const uint2 a = __ldcs(reinterpret_cast<const uint2*>(p)), b = __ldcs(reinterpret_cast<const uint2*>(p + 4));
-    u = make_uint4(a.x, a.y, b.x, b.y);
+    r.u[0] = make_uint4(a.x, a.y, b.x, b.y);
   }
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+}
+__device__ __forceinline__ void values(const Raw<float>& r, float (&f)[8]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    f[4 * i] = __uint_as_float(r.u[i].x);
+    f[4 * i + 1] = __uint_as_float(r.u[i].y);
+    f[4 * i + 2] = __uint_as_float(r.u[i].z);
+    f[4 * i + 3] = __uint_as_float(r.u[i].w);
+  }
+}
+__device__ __forceinline__ void values(const Raw<bf16>& r, float (&f)[8]) {
+  const uint32_t w[4] = {r.u[0].x, r.u[0].y, r.u[0].z, r.u[0].w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     f[2 * i] = __uint_as_float(w[i] << 16);
@@ -85,102 +100,114 @@ __device__ __forceinline__ uint2 e4m3_row8(const float (&f)[8], float inv) {
                     e4m3_row4(make_float4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv)));
 }
 
-// UN: heads that a group has in flight at once.
-template <typename T, bool E8, int UN>
+// A CTA takes ROWS rows: their pages and angles are found together, behind the first heads'
+// loads, and a group asks for its next head before it works on the one it has.
+template <typename T, bool E8, int ROWS>
 __global__ void __launch_bounds__(256) k_paged_write(const WriteArgs a, const Turns turns) {
-  __shared__ __align__(16) float cs[2][DMTP_OPS_MAX_HEAD_DIM / 2];
-  const int row = blockIdx.x, hd = a.m.head_dim, half = hd >> 1;
+  __shared__ __align__(16) float cs[ROWS][2][DMTP_OPS_MAX_HEAD_DIM / 2];
+  __shared__ int s_page[ROWS], s_off[ROWS], s_pos[ROWS];
+  const int row0 = blockIdx.x * ROWS, hd = a.m.head_dim, half = hd >> 1;
   const bool rot = a.r.rope_theta > 0.f;
   const int nq = a.r.q ? a.r.n_heads : 0, hkv = a.m.n_kv_heads, items = nq + 2 * hkv;
+  const int rows = min(ROWS, a.r.n_rows - row0), all = rows * items;
   const int gl = threadIdx.x & (a.group - 1), ng = blockDim.x / a.group;
   const bool on = gl < a.lanes;
-  // a group's loop count is the CTA's: the shuffles and the barrier below see every thread
-  const int step = gridDim.y * ng;
-  const int seq = __ldg(a.r.seq + row), pos = __ldg(a.r.pos + row);
-  int page = -1, off = 0;
-  bool angles = false;
-  for (int it0 = blockIdx.y * ng; it0 < items; it0 += step * UN) {
-    float x[UN][8], y[UN][8];
+  // a group's loop count is the CTA's: the shuffles below see every lane
+  const int step = gridDim.y * ng, mine = threadIdx.x / a.group;
+  Raw<T> x, y;
+  auto ask = [&](int it) {
+    if (on && it < all) {
+      const int r = ROWS == 1 ? 0 : it / items, i = it - r * items;
+      const int64_t row = row0 + r;
+      const T* src = i < nq         ? (const T*)a.r.q + row * a.r.q_row + (int64_t)i * a.r.q_head
+                     : i < nq + hkv ? (const T*)a.r.k + row * a.r.k_row + (int64_t)(i - nq) * a.r.k_head
+                                    : (const T*)a.r.v + row * a.r.v_row + (int64_t)(i - nq - hkv) * a.r.v_head;
+      fetch(src + 8 * gl, a.wide, x);
+      fetch(src + half + 8 * gl, a.wide, y);
+    }
+  };
+  ask(blockIdx.y * ng + mine);
+  if (threadIdx.x < ROWS) {
+    int page = -1, off = 0, pos = 0;
+    if ((int)threadIdx.x < rows) {
+      const int seq = __ldg(a.r.seq + row0 + threadIdx.x);
+      pos = __ldg(a.r.pos + row0 + threadIdx.x);
+      if (seq >= a.m.n_seqs)
+        set_err(a.err, DMTP_OPS_ERR_SEQ);
+      else if (seq >= 0 && (unsigned)pos >= (unsigned)a.m.reach)
+        set_err(a.err, DMTP_OPS_ERR_POS);
+      else if (seq >= 0)
+        page = page_of(a.m, seq, pos, off, a.err);
+    }
+    s_page[threadIdx.x] = page;
+    s_off[threadIdx.x] = off;
+    s_pos[threadIdx.x] = pos;
+  }
+  if (ROWS > 1) __syncthreads();
+  if (rot) {
+    for (int i = threadIdx.x; i < rows * half; i += blockDim.x) {
+      const int r = ROWS == 1 ? 0 : i / half, h = i - r * half;
+      // (of a single row every thread reads the position for itself: no barrier before)
+      const int pos = ROWS == 1 ? __ldg(a.r.pos + row0) : s_pos[r];
+      const float2 t = cos_sin_turns((unsigned long long)(unsigned)pos * turns.f[h]);
+      cs[r][0][h] = t.x;
+      cs[r][1][h] = t.y;
+    }
+  }
+  __syncthreads();
+  for (int it0 = blockIdx.y * ng; it0 < all; it0 += step) {
+    const int it = it0 + mine;
+    float f[8], g[8];
 #pragma unroll
-    for (int n = 0; n < UN; ++n) {
-      const int it = it0 + n * step + (int)threadIdx.x / a.group;
-      const bool isq = it < nq, isv = it >= nq + hkv;
-      const int h = isq ? it : it - nq - (isv ? hkv : 0);
+    for (int e = 0; e < 8; ++e) f[e] = g[e] = 0.f;
+    const int r = ROWS == 1 ? 0 : it / items, i = it - r * items;
+    const int page = it < all ? s_page[r] : -1;
+    const bool live = on && page >= 0, isq = i < nq, isv = i >= nq + hkv;
+    if (live) {
+      values(x, f);
+      values(y, g);
+    }
+    ask(it + step);
+    if (rot && live && !isv) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[n][i] = y[n][i] = 0.f;
-      if (on && it < items) {
-        const T* src = isq   ? (const T*)a.r.q + (int64_t)row * a.r.q_row + (int64_t)h * a.r.q_head
-                       : isv ? (const T*)a.r.v + (int64_t)row * a.r.v_row + (int64_t)h * a.r.v_head
-                             : (const T*)a.r.k + (int64_t)row * a.r.k_row + (int64_t)h * a.r.k_head;
-        load8(src + 8 * gl, a.wide, x[n]);
-        load8(src + half + 8 * gl, a.wide, y[n]);
+      for (int e = 0; e < 8; e += 4) {
+        const float4 c = *reinterpret_cast<const float4*>(&cs[r][0][8 * gl + e]);
+        const float4 s = *reinterpret_cast<const float4*>(&cs[r][1][8 * gl + e]);
+        const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float p = f[e + j], q = g[e + j];
+          f[e + j] = p * cc[j] - q * ss[j];
+          g[e + j] = q * cc[j] + p * ss[j];
+        }
       }
     }
-    if (!angles) {  // the page and the angles, while the rows are on their way
-      if (seq < 0) return;
-      if (seq >= a.m.n_seqs || (unsigned)pos >= (unsigned)a.m.reach) {
-        if (threadIdx.x == 0)
-          set_err(a.err, seq >= a.m.n_seqs ? DMTP_OPS_ERR_SEQ : DMTP_OPS_ERR_POS);
-        return;
-      }
-      page = page_of(a.m, seq, pos, off, threadIdx.x == 0 ? a.err : nullptr);
-      if (page < 0) return;
-      if (rot) {
-        for (int i = threadIdx.x; i < half; i += blockDim.x) {
-          const float2 t = cos_sin_turns((unsigned long long)(unsigned)pos * turns.f[i]);
-          cs[0][i] = t.x;
-          cs[1][i] = t.y;
-        }
-        __syncthreads();
-      }
-      angles = true;
+    if (live && isq) {
+      T* dst = (T*)a.r.q_out + (int64_t)(row0 + r) * a.r.qo_row + (int64_t)i * a.r.qo_head;
+      store8(dst + 8 * gl, a.wide, f);
+      store8(dst + half + 8 * gl, a.wide, g);
     }
+    float amax = 0.f;
+    if (E8) {
 #pragma unroll
-    for (int n = 0; n < UN; ++n) {
-      const int it = it0 + n * step + (int)threadIdx.x / a.group;
-      const bool live = on && it < items, isq = it < nq, isv = it >= nq + hkv;
-      const int h = isq ? it : it - nq - (isv ? hkv : 0);
-      if (rot && live && !isv) {
-#pragma unroll
-        for (int i = 0; i < 8; i += 4) {
-          const float4 c = *reinterpret_cast<const float4*>(&cs[0][8 * gl + i]);
-          const float4 s = *reinterpret_cast<const float4*>(&cs[1][8 * gl + i]);
-          const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float p = x[n][i + e], q = y[n][i + e];
-            x[n][i + e] = p * cc[e] - q * ss[e];
-            y[n][i + e] = q * cc[e] + p * ss[e];
-          }
-        }
-      }
-      if (live && isq) {
-        T* dst = (T*)a.r.q_out + (int64_t)row * a.r.qo_row + (int64_t)h * a.r.qo_head;
-        store8(dst + 8 * gl, a.wide, x[n]);
-        store8(dst + half + 8 * gl, a.wide, y[n]);
-      }
-      float amax = 0.f;
+      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fmaxf(finite_abs(f[e]), finite_abs(g[e])));
+      for (int o = a.group >> 1; o > 0; o >>= 1)
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    }
+    if (live && !isq) {
+      const int64_t line = (int64_t)(i - nq - (isv ? hkv : 0)) * a.m.page_size + s_off[r];
+      const int64_t at = (int64_t)page * a.m.page_stride + line * hd;
       if (E8) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fmaxf(finite_abs(x[n][i]), finite_abs(y[n][i])));
-        for (int o = a.group >> 1; o > 0; o >>= 1)
-          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      }
-      if (live && !isq) {
-        const int64_t line = (int64_t)h * a.m.page_size + off;
-        const int64_t at = (int64_t)page * a.m.page_stride + line * hd;
-        if (E8) {
-          const int e = e4m3_exponent(amax);
-          const float inv = pow2f(-e);  // |e| <= 126: a normal number, the scaling is exact
-          uint8_t* dst = (uint8_t*)(isv ? a.v : a.k) + at;
-          *reinterpret_cast<uint2*>(dst + 8 * gl) = e4m3_row8(x[n], inv);
-          *reinterpret_cast<uint2*>(dst + half + 8 * gl) = e4m3_row8(y[n], inv);
-          if (gl == 0) (isv ? a.vs : a.ks)[(int64_t)page * a.m.scale_stride + line] = pow2f(e);
-        } else {
-          T* dst = (T*)(isv ? a.v : a.k) + at;
-          store8(dst + 8 * gl, true, x[n]);
-          store8(dst + half + 8 * gl, true, y[n]);
-        }
+        const int e = e4m3_exponent(amax);
+        const float inv = pow2f(-e);  // |e| <= 126: a normal number, the scaling is exact
+        uint8_t* dst = (uint8_t*)(isv ? a.v : a.k) + at;
+        *reinterpret_cast<uint2*>(dst + 8 * gl) = e4m3_row8(f, inv);
+        *reinterpret_cast<uint2*>(dst + half + 8 * gl) = e4m3_row8(g, inv);
+        if (gl == 0) (isv ? a.vs : a.ks)[(int64_t)page * a.m.scale_stride + line] = pow2f(e);
+      } else {
+        T* dst = (T*)(isv ? a.v : a.k) + at;
+        store8(dst + 8 * gl, true, f);
+        store8(dst + half + 8 * gl, true, g);
       }
     }
   }
@@ -342,17 +369,17 @@ extern "C" int dmtp_paged_write(const dmtp_paged_kv* c, const dmtp_paged_rows* r
                              r->q ? r->q_row : 0, r->q ? r->q_head : 0, r->q ? r->qo_row : 0, r->q ? r->qo_head : 0};
   for (int64_t x : strides) a.wide = a.wide && mult(x * es, 16);
   for (const void* p : {r->k, r->v, r->q, (const void*)r->q_out}) a.wide = a.wide && aligned_to(p, 16);
-  // few rows: their heads spread over CTAs, one a group; many: a row's heads in one CTA
+  // few rows: one a CTA, its heads spread over CTAs, one a group; many: four rows a CTA
   const int items = (r->q ? r->n_heads : 0) + 2 * c->n_kv_heads, ng = 256 / a.group;
   const int blocks = (items + ng - 1) / ng;
   const bool few = r->n_rows < 304;
-  const dim3 grid(r->n_rows, few ? (blocks < 65535 ? blocks : 65535) : 1);
+  const dim3 grid(few ? r->n_rows : (r->n_rows + 3) / 4, few ? (blocks < 65535 ? blocks : 65535) : 1);
   const Turns* t = r->rope_theta > 0.f ? &turns_of(r->rope_theta, hd) : nullptr;
   static const Turns none = {};
   auto k = few ? (c->dtype ? (c->e4m3 ? k_paged_write<bf16, true, 1> : k_paged_write<bf16, false, 1>)
                            : (c->e4m3 ? k_paged_write<float, true, 1> : k_paged_write<float, false, 1>))
-               : (c->dtype ? (c->e4m3 ? k_paged_write<bf16, true, 2> : k_paged_write<bf16, false, 2>)
-                           : (c->e4m3 ? k_paged_write<float, true, 2> : k_paged_write<float, false, 2>));
+               : (c->dtype ? (c->e4m3 ? k_paged_write<bf16, true, 4> : k_paged_write<bf16, false, 4>)
+                           : (c->e4m3 ? k_paged_write<float, true, 4> : k_paged_write<float, false, 4>));
   return launch_op(k, grid, 256, 0, (cudaStream_t)stream, false, 1, a, t ? *t : none) == cudaSuccess
              ? DMTP_OK
              : (cudaGetLastError(), DMTP_ECUDA);

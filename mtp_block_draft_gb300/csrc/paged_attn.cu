@@ -6,59 +6,76 @@ using namespace dmtp;
 
 namespace {
 
-// The merge of the unit that CTA blockIdx.x began and did not end (paged_attn.cuh): with M the
-// largest of the pieces' maxima, out = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c. A CTA takes
-// PER queries: four of them, one a warp, or one, with every fourth piece a warp's and the four
-// sums added in order. It is all latency (the pieces lie in L2), so their rows are asked for
-// eight at a time.
+// The merge of split units (paged_attn.cuh): with M the largest of the pieces' maxima,
+// out = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c. A CTA of 16 warps takes a unit's queries
+// PER at a time: each with 16 / PER warps that take turns on the pieces, whose sums are then added
+// in order. It is all latency (the pieces lie in L2), so a warp asks for its first pieces' rows
+// together with their maxima.
 template <typename T, int PER>
-__global__ void __launch_bounds__(128) k_paged_merge(const PagedAttn p) {
-  __shared__ __align__(16) float part[3][DMTP_OPS_MAX_HEAD_DIM];
+__global__ void __launch_bounds__(512) k_paged_merge(const PagedAttn p, int units) {
+  constexpr int WQ = 16 / PER, AHEAD = 4;
+  __shared__ __align__(16) float part[16][DMTP_OPS_MAX_HEAD_DIM];
   pdl_wait();
-  const int c0 = blockIdx.x, hd = p.m.head_dim, lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  const PagedNote note = p.note[c0];
-  if (note.b < 0) return;
-  const int t = PER == 4 ? blockIdx.y * 4 + wid : blockIdx.y;
-  if (t >= queries_of(p, note.unit)) return;
-  const int c1 = note.last;
-  float M = -INFINITY, L = 0.f;
-  for (int c = c0 + lane; c <= c1; c += 32)
-    M = fmaxf(M, p.part_ml[(c * 2 + (c == c0)) * p.qn + t].x);
-  M = warp_max(M);
-  const float ref = M == -INFINITY ? 0.f : M;
-  for (int c = c0 + lane; c <= c1; c += 32) {
-    const float2 ml = p.part_ml[(c * 2 + (c == c0)) * p.qn + t];
-    L += ml.y * ex2(ml.x - ref);
-  }
-  L = warp_sum(L);
-  const float inv = L != 0.f ? 1.f / L : 0.f;
-  int head, row;
-  query_of(p, note.unit, t, &head, &row);
-  T* out = (T*)p.a.out + (int64_t)note.b * p.a.o_seq + (int64_t)row * p.a.o_row + (int64_t)head * p.a.o_head;
-  for (int d = 4 * lane; d < (hd + 127) / 128 * 128; d += 128) {
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (d < hd) {
-#pragma unroll 8
-      for (int c = c0 + (PER == 4 ? 0 : wid); c <= c1; c += (PER == 4 ? 1 : 4)) {
-        const int at = (c * 2 + (c == c0)) * p.qn + t;
-        const float w = ex2(p.part_ml[at].x - ref);
-        const float4 v = *reinterpret_cast<const float4*>(p.part_o + (int64_t)at * hd + d);
-        o = make_float4(fmaf(w, v.x, o.x), fmaf(w, v.y, o.y), fmaf(w, v.z, o.z), fmaf(w, v.w, o.w));
-      }
-    }
-    if (PER == 1) {
-      if (wid && d < hd) *reinterpret_cast<float4*>(&part[wid - 1][d]) = o;
-      __syncthreads();
-      if (wid) continue;
-      if (d < hd) {
+  const int hd = p.m.head_dim, lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const int turn = wid % WQ, t = blockIdx.y * PER + wid / WQ;
+  for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
+    const PagedNote note = p.note[unit];
+    if (note.last < 0) continue;
+    const int b = unit / p.units, u = unit - b * p.units;
+    const int c0 = note.first, c1 = note.last;
+    const bool live = t < queries_of(p, u);
+    float M = -INFINITY, L = 0.f;
+    auto at = [&](int c) { return (c * 2 + (c == c0)) * p.qn + t; };
+    for (int d0 = 0; d0 < hd; d0 += 128) {
+      const int d = d0 + 4 * lane;
+      float4 ahead[AHEAD];
 #pragma unroll
-        for (int i = 0; i < 3; ++i) {
-          const float4 v = *reinterpret_cast<const float4*>(&part[i][d]);
+      for (int i = 0; i < AHEAD; ++i) {
+        const int c = c0 + turn + i * WQ;
+        ahead[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (live && c <= c1 && d < hd) ahead[i] = *reinterpret_cast<const float4*>(p.part_o + (int64_t)at(c) * hd + d);
+      }
+      if (d0 == 0 && live) {
+#pragma unroll 2
+        for (int c = c0 + lane; c <= c1; c += 32) {
+          const float2 ml = p.part_ml[at(c)];
+          const float n = fmaxf(M, ml.x), ref = n == -INFINITY ? 0.f : n;
+          L = L * ex2(M - ref) + ml.y * ex2(ml.x - ref);
+          M = n;
+        }
+        const float n = warp_max(M), ref = n == -INFINITY ? 0.f : n;
+        L = warp_sum(L * ex2(M - ref));
+        M = ref;
+      }
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      auto add = [&](int c, float4 v) {
+        const float w = ex2(p.part_ml[at(c)].x - M);
+        o = make_float4(fmaf(w, v.x, o.x), fmaf(w, v.y, o.y), fmaf(w, v.z, o.z), fmaf(w, v.w, o.w));
+      };
+      if (live && d < hd) {
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+          if (c0 + turn + i * WQ <= c1) add(c0 + turn + i * WQ, ahead[i]);
+#pragma unroll 4
+        for (int c = c0 + turn + AHEAD * WQ; c <= c1; c += WQ)
+          add(c, *reinterpret_cast<const float4*>(p.part_o + (int64_t)at(c) * hd + d));
+        *reinterpret_cast<float4*>(&part[wid][d]) = o;
+      }
+      __syncthreads();
+      if (turn == 0 && live && d < hd) {
+#pragma unroll
+        for (int i = 1; i < WQ; ++i) {
+          const float4 v = *reinterpret_cast<const float4*>(&part[wid + i][d]);
           o = make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w);
         }
+        int head, row;
+        query_of(p, u, t, &head, &row);
+        T* out = (T*)p.a.out + (int64_t)b * p.a.o_seq + (int64_t)row * p.a.o_row + (int64_t)head * p.a.o_head;
+        const float inv = L != 0.f ? 1.f / L : 0.f;
+        store_act4(out + d, 0, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
       }
+      __syncthreads();  // part is free again
     }
-    if (d < hd) store_act4(out + d, 0, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
   }
 }
 
@@ -97,7 +114,7 @@ int plan(const dmtp_paged_kv* c, const dmtp_paged_query* a, PagedPlan* pl) {
   pl->part_o = 0;
   pl->part_ml = up256(parts * hd * 4);
   pl->note = pl->part_ml + up256(parts * 8);
-  pl->bytes = pl->note + up256((size_t)pl->grid * sizeof(PagedNote));
+  pl->bytes = pl->note + up256((size_t)units * sizeof(PagedNote));
   return DMTP_OK;
 }
 
@@ -155,12 +172,19 @@ extern "C" int dmtp_paged_attention(const dmtp_paged_kv* c, const dmtp_paged_que
   cudaError_t le = pl.tc ? paged_attn_tc(p, pl, c->e4m3 != 0, st)
                          : paged_attn_simt(p, pl, c->dtype, c->e4m3 != 0, st);
   if (le == cudaSuccess && !pl.whole) {
-    const int nq = p.nq < pl.qn ? p.nq : pl.qn;
-    const bool four = nq > 8;
-    const dim3 grid(pl.grid, four ? (nq + 3) / 4 : nq);
-    auto k = c->dtype ? (four ? k_paged_merge<bf16, 4> : k_paged_merge<bf16, 1>)
-                      : (four ? k_paged_merge<float, 4> : k_paged_merge<float, 1>);
-    le = launch_op(k, grid, 128, 0, st, true, 1, p);
+    const int nq = p.nq < pl.qn ? p.nq : pl.qn, units = p.units * c->n_seqs;
+    // a CTA's 16 warps go by the pieces that a unit has on average, and one more
+    const int pieces = pl.grid / units + 1, per = pieces > 24 ? 1 : pieces > 6 ? 4 : nq > 8 ? 16 : 8;
+    const dim3 grid(units < 1216 ? units : 1216, (nq + per - 1) / per);
+    auto k = c->dtype ? (per == 1   ? k_paged_merge<bf16, 1>
+                         : per == 4 ? k_paged_merge<bf16, 4>
+                         : per == 8 ? k_paged_merge<bf16, 8>
+                                    : k_paged_merge<bf16, 16>)
+                      : (per == 1   ? k_paged_merge<float, 1>
+                         : per == 4 ? k_paged_merge<float, 4>
+                         : per == 8 ? k_paged_merge<float, 8>
+                                    : k_paged_merge<float, 16>);
+    le = launch_op(k, grid, 512, 0, st, true, 1, p, units);
   }
   return le == cudaSuccess ? DMTP_OK : (cudaGetLastError(), DMTP_ECUDA);
 }

@@ -13,8 +13,8 @@
 // the same number of tiles whatever the lengths, which only the device knows, and the grid is
 // fixed, so a call can be captured. A CTA's part of one unit is a piece. A piece that is a whole
 // unit writes its output rows; any other leaves (max, sum, O) in the workspace, in slot 0 of its
-// CTA if an earlier CTA began the unit, else in slot 1 (the unit is then the CTA's last), with a
-// note of the unit and its last CTA; the merge kernel joins each noted unit's pieces in order.
+// CTA if an earlier CTA began the unit, else in slot 1 (the unit is then the CTA's last). The CTA
+// that begins a unit notes which CTAs have its pieces, and the merge kernel joins them in order.
 // Sequences without a tile get their zeros from CTA b % G.
 #pragma once
 
@@ -27,7 +27,7 @@ namespace dmtp {
 constexpr int kWholeReach = 1024;
 
 struct PagedNote {
-  int b, unit, last, pad;  // a split unit that begins in this CTA, and its last CTA; b < 0: none
+  int first, last;  // the CTAs of a unit's pieces; last < 0: nothing to join
 };
 
 struct PagedAttn {
@@ -39,7 +39,7 @@ struct PagedAttn {
   int group, nq, qn, chunks, units;  // queries per kv head; of a unit; units of a sequence
   float* part_o;                     // [G][2][qn][head_dim]
   float2* part_ml;                   // [G][2][qn] (max in base 2, sum)
-  PagedNote* note;                   // [G]; null: whole units
+  PagedNote* note;                   // [n_seqs units]; null: whole units
   float scale2;                      // scale log2(e)
 };
 
@@ -151,6 +151,8 @@ __device__ __forceinline__ Tiles my_tiles(const PagedAttn& p, Deal& d, int threa
     if (raw > p.m.reach && threadIdx.x == 0) set_err(p.err, DMTP_OPS_ERR_POS);
     if (raw > 0) continue;
     const int hd = p.m.head_dim;
+    if (p.note)
+      for (int i = threadIdx.x; i < p.units; i += threads) p.note[b * p.units + i] = PagedNote{0, -1};
     for (int i = threadIdx.x; i < p.a.rows * p.a.n_heads * hd; i += threads) {
       const int rh = i / hd, row = rh / p.a.n_heads;
       ((T*)p.a.out)[(int64_t)b * p.a.o_seq + (int64_t)row * p.a.o_row +
@@ -159,12 +161,11 @@ __device__ __forceinline__ Tiles my_tiles(const PagedAttn& p, Deal& d, int threa
   }
   return w;
 }
-// Once per CTA of a split call: the unit that it begins and does not end. pos: the unit's first
-// tile among all; one thread.
-__device__ __forceinline__ void leave_note(const PagedAttn& p, const Deal& d, const Tiles& w, bool some) {
-  PagedNote n = {-1, 0, 0, 0};
-  if (some) n = {w.b, w.unit, d.owner(w.pos + w.n - 1), 0};
-  p.note[blockIdx.x] = n;
+// The note of the unit that begins at w, by one thread of the CTA that begins it.
+__device__ __forceinline__ void leave_note(const PagedAttn& p, const Deal& d, const Tiles& w) {
+  if (!p.note) return;
+  const int last = d.owner(w.pos + w.n - 1), first = blockIdx.x;
+  p.note[w.b * p.units + w.unit] = PagedNote{first, last == first ? -1 : last};
 }
 
 // Output row of query t of a unit: query head and row.

@@ -108,7 +108,6 @@ __global__ void __launch_bounds__(kThreads) k_paged_attn_simt(const PagedAttn p)
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   Deal deal;
   Tiles w = my_tiles<T>(p, deal, kThreads);
-  bool noted = false;
 
   while (w.pos < w.end) {
     const int len = w.len, first = w.first, n = w.n, unit = w.unit, t0 = w.t;
@@ -254,14 +253,10 @@ __global__ void __launch_bounds__(kThreads) k_paged_attn_simt(const PagedAttn p)
         }
       }
     }
-    if (t0 == 0 && t1 < n) {
-      noted = true;
-      if (tid == 0) leave_note(p, deal, w, true);
-    }
+    if (t0 == 0 && tid == 0) leave_note(p, deal, w);
     w.skip(p, t1 - t0);
     __syncthreads();
   }
-  if (p.note && !noted && tid == 0) leave_note(p, deal, w, false);
 }
 
 template <typename T, typename S, int NI>

@@ -3,16 +3,20 @@
 //
 // One pass over the cached rows bounds it: each byte of K and V feeds at most 64 queries of
 // its kv head (rows x query heads), a few hundred operations. So the warps keep rings of
-// 16-key blocks in flight by 16-byte asynchronous copies (the page of a block looked up a
-// tile ahead, so no copy waits for the table) and work on 16-bit fragments with m16n8k16
+// 16-key blocks in flight by 16-byte asynchronous copies (the pages of the next 32 blocks in one
+// read of the table) and work on 16-bit fragments with m16n8k16
 // products that need no staging beyond the block itself. Keys are the M side and queries the N
 // side of both products (S^T = K Q^T, O^T = V^T P^T), so 8 queries fill an instruction. (The
 // tcgen05 form wants 128 rows of keys and one thread to start each product of the whole CTA;
 // a block would wait for its neighbours, and E4M3 rows would go through shared memory twice.)
 //
 //   QN queries    teams             a team's ring
-//   8, 16, 32     4 of one warp     16 keys a stage, no barrier but the warp's own
-//   64            2 of two warps    each warp 32 queries, 32 keys a stage
+//   8, 16         4 of one warp     16 keys a stage, no barrier but the warp's own
+//   32            2 of two warps    32 keys a stage
+//   64            one of four       64 keys a stage
+//
+// A warp has at most 16 queries: with 32 (and half the conversions of E4M3 rows) only two CTAs fit
+// an SM, and 32 sequences of 2304 E4M3 positions x 64 queries took 77 us instead of V64.
 //
 // Weights 2^(s - m) use a running maximum m per query that moves only when a score passes it
 // by 2^8 (so most blocks skip the rescaling). bf16 caches: P as a bf16 pair (16 bits of each
@@ -33,8 +37,8 @@ constexpr int kThreads = 128;
 
 template <int HD, bool E8, int QN>
 struct Shape {
-  static constexpr int NT = QN >= 32 ? 4 : QN / 8;  // 8-query blocks of a warp
-  static constexpr int QG = QN == 64 ? 2 : 1;       // warps of a team
+  static constexpr int NT = QN == 8 ? 1 : 2;        // 8-query blocks of a warp
+  static constexpr int QG = QN / (8 * NT);          // warps of a team
   static constexpr int KS = 4 / QG;                 // teams
   static constexpr int RB = HD * (E8 ? 1 : 2);      // bytes of a cached row
   static constexpr int NSUB = 4 / KS;         // 16-key blocks of a team in a tile
@@ -42,11 +46,9 @@ struct Shape {
   static constexpr int kStage = NSUB * kBlock;      // of a team
   static constexpr int kPitch = HD + 4;             // floats of a joined row: no conflicts
   static constexpr int kJoin = QN * kPitch * 4 + KS * QN * 8;
-  static constexpr bool QS = NT == 4;               // query fragments in shared memory (the
-                                                    // joined rows' place, until the join)
   static constexpr int kMisc = KS * 8 * NSUB * 4;   // valid rows of the blocks
-  // CTAs of an SM: registers (128 threads x 128, 168 or 255) and a ring of two stages at least
-  static constexpr int CTAS = QN == 8 ? (RB == 256 ? 3 : 4) : QN == 16 ? (HD == 64 ? 4 : 3) : 2;
+  // CTAs of an SM: registers (128 threads x 128 or 168) and a ring of two stages at least
+  static constexpr int CTAS = HD == 64 ? 4 : QN == 8 ? (E8 ? 4 : 3) : E8 || QN == 16 ? 3 : 2;
   static constexpr int kRoom = 228 * 1024 / CTAS - 1024 - kJoin - kMisc;
   static constexpr int NST = kRoom / (KS * kStage) > 8 ? 8 : kRoom / (KS * kStage);
   static constexpr int kSmem = NST * KS * kStage + kJoin + kMisc;
@@ -109,6 +111,8 @@ template <int QG>
 __device__ __forceinline__ void team_sync(int team) {
   if (QG == 1)
     __syncwarp();
+  else if (QG == 4)
+    __syncthreads();
   else
     asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(32 * QG) : "memory");
 }
@@ -125,8 +129,7 @@ struct State {
 // EDGE: some row is not seen by every query.
 template <int HD, bool E8, int NT, bool EDGE>
 __device__ __forceinline__ void block(const PagedAttn& p, State<HD, NT>& z,
-                                      const uint32_t (&qf)[NT == 4 ? 1 : NT][HD / 16][2], const uint4* sq,
-                                      const unsigned char* blk, int jb, unsigned ok) {
+                                      const uint32_t (&qf)[NT][HD / 16][2], const unsigned char* blk, int jb, unsigned ok) {
   constexpr int RB = HD * (E8 ? 1 : 2), KK = HD / 16;
   const int lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3, mi = lane >> 3;
   const uint32_t sK = smem_u32(blk), sV = sK + 16 * RB;
@@ -154,16 +157,8 @@ __device__ __forceinline__ void block(const PagedAttn& p, State<HD, NT>& z,
       }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        uint32_t q[4];
-        if (NT == 4) {
-          const uint4 u = sq[(n * KK + k2) * 16];
-          q[0] = u.x, q[1] = u.y, q[2] = u.z, q[3] = u.w;
-        } else {
-          q[0] = qf[NT == 4 ? 0 : n][k2][0], q[1] = qf[NT == 4 ? 0 : n][k2][1];
-          q[2] = qf[NT == 4 ? 0 : n][k2 + 1][0], q[3] = qf[NT == 4 ? 0 : n][k2 + 1][1];
-        }
-        mma16816<E8>(s[n], a[0], q[0], q[1]);
-        mma16816<E8>(s[n], a[1], q[2], q[3]);
+        mma16816<E8>(s[n], a[0], qf[n][k2][0], qf[n][k2][1]);
+        mma16816<E8>(s[n], a[1], qf[n][k2 + 1][0], qf[n][k2 + 1][1]);
       }
     }
   }
@@ -329,7 +324,6 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, E8, QN>::CTAS) k_paged_att
   extern __shared__ __align__(128) unsigned char smem[];
   float* sO = (float*)(smem + NST * KS * S::kStage);
   float2* sML = (float2*)(sO + QN * S::kPitch);
-  uint4* sQ = (uint4*)sO;
   uint32_t* sOk = (uint32_t*)(sML + KS * QN);
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, g = lane >> 2, tq = lane & 3;
   const int team = wid / QG, qg = wid % QG;
@@ -338,24 +332,27 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, E8, QN>::CTAS) k_paged_att
   pdl_trigger();
   Deal deal;
   Tiles cons = my_tiles<bf16>(p, deal, kThreads);
-  bool noted = false;
-  if (cons.pos >= cons.end) {
-    if (p.note && tid == 0) leave_note(p, deal, cons, false);
-    return;
-  }
+  if (cons.pos >= cons.end) return;
   Tiles prod = cons;
 
   // ---- copies: a team brings the blocks team + KS i of every tile ----
-  constexpr int CPR = RB / 16, RPI = 32 * QG / CPR, NI = 16 / RPI;  // rows of one copy of the team
+  constexpr int CPR = RB / 16, RPI = 32 * QG / CPR, NI = RPI < 16 ? 16 / RPI : 1;  // rows of one copy of the team
+  const bool copies = RPI <= 16 || (qg * 32 + lane) / CPR < 16;  // (a team may be larger than a block)
   const bool paged16 = p.m.page_size % 16 == 0;  // a block lies in one page
-  int page[NSUB], off[NSUB];  // of the blocks of the next tile to bring: page, first row in it
-  auto look_up = [&]() {
-#pragma unroll
-    for (int i = 0; i < NSUB; ++i) {
-      const int j = prod.first + prod.t * 64 + (team + KS * i) * 16;
-      page[i] = -1;
-      if (paged16 && prod.pos < prod.end && j < prod.len) page[i] = page_of(p.m, prod.b, j, off[i], p.err);
-    }
+  // Cached rows pass through L2 once (unless several chunks read them): the tables, lengths and
+  // partial results should outlive them there.
+  const uint64_t stream = p.chunks > 1 ? policy_evict_normal() : policy_evict_first();
+  // Pages of this team's blocks, 32 of them at a time: lane i holds the block of tile
+  // win_t + i / NSUB, number i % NSUB, of sequence win_b. One table read serves them all.
+  int win_b = -1, win_t = 0, win_page = -1, win_off = 0;
+  auto look_up = [&]() {  // the window holds the next tile to bring
+    if (prod.pos >= prod.end || (prod.b == win_b && prod.t >= win_t && prod.t < win_t + 32 / NSUB)) return;
+    win_b = prod.b;
+    win_t = prod.t;
+    const int j = prod.first + (win_t + lane / NSUB) * 64 + (team + KS * (lane % NSUB)) * 16;
+    win_page = -1;
+    // (no further than this CTA's tiles: pages that others read are theirs to report)
+    if (paged16 && j < prod.len && lane / NSUB < prod.end - prod.pos) win_page = page_of(p.m, prod.b, j, win_off, p.err);
   };
   int stage_in = 0;
   auto produce = [&]() {
@@ -370,25 +367,40 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, E8, QN>::CTAS) k_paged_att
         int rows = min(16, prod.len - jb);
         unsigned ok;
         if (paged16) {
-          if (page[i] < 0) rows = 0;
+          const int src_lane = (prod.t - win_t) * NSUB + i;
+          const int page = __shfl_sync(0xffffffffu, win_page, src_lane);
+          const int off = __shfl_sync(0xffffffffu, win_off, src_lane);
+          if (page < 0) rows = 0;
           ok = rows >= 16 ? 0xffffu : rows > 0 ? (1u << rows) - 1 : 0u;
-          const int64_t line = (int64_t)kvh * p.m.page_size + (rows > 0 ? off[i] : 0);
-          const int64_t pg = rows > 0 ? page[i] : 0;
+          const int64_t line = (int64_t)kvh * p.m.page_size + (rows > 0 ? off : 0);
+          const int64_t pg = rows > 0 ? page : 0;
           const int64_t at = (pg * p.m.page_stride + line * HD) * (E8 ? 1 : 2) + tl * 16;
           const char *ka = (const char*)p.k + at, *va = (const char*)p.v + at;
+          const int64_t sat = pg * p.m.scale_stride + line + (lane & 15);
+          if (rows >= 16) {
 #pragma unroll
-          for (int x = 0; x < NI; ++x) {
-            const int r = x * RPI + rin, bytes = r < rows ? 16 : 0;
-            const uint32_t d = dst + tile_at<RB>(r, c);
+            for (int x = 0; x < NI; ++x) {
+              if (!copies) break;
+              const uint32_t d = dst + tile_at<RB>(x * RPI + rin, c);
+              cp_async16_hint(d, ka + x * (512 * QG), stream);
+              cp_async16_hint(d + 16 * RB, va + x * (512 * QG), stream);
+            }
+            if (E8 && qg == 0) cp_async4(dst + 32 * RB + lane * 4, (lane < 16 ? p.ks : p.vs) + sat, 4);
+          } else {
             // (a row that is not there is not read: its address is that of one that is)
-            cp_async16(d, bytes ? ka + x * (512 * QG) : (const char*)p.k, bytes);
-            cp_async16(d + 16 * RB, bytes ? va + x * (512 * QG) : (const char*)p.v, bytes);
-          }
-          if (E8 && qg == 0) {
-            const int64_t sat = pg * p.m.scale_stride + line + (lane & 15);
-            const float* src = (lane < 16 ? p.ks : p.vs);
-            const bool there = (lane & 15) < rows;
-            cp_async4(dst + 32 * RB + lane * 4, there ? src + sat : src, there ? 4 : 0);
+#pragma unroll
+            for (int x = 0; x < NI; ++x) {
+              if (!copies) break;
+              const int r = x * RPI + rin, bytes = r < rows ? 16 : 0;
+              const uint32_t d = dst + tile_at<RB>(r, c);
+              cp_async16(d, bytes ? ka + x * (512 * QG) : (const char*)p.k, bytes);
+              cp_async16(d + 16 * RB, bytes ? va + x * (512 * QG) : (const char*)p.v, bytes);
+            }
+            if (E8 && qg == 0) {
+              const float* src = (lane < 16 ? p.ks : p.vs);
+              const bool there = (lane & 15) < rows;
+              cp_async4(dst + 32 * RB + lane * 4, there ? src + sat : src, there ? 4 : 0);
+            }
           }
         } else {
           const int j = jb + (lane & 15);
@@ -407,7 +419,8 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, E8, QN>::CTAS) k_paged_att
 #pragma unroll
           for (int x = 0; x < NI; ++x) {
             const int r = x * RPI + rin;
-            const int64_t a = __shfl_sync(0xffffffffu, at, r);
+            const int64_t a = __shfl_sync(0xffffffffu, at, r & 15);
+            if (!copies) break;
             const int bytes = a < 0 ? 0 : 16;
             const int64_t src = a < 0 ? 0 : a + c * 16;
             const uint32_t d = dst + tile_at<RB>(r, c);
@@ -434,33 +447,34 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, E8, QN>::CTAS) k_paged_att
     const int t0 = cons.t, t1 = min(cons.n, t0 + cons.end - cons.pos);
     const int nq = queries_of(p, cons.unit);
     State<HD, NT> z;
-    uint32_t qf[S::QS ? 1 : NT][KK][2];
+    // B fragments of Q^T: query g, columns 2 tq.. in the products' order, or, as the bytes of
+    // an E4M3 K come, four consecutive ones
+    uint32_t qf[NT][KK][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      uint32_t f[KK][2];
-      const int q0 = (qg * NT + n) * 8;
-      const bf16* qp = nullptr;
+      const int t = (qg * NT + n) * 8 + g;
       int head, row;
-      if (q0 + g < nq) {
-        query_of(p, cons.unit, q0 + g, &head, &row);
-        qp = (const bf16*)p.a.q + (int64_t)cons.b * p.a.q_seq + (int64_t)row * p.a.q_row + (int64_t)head * p.a.q_head;
-      }
-      // B fragments of Q^T: query g, columns 2 tq.. in the products' order, or, as the bytes of
-      // an E4M3 K come, four consecutive ones
+      query_of(p, cons.unit, t, &head, &row);
+      const bf16* qp = (const bf16*)p.a.q + (int64_t)cons.b * p.a.q_seq + (int64_t)row * p.a.q_row + (int64_t)head * p.a.q_head;
 #pragma unroll
       for (int k = 0; k < KK; ++k) {
-        f[k][0] = f[k][1] = 0;
-        if (qp) {
+        qf[n][k][0] = qf[n][k][1] = 0;
+        if (t < nq) {
           if (E8) {
             const uint2 u = *reinterpret_cast<const uint2*>(qp + 16 * k + 4 * tq);
-            f[k][0] = u.x;
-            f[k][1] = u.y;
+            qf[n][k][0] = u.x;
+            qf[n][k][1] = u.y;
           } else {
-            f[k][0] = *reinterpret_cast<const uint32_t*>(qp + 16 * k + 2 * tq);
-            f[k][1] = *reinterpret_cast<const uint32_t*>(qp + 16 * k + 8 + 2 * tq);
+            qf[n][k][0] = *reinterpret_cast<const uint32_t*>(qp + 16 * k + 2 * tq);
+            qf[n][k][1] = *reinterpret_cast<const uint32_t*>(qp + 16 * k + 8 + 2 * tq);
           }
         }
       }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int q0 = (qg * NT + n) * 8;
+      int head, row;
       float down = p.scale2;
       if (E8) {  // bf16 -> fp16, the query's largest magnitude brought into [2^12, 2^13)
         uint32_t big = 0;
@@ -468,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, E8, QN>::CTAS) k_paged_att
         for (int k = 0; k < KK; ++k)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const uint32_t a = f[k][i] << 16 & 0x7fff0000u, b = f[k][i] & 0x7fff0000u;
+            const uint32_t a = qf[n][k][i] << 16 & 0x7fff0000u, b = qf[n][k][i] & 0x7fff0000u;
             if (a < 0x7f800000u) big = max(big, a);
             if (b < 0x7f800000u) big = max(big, b);
           }
@@ -482,16 +496,8 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, E8, QN>::CTAS) k_paged_att
         for (int k = 0; k < KK; ++k)
 #pragma unroll
           for (int i = 0; i < 2; ++i)
-            f[k][i] = pack_f16(__uint_as_float(f[k][i] << 16) * up,
-                                   __uint_as_float(f[k][i] & 0xffff0000u) * up);
-      }
-      if (!S::QS) {
-#pragma unroll
-        for (int k = 0; k < KK; ++k) qf[S::QS ? 0 : n][k][0] = f[k][0], qf[S::QS ? 0 : n][k][1] = f[k][1];
-      } else if (team == 0) {  // two products' fragments side by side
-#pragma unroll
-        for (int k = 0; k < KK; k += 2)
-          sQ[((qg * NT + n) * KK + k) * 16 + lane] = make_uint4(f[k][0], f[k][1], f[k + 1][0], f[k + 1][1]);
+            qf[n][k][i] = pack_f16(__uint_as_float(qf[n][k][i] << 16) * up,
+                                   __uint_as_float(qf[n][k][i] & 0xffff0000u) * up);
       }
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
@@ -508,9 +514,6 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, E8, QN>::CTAS) k_paged_att
       for (int i = 0; i < KK; ++i) z.o[n][i][0] = z.o[n][i][1] = z.o[n][i][2] = z.o[n][i][3] = 0.f;
     }
 
-    if (S::QS) __syncthreads();
-    const uint4* sq = S::QS ? sQ + qg * NT * KK * 16 + lane : nullptr;
-
     for (int t = t0; t < t1; ++t) {
       cp_async_wait<NST - 2>();
       team_sync<QG>(team);  // this stage is here; the one before has been used
@@ -521,9 +524,9 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, E8, QN>::CTAS) k_paged_att
         const unsigned ok = sOk[stage * NSUB + i];
         const int jb = cons.first + t * 64 + (team + KS * i) * 16;
         if (ok == 0xffffu && jb + 15 <= cons.len - p.a.rows && (p.a.window <= 0 || jb >= cons.len - p.a.window))
-          block<HD, E8, NT, false>(p, z, qf, sq, blk, jb, ok);
+          block<HD, E8, NT, false>(p, z, qf, blk, jb, ok);
         else if (ok)
-          block<HD, E8, NT, true>(p, z, qf, sq, blk, jb, ok);
+          block<HD, E8, NT, true>(p, z, qf, blk, jb, ok);
       }
       stage = stage + 1 == NST ? 0 : stage + 1;
     }
@@ -604,14 +607,10 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, E8, QN>::CTAS) k_paged_att
         if (d == 0) p.part_ml[slot + q] = make_float2(M, L);
       }
     }
-    if (!whole && t0 == 0) {
-      noted = true;
-      if (tid == 0) leave_note(p, deal, cons, true);
-    }
+    if (t0 == 0 && tid == 0) leave_note(p, deal, cons);
     cons.skip(p, t1 - t0);
-    __syncthreads();  // sO, sML and sQ are free again
+    __syncthreads();  // sO and sML are free again
   }
-  if (p.note && !noted && tid == 0) leave_note(p, deal, cons, false);
   cp_async_wait<0>();
 }
 
@@ -640,7 +639,7 @@ namespace dmtp {
 int paged_tc_grid(int head_dim, bool e8, int qn) {
 #define DMTP_CTAS(HD_, E8_)                                                           \
   (qn == 8 ? Shape<HD_, E8_, 8>::CTAS : qn == 16 ? Shape<HD_, E8_, 16>::CTAS          \
-                                      : Shape<HD_, E8_, 32>::CTAS)
+                                      : qn == 32 ? Shape<HD_, E8_, 32>::CTAS : Shape<HD_, E8_, 64>::CTAS)
   return 152 * (head_dim == 64 ? (e8 ? DMTP_CTAS(64, true) : DMTP_CTAS(64, false))
                                : (e8 ? DMTP_CTAS(128, true) : DMTP_CTAS(128, false)));
 #undef DMTP_CTAS

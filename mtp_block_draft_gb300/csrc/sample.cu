@@ -176,10 +176,10 @@ struct Shared {
   unsigned long long table[256];
 };
 
-template <int THREADS>
+template <int THREADS, typename S>
 struct Cluster {
   static constexpr int kWarps = THREADS / 32;
-  Shared<THREADS>* s;
+  S* s;
   unsigned rank, size;
   int phase;
 
@@ -201,8 +201,8 @@ struct Cluster {
     sync();
     return p;
   }
-  // Sums of (a, b) over all threads of the cluster.
-  __device__ __forceinline__ void sum(unsigned long long& a, unsigned long long& b) {
+  // Sums of (a, b) over the CTA, valid in the first warp.
+  __device__ __forceinline__ void cta_sum(unsigned long long& a, unsigned long long& b) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       a += __shfl_xor_sync(0xffffffffu, a, o);
@@ -211,25 +211,31 @@ struct Cluster {
     __syncthreads();
     if ((threadIdx.x & 31) == 0) s->warp[threadIdx.x >> 5][0] = a, s->warp[threadIdx.x >> 5][1] = b;
     __syncthreads();
-    a = b = 0;
     if (threadIdx.x < 32) {
+      a = b = 0;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) a += s->warp[w][0], b += s->warp[w][1];
     }
+  }
+  // Sums of (a, b) over all threads of the cluster.
+  __device__ __forceinline__ void sum(unsigned long long& a, unsigned long long& b) {
+    cta_sum(a, b);
     const int p = exchange(a, b);
     a = b = 0;
     for (unsigned r = 0; r < size; ++r) a += s->slot[p][r][0], b += s->slot[p][r][1];
   }
-  __device__ __forceinline__ uint32_t max(uint32_t a) {
+  __device__ __forceinline__ uint32_t cta_max(uint32_t a) {
     a = __reduce_max_sync(0xffffffffu, a);
     __syncthreads();
     if ((threadIdx.x & 31) == 0) s->warp[threadIdx.x >> 5][0] = a;
     __syncthreads();
-    if (threadIdx.x < 32) {
+    a = 0;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) a = ::max(a, (uint32_t)s->warp[w][0]);
-    }
-    const int p = exchange(a, 0);
+    for (int w = 0; w < kWarps; ++w) a = ::max(a, (uint32_t)s->warp[w][0]);
+    return a;
+  }
+  __device__ __forceinline__ uint32_t max(uint32_t a) {
+    const int p = exchange(cta_max(a), 0);
     a = 0;
     for (unsigned r = 0; r < size; ++r) a = ::max(a, (uint32_t)s->slot[p][r][0]);
     return a;
@@ -296,13 +302,47 @@ struct Cluster {
     before = s->found[1];
     own = s->found[2];
   }
+  // The neighbourhood of top-p's cut: the bins (of `all`, bin `first` centred at the largest
+  // weight, no more than last_n of last_bin and none after it) at which the running weight is
+  // about top_p of all, into s->bins. All threads call it.
+  __device__ __forceinline__ void neighbours(float top_p, int last_bin, unsigned long long last_n, float first) {
+    constexpr int N = kBins / THREADS;
+    float m[N], sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      const int i = threadIdx.x * N + e;
+      const unsigned long long c = s->all[i];
+      m[e] = i < last_bin ? (float)c : i == last_bin ? (float)(c < last_n ? c : last_n) : 0.f;
+      m[e] *= ex2(((first - (float)i)) * 0.03125f);
+      sum += m[e];
+    }
+    if (threadIdx.x == 0) s->bins[0] = s->bins[1] = last_bin;
+    unsigned long long total;  // in 2^-24
+    const unsigned long long at = scan((unsigned long long)(sum * 16777216.f), total);
+    // a weight taken at its bin's centre is off by 1.1% at most, 0.6% in the mean square, and the
+    // errors of the many weights of a flat row average out
+    const float p = fmaxf(top_p, 0.f) * (float)total;
+    const float wide = fminf(0.023f, 0.0005f + 0.025f * rsqrtf((float)total * 5.9604645e-8f));
+    float run = (float)at;
+    int lo_b = kBins, hi_b = kBins;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      run += m[e] * 16777216.f;
+      if (run >= p * (1.f - wide)) lo_b = min(lo_b, (int)threadIdx.x * N + e);
+      if (run >= p * (1.f + wide)) hi_b = min(hi_b, (int)threadIdx.x * N + e);
+    }
+    if (lo_b <= last_bin) atomicMin(&s->bins[0], lo_b);
+    if (hi_b <= last_bin) atomicMin(&s->bins[1], hi_b);
+    __syncthreads();
+  }
   // 2^-44 weights as three 15-bit parts and a count in bins of the histogram: 32-bit sums hold
   // the 2^16 logits a CTA has at most.
   __device__ __forceinline__ void add_fine(int i, unsigned long long w) {
-    atomicAdd(&s->hist[i], 1u);
-    atomicAdd(&s->hist[kFine + i], (uint32_t)w & 0x7fffu);
-    atomicAdd(&s->hist[2 * kFine + i], (uint32_t)(w >> 15) & 0x7fffu);
-    atomicAdd(&s->hist[3 * kFine + i], (uint32_t)(w >> 30));
+    uint32_t* h = &s->hist[4 * i];
+    atomicAdd(h, 1u);
+    atomicAdd(h + 1, (uint32_t)w & 0x7fffu);
+    atomicAdd(h + 2, (uint32_t)(w >> 15) & 0x7fffu);
+    atomicAdd(h + 3, (uint32_t)(w >> 30));
   }
 };
 
@@ -332,7 +372,7 @@ __global__ void __launch_bounds__(THREADS) k_sample_rows(const RowsArgs sa) {
   const dmtp_sample_args& a = sa.a;
   unsigned size;
   asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(size));
-  Cluster<THREADS> cl{&sh, cluster_rank(), size, 0};
+  Cluster<THREADS, Sh> cl{&sh, cluster_rank(), size, 0};
   const int row = blockIdx.x / size, tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const int V = a.vocab, slice = sa.slice, E = slice / THREADS;
   const int base = (int)cl.rank * slice;
@@ -440,37 +480,7 @@ __global__ void __launch_bounds__(THREADS) k_sample_rows(const RowsArgs sa) {
       want -= before;
       last_n = want;
     }
-    if (by_p) {
-      // the neighbourhood of top-p's cut: bins whose running weight is about top_p of all
-      constexpr int BE = kBins / THREADS;
-      float m[BE], sum = 0.f;
-#pragma unroll
-      for (int e = 0; e < BE; ++e) {
-        const int i = tid * BE + e;
-        const unsigned long long c = sh.all[i];
-        m[e] = i < last_bin ? (float)c : i == last_bin ? (float)(c < last_n ? c : last_n) : 0.f;
-        m[e] *= ex2(-(float)i * 0.03125f);
-        sum += m[e];
-      }
-      if (tid == 0) sh.bins[0] = sh.bins[1] = last_bin;
-      unsigned long long total;  // in 2^-24
-      const unsigned long long at = cl.scan((unsigned long long)(sum * 16777216.f), total);
-      // a weight taken at its bin's centre is off by 1.1% at most, 0.6% in the mean square,
-      // and the errors of the many weights of a flat row average out
-      const float p = fmaxf(top_p, 0.f) * (float)total;
-      const float wide = fminf(0.023f, 0.0005f + 0.025f * rsqrtf((float)total * 5.9604645e-8f));
-      float run = (float)at;
-      int lo_b = kBins, hi_b = kBins;
-#pragma unroll
-      for (int e = 0; e < BE; ++e) {
-        run += m[e] * 16777216.f;
-        if (run >= p * (1.f - wide)) lo_b = min(lo_b, tid * BE + e);
-        if (run >= p * (1.f + wide)) hi_b = min(hi_b, tid * BE + e);
-      }
-      if (lo_b <= last_bin) atomicMin(&sh.bins[0], lo_b);
-      if (hi_b <= last_bin) atomicMin(&sh.bins[1], hi_b);
-      __syncthreads();
-    }
+    if (by_p) cl.neighbours(top_p, last_bin, last_n, 0.f);
     if (by_k) {
       if (wid < 2) {
         const int b = wid ? last_bin - 1 : last_bin;
@@ -577,16 +587,15 @@ __global__ void __launch_bounds__(THREADS) k_sample_rows(const RowsArgs sa) {
 #pragma unroll
       for (int e = 0; e < FE; ++e) {
         const int i = tid * FE + e;
-        m[e] = i < kFine ? (unsigned long long)sh.all[kFine + i] + ((unsigned long long)sh.all[2 * kFine + i] << 15) +
-                               ((unsigned long long)sh.all[3 * kFine + i] << 30)
-                         : 0ull;
+        const uint32_t* c = sh.all + 4 * i;
+        m[e] = i < kFine ? (unsigned long long)c[1] + ((unsigned long long)c[2] << 15) + ((unsigned long long)c[3] << 30) : 0ull;
         mine_m += m[e];
       }
       unsigned long long at = above + cl.scan(mine_m, total);
 #pragma unroll
       for (int e = 0; e < FE; ++e) {
         if (at < goal && goal <= at + m[e])
-          sh.found[0] = tid * FE + e, sh.found[1] = at, sh.found[2] = sh.all[tid * FE + e], sh.found[3] = m[e];
+          sh.found[0] = tid * FE + e, sh.found[1] = at, sh.found[2] = sh.all[4 * (tid * FE + e)], sh.found[3] = m[e];
         at += m[e];
       }
       __syncthreads();
@@ -729,6 +738,461 @@ __global__ void __launch_bounds__(THREADS) k_sample_rows(const RowsArgs sa) {
   cl.sync();
 }
 
+// ---- many rows ------------------------------------------------------------------------
+// With more rows than the GPU holds at once, what every thread does once per row counts as much
+// as what it does per logit, so a row gets only two CTAs of 512 threads, and the logits, too many
+// for their shared memory, are read again from L2 (the rows in flight fit it) for the second
+// pass. Warps take segments of 1024 consecutive ids, whose kept weights the pick searches.
+// The bins of the first pass hang on the largest of the row's first logits (256 bins above it; a
+// row whose later logits are higher still is counted again).
+constexpr int kManyRows = 38;
+constexpr int kStream = 512, kSegment = 1024, kAhead = 256;
+
+struct StreamShared {
+  static constexpr int kWarps = kStream / 32, kSlots = 16;
+  uint32_t hist[kBins], all[kBins];
+  unsigned long long slot[2][16][2];
+  unsigned long long warp[kWarps][2];
+  unsigned long long found[4];
+  unsigned long long table[256];
+  unsigned long long seg[DMTP_OPS_MAX_SAMPLE_VOCAB / 2 / kSegment];  // kept weight of a segment
+  uint32_t seg_n[DMTP_OPS_MAX_SAMPLE_VOCAB / 2 / kSegment];          // ties of the cut in it
+  uint8_t list[kSlots][kStream];
+  uint32_t edge[3];
+  int bins[2];
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kStream, 2) k_sample_stream(const RowsArgs sa) {
+  using Sh = StreamShared;
+  constexpr int X = 16 / sizeof(T), J = 32 / X;  // ids of a load, loads of a thread and segment
+  extern __shared__ __align__(16) unsigned char smem[];
+  Sh& sh = *reinterpret_cast<Sh*>(smem);
+  const dmtp_sample_args& a = sa.a;
+  unsigned size;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(size));
+  Cluster<kStream, Sh> cl{&sh, cluster_rank(), size, 0};
+  const int row = blockIdx.x / size, tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const int base = (int)cl.rank * sa.slice, end = min(a.vocab, base + sa.slice);
+  const int segs = end > base ? (end - base + kSegment - 1) / kSegment : 0;
+  const T* lg = (const T*)a.logits + (int64_t)row * a.ld;
+  // X logits from id on (masked past `end`)
+  auto load = [&](int id, float (&f)[X]) {
+    if (sa.vec && id + X <= end) {
+      const uint4 u = __ldg(reinterpret_cast<const uint4*>(lg + id));
+      const T* t = reinterpret_cast<const T*>(&u);
+#pragma unroll
+      for (int e = 0; e < X; ++e) f[e] = clean(to_f32(t[e]));
+    } else {
+#pragma unroll
+      for (int e = 0; e < X; ++e) f[e] = id + e < end ? clean(to_f32(__ldg(lg + id + e))) : kMasked;
+    }
+  };
+  auto id_of = [&](int seg, int j) { return base + seg * kSegment + j * (32 * X) + lane * X; };
+  auto one = [&](int code) {  // a listed logit of this thread: step, load, element
+    return clean(to_f32(__ldg(lg + id_of((code >> 5) * Sh::kWarps + wid, (code & 31) / X) + code % X)));
+  };
+  const float temp = a.temperature ? __ldg(a.temperature + row) : 1.f;
+  const int k = a.top_k ? __ldg(a.top_k + row) : 0;
+  const float top_p = a.top_p ? __ldg(a.top_p + row) : 1.f;
+  const float min_p = a.min_p ? __ldg(a.min_p + row) : 0.f;
+  const float u = __ldg(a.u + row);
+  const bool greedy = !(temp > 0.f), by_p = top_p < 1.f, binned = !greedy && (k > 0 || by_p);
+  for (int i = tid; i < 256; i += kStream) sh.table[i] = exp2_256th(i);
+  for (int i = tid; i < kBins; i += kStream) sh.hist[i] = 0;
+  for (int i = tid; i < segs; i += kStream) sh.seg[i] = 0, sh.seg_n[i] = 0;
+  Weigh W;
+  W.table = sh.table;
+  const float tt = fmaxf(temp, 1e-30f);
+  W.chi = 1.44269502162933349609f / tt;
+  W.clo = (fmaf(-W.chi, tt, 1.44269502162933349609f) + 1.92596299112661746887e-08f) / tt;
+  W.cb = W.chi * 32.f;
+
+  // the first pass: the largest logit and, for the filters, the bins
+  float from_l = kMasked;  // what the bins hang on: both CTAs look at the same logits
+  if (binned) {
+    float best = kMasked;
+    for (int i = tid; i < min(a.vocab, 2 * kStream); i += kStream) best = fmaxf(best, clean(to_f32(__ldg(lg + i))));
+    from_l = logit_of(cl.cta_max(key_of(best)));
+  }
+  int ahead = kAhead;
+  const float cb = W.cb;
+  // Bin of a logit: (from_l - l) cb to the nearest, `ahead` bins later.
+  auto bin_of = [&](float l) {
+    const float y = fmaxf((l - from_l) * cb, -4096.f);  // (masked: 4096)
+    return ahead - (__float_as_int(fminf(y, 4096.f) + 12582912.f) - 0x4b400000);
+  };
+  uint32_t top = 0;
+  unsigned long long nvalid = 0;
+  while (true) {
+    float best = kMasked;
+    uint32_t last = 0, valid = 0;
+    const bool use = binned && from_l > kMasked;
+    __syncthreads();  // the histogram is clear
+    for (int s = wid; s < segs; s += Sh::kWarps) {
+#pragma unroll 2
+      for (int j = 0; j < J; ++j) {
+        float f[X];
+        load(id_of(s, j), f);
+#pragma unroll
+        for (int e = 0; e < X; ++e) {
+          best = fmaxf(best, f[e]);
+          if (use) {
+            const int b = max(bin_of(f[e]), 0);
+            if (b < kBins - 1)
+              atomicAdd(&sh.hist[b], 1u);
+            else
+              last += f[e] > kMasked;
+          }
+        }
+      }
+    }
+    (void)valid;
+    const uint32_t my_top = cl.cta_max(key_of(best));
+    unsigned long long l64 = last, pad = 0;
+    cl.cta_sum(l64, pad);
+    const int p = cl.exchange(my_top, l64);
+    top = 0;
+    unsigned long long lasts = 0;
+    for (unsigned r = 0; r < size; ++r) {
+      top = max(top, (uint32_t)sh.slot[p][r][0]);
+      lasts += sh.slot[p][r][1];
+    }
+    nvalid = lasts;  // and the bins' counts, below
+    if (!binned || top == key_of(kMasked)) break;
+    if (use && bin_of(logit_of(top)) >= 0) break;
+    // the first logits were far below the largest, or masked: hang the bins on that one
+    from_l = logit_of(top);
+    ahead = 0;
+    cl.sync();
+    for (int i = tid; i < kBins; i += kStream) sh.hist[i] = 0;
+  }
+  W.top = logit_of(top);
+  const bool none = top == key_of(kMasked);
+  if (none || greedy) {
+    uint32_t id = 0;  // of the largest logit, the lowest: 2^32 - 1 - id is maximal
+    if (!none)
+      for (int s = wid; s < segs; s += Sh::kWarps)
+        for (int j = 0; j < J; ++j) {
+          float f[X];
+          load(id_of(s, j), f);
+#pragma unroll
+          for (int e = 0; e < X; ++e)
+            if (f[e] == W.top) id = max(id, 0xffffffffu - (unsigned)(id_of(s, j) + e));
+        }
+    id = cl.cta_max(id);
+    const int p = cl.exchange(id, 0);
+    id = 0;
+    for (unsigned r = 0; r < size; ++r) id = max(id, (uint32_t)sh.slot[p][r][0]);
+    if (cl.rank == 0 && tid == 0) {
+      a.ids[row] = none ? -1 : (int)(0xffffffffu - id);
+      if (a.kept) a.kept[row] = none ? 0 : 1;
+    }
+    cl.sync();  // no CTA leaves while another may still write its slots
+    return;
+  }
+  // the smallest logit that stays, as a key; `ties` of its ids stay, all of them unless `partial`
+  uint32_t cut = 0x00800000u;
+  unsigned long long ties = 0;
+  bool partial = false, by_k = false;
+  // The smallest key of bins 0..b, top + 1 if none is that high. One warp.
+  auto bin_edge = [&](int b) {
+    auto in = [&](float x) { return bin_of(x) <= b; };
+    return b >= kBins - 1 ? 0x00800000u : b >= 0 && in(W.top) ? first_key(top, in) : top + 1;
+  };
+  // every logit in [lo, hi]
+  auto each_in = [&](uint32_t lo, uint32_t hi, auto&& f) {
+    const float lf = logit_of(lo), hf = logit_of(hi);
+    for (int s = wid; s < segs; s += Sh::kWarps)
+#pragma unroll 2
+      for (int j = 0; j < J; ++j) {
+        float x[X];
+        load(id_of(s, j), x);
+#pragma unroll
+        for (int e = 0; e < X; ++e)
+          if (x[e] >= lf && x[e] <= hf) f(x[e]);
+      }
+  };
+
+  if (binned) {
+    constexpr int N = kBins / kStream;
+    cl.sum_hist();
+    unsigned long long n = 0, total, before, cnt, want = k;
+#pragma unroll
+    for (int e = 0; e < N; ++e) n += tid * N + e < kBins - 1 ? sh.all[tid * N + e] : 0u;
+    cl.scan(n, total);
+    if (tid == 0) sh.all[kBins - 1] = (uint32_t)nvalid;  // the last bin was counted by thread
+    nvalid += total;
+    __syncthreads();
+    by_k = k > 0 && (unsigned long long)k < nvalid;
+    int last_bin = kBins - 1;           // the last bin that top-k leaves
+    unsigned long long last_n = ~0ull;  // and how many of its logits
+    if (by_k) {
+      cl.find_count(want, last_bin, before, cnt);
+      want -= before;
+      last_n = want;
+    }
+    if (by_p) cl.neighbours(top_p, last_bin, last_n, (float)bin_of(W.top));
+    if (by_k) {
+      if (wid < 2) {
+        const uint32_t f = bin_edge(wid ? last_bin - 1 : last_bin);
+        if (lane == 0) sh.edge[wid] = wid ? f - 1 : f;
+      }
+      __syncthreads();
+      uint32_t lo = sh.edge[0], hi = sh.edge[1];
+      while (want != cnt && lo != hi) {
+        const int shift = max(0, 32 - __clz((int)(hi - lo)) - 11);
+        each_in(lo, hi, [&](float x) { atomicAdd(&sh.hist[hi - key_of(x) >> shift], 1u); });
+        cl.sum_hist();
+        int f;
+        cl.find_count(want, f, before, cnt);
+        want -= before;
+        hi -= (uint32_t)f << shift;
+        lo = hi - lo < (1u << shift) ? lo : hi - ((1u << shift) - 1);
+      }
+      cut = lo;
+      partial = want != cnt;
+      ties = want;
+    }
+  }
+  const unsigned long long tie_mass = partial ? ties * W(logit_of(cut)) : 0ull;
+  const uint32_t least_key = partial ? cut + 1 : cut;  // below it, only the cut's own ties
+  // the neighbourhood's ends and min_p as keys
+  if (wid < 2 && by_p) {
+    const uint32_t f = bin_edge(wid ? sh.bins[0] - 1 : sh.bins[1]);
+    if (lane == 0) sh.edge[wid] = wid ? f - 1 : f;
+  }
+  if (wid == 2 && min_p > 0.f) {
+    const unsigned long long least = min_p < 1.f ? part_of(min_p, 1ull << kShift, true) : 1ull << kShift;
+    const uint32_t f = first_key(top, [&](float x) { return W(x) >= least; });
+    if (lane == 0) sh.edge[2] = f;
+  }
+  __syncthreads();
+  const uint32_t min_key = min_p > 0.f ? sh.edge[2] : 0u;
+
+  // The weights of a segment's logits, by pairs: f(weight, logit, code).
+  auto weights = [&](int s, int step, float floor_l, auto&& f) {
+#pragma unroll 2
+    for (int j = 0; j < J; ++j) {
+      float x[X];
+      load(id_of(s, j), x);
+#pragma unroll
+      for (int e = 0; e < X; e += 2) {
+        if (!(fmaxf(x[e], x[e + 1]) >= floor_l)) continue;
+        unsigned long long w0, w1;
+        W.two(make_float2(x[e], x[e + 1]), w0, w1);
+        f(w0, x[e], step * 32 + j * X + e);
+        f(w1, x[e + 1], step * 32 + j * X + e + 1);
+      }
+    }
+  };
+  // Add a thread's kept weight to its warp's segment.
+  auto add_segment = [&](int s, unsigned long long m) {
+    const uint32_t lo = __reduce_add_sync(0xffffffffu, (uint32_t)m & 0xffffffu);
+    const uint32_t mid = __reduce_add_sync(0xffffffffu, (uint32_t)(m >> 24) & 0xffffffu);
+    const uint32_t hi = __reduce_add_sync(0xffffffffu, (uint32_t)(m >> 48));
+    if (lane == 0) sh.seg[s] += (unsigned long long)lo + ((unsigned long long)mid << 24) + ((unsigned long long)hi << 48);
+  };
+
+  uint32_t cnt = 0, from = 0xffffffffu;  // kept logits, so far those above `from`
+  int listed = -1;                       // >= 0: the others are in this thread's list, so many
+  if (by_p) {
+    uint32_t lo = max(sh.edge[0], least_key), hi = max(sh.edge[1], lo);
+    // every weight once: all, above the neighbourhood, and a list of the neighbourhood
+    unsigned long long sum = 0, above = 0;
+    int shift = max(0, 32 - __clz((int)(hi - lo)) - 9);
+    from = hi;
+    listed = 0;
+    {
+      const float lf = logit_of(lo), hf = logit_of(hi), cf = by_k ? logit_of(least_key) : kMasked;
+      const bool deep = min_key > hi + 1;  // min_p cuts above the neighbourhood
+      const float mf = logit_of(deep ? min_key : hi + 1);
+      int step = 0;
+      for (int s = wid; s < segs; s += Sh::kWarps, ++step) {
+        unsigned long long mass = 0;
+        weights(s, step, cf, [&](unsigned long long w, float x, int code) {
+          if (by_k && !(x >= cf)) w = 0;
+          sum += w;
+          if (x >= mf) mass += w, ++cnt;
+          if (deep && x > hf) above += w;
+          if (x >= lf && x <= hf) {
+            if (listed < Sh::kSlots) sh.list[listed][tid] = (uint8_t)code;
+            ++listed;
+          }
+        });
+        if (!deep) above += mass;
+        add_segment(s, mass);
+      }
+    }
+    // the first logit from above at which the running weight reaches the goal: finer bins
+    bool moved = false;  // out of the neighbourhood
+    unsigned long long goal = 0;
+    while (true) {
+      if (!moved && listed <= Sh::kSlots) {
+        const float lf = logit_of(lo), hf = logit_of(hi);
+        for (int i = 0; i < listed; ++i) {
+          const float x = one(sh.list[i][tid]);
+          if (x >= lf && x <= hf) cl.add_fine(hi - key_of(x) >> shift, W(x));
+        }
+      }
+      // (a thread whose list overflowed, or a range outside: over its logits again; the loads of
+      // a warp stay together)
+      if (__any_sync(0xffffffffu, moved || listed > Sh::kSlots)) {
+        const bool mine = moved || listed > Sh::kSlots;
+        each_in(lo, hi, [&](float x) {
+          if (mine) cl.add_fine(hi - key_of(x) >> shift, W(x));
+        });
+      }
+      if (!goal) {  // the first time, with the sums
+        cl.cta_sum(sum, above);
+        const int p = cl.exchange(sum, above);
+        sum = tie_mass;
+        above = 0;
+        for (unsigned r = 0; r < size; ++r) sum += sh.slot[p][r][0], above += sh.slot[p][r][1];
+        goal = part_of(fmaxf(top_p, 0.f), sum, true);
+        goal = goal ? goal : 1ull;
+      }
+      cl.sum_hist();
+      const uint32_t* c = sh.all + 4 * tid;
+      const unsigned long long m = (unsigned long long)c[1] + ((unsigned long long)c[2] << 15) + ((unsigned long long)c[3] << 30);
+      unsigned long long total;
+      const unsigned long long at = above + cl.scan(m, total);
+      if (at < goal && goal <= at + m) sh.found[0] = tid, sh.found[1] = at, sh.found[2] = c[0], sh.found[3] = m;
+      __syncthreads();
+      if (above >= goal) {  // the goal lies above this range
+        lo = hi + 1;
+        hi = top;
+        above = 0;
+        moved = true;
+      } else if (above + total < goal) {  // or below it
+        above += total;
+        if (lo <= least_key) {  // only the cut's own ties are left
+          const unsigned long long wc = W(logit_of(cut));
+          const unsigned long long need = wc ? (goal - above + wc - 1) / wc : ties;
+          ties = need < ties ? need : ties;
+          break;
+        }
+        hi = lo - 1;
+        lo = least_key;
+        moved = true;
+      } else {
+        const int f = (int)sh.found[0];
+        above = sh.found[1];
+        hi -= (uint32_t)f << shift;
+        lo = hi - lo < (1u << shift) ? lo : hi - ((1u << shift) - 1);
+        const unsigned long long n = sh.found[2];
+        if (n == 1 || lo == hi) {
+          const unsigned long long wl = n == 1 ? 0ull : sh.found[3] / n;
+          const unsigned long long need = n == 1 ? 1ull : (goal - above + wl - 1) / wl;
+          partial = need < n;
+          ties = need;
+          cut = lo;
+          break;
+        }
+      }
+      shift = max(0, 32 - __clz((int)(hi - lo)) - 9);
+      __syncthreads();  // found has been read
+    }
+    if (moved) {  // the cut came out elsewhere: count again
+      from = 0xffffffffu;
+      cnt = 0;
+      for (int i = tid; i < segs; i += kStream) sh.seg[i] = 0;
+      __syncthreads();
+      listed = -1;
+    }
+  }
+  if (min_key > cut) {  // min_p cuts deeper
+    cut = min_key;
+    partial = false;
+  }
+
+  // what the neighbourhood keeps (of the cut itself only if all its ties stay)
+  const float cf = logit_of(cut), ff = logit_of(min(from, top));
+  const bool again = listed < 0 || listed > Sh::kSlots;
+  if (!again)
+    for (int i = 0; i < listed; ++i) {
+      const int code = sh.list[i][tid];
+      const float x = one(code);
+      if (x > cf || (x == cf && !partial)) {
+        atomicAdd(&sh.seg[(code >> 5) * Sh::kWarps + wid], W(x));
+        ++cnt;
+      }
+    }
+  if (__any_sync(0xffffffffu, again) && cut <= from) {
+    int step = 0;
+    for (int s = wid; s < segs; s += Sh::kWarps, ++step) {
+      unsigned long long mass = 0;
+      weights(s, step, cf, [&](unsigned long long w, float x, int) {
+        if (again && x <= ff && (x > cf || (x == cf && !partial))) mass += w, ++cnt;
+      });
+      add_segment(s, mass);
+    }
+  }
+  // the cut's ties, lowest ids first
+  const unsigned long long wc = partial ? W(cf) : 0ull;
+  if (partial) {
+    for (int s = wid; s < segs; s += Sh::kWarps) {
+      uint32_t n = 0;
+      for (int j = 0; j < J; ++j) {
+        float x[X];
+        load(id_of(s, j), x);
+#pragma unroll
+        for (int e = 0; e < X; ++e) n += x[e] == cf;
+      }
+      n = __reduce_add_sync(0xffffffffu, n);
+      if (lane == 0) sh.seg_n[s] = n;
+    }
+  }
+  __syncthreads();
+  // the pick: the segment that holds it (of `segs` <= 512, one a thread), then its ids
+  unsigned long long rank = 0, total, kept, in_cta, n_cta = cnt, pad = 0, tie_n = 0;
+  const uint32_t my_ties = partial && tid < segs ? sh.seg_n[tid] : 0u;
+  if (partial) {
+    rank = cl.scan(my_ties, tie_n);
+    const int p = cl.exchange(tie_n, 0);
+    for (unsigned r = 0; r < cl.rank; ++r) rank += sh.slot[p][r][0];
+    tie_n = rank < ties ? min((unsigned long long)my_ties, ties - rank) : 0ull;
+    n_cta += tie_n;
+  }
+  const unsigned long long mass = (tid < segs ? sh.seg[tid] : 0ull) + tie_n * wc;
+  unsigned long long before = cl.scan(mass, in_cta);
+  cl.cta_sum(n_cta, pad);
+  {
+    const int p = cl.exchange(in_cta, n_cta);
+    total = kept = 0;
+    for (unsigned r = 0; r < size; ++r) {
+      if (r < cl.rank) before += sh.slot[p][r][0];
+      total += sh.slot[p][r][0];
+      kept += sh.slot[p][r][1];
+    }
+  }
+  const unsigned long long goal = u >= 1.f ? total - 1 : u > 0.f ? part_of(u, total, false) : 0ull;
+  if (cl.rank == 0 && tid == 0 && a.kept) a.kept[row] = (int)kept;
+  if (tid == 0) sh.found[3] = ~0ull;
+  __syncthreads();
+  if (goal >= before && goal < before + mass) sh.found[3] = tid, sh.found[0] = before, sh.found[1] = rank;
+  __syncthreads();
+  if (sh.found[3] != ~0ull) {  // two ids a thread
+    const int s = (int)sh.found[3], id = base + s * kSegment + 2 * tid;
+    float x[2];
+    unsigned long long w[2], t0, all;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) x[e] = id + e < end ? clean(to_f32(__ldg(lg + id + e))) : kMasked;
+    W.two(make_float2(x[0], x[1]), w[0], w[1]);
+    const unsigned long long run = sh.found[0], r0 = sh.found[1];
+    t0 = r0 + cl.scan(partial ? (x[0] == cf) + (x[1] == cf) : 0, all);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      if (!(x[e] >= cf) || (partial && x[e] == cf && t0 >= ties)) w[e] = 0;
+      t0 += partial && x[e] == cf;
+    }
+    const unsigned long long at = run + cl.scan(w[0] + w[1], all);
+    if (goal >= at && goal < at + w[0]) a.ids[row] = id;
+    if (goal >= at + w[0] && goal < at + w[0] + w[1]) a.ids[row] = id + 1;
+  }
+  cl.sync();
+}
+
 }  // namespace
 
 using namespace dmtp;
@@ -755,8 +1219,20 @@ cudaError_t launch(const dmtp_sample_args& a, unsigned cluster, cudaStream_t st)
   return launch_op(k, (unsigned)a.rows * cluster, THREADS, (size_t)(kFixed + s.slice * 4), st, false, cluster, s);
 }
 template <typename T>
+cudaError_t launch_stream(const dmtp_sample_args& a, cudaStream_t st) {
+  static unsigned long long done = 0;
+  auto k = k_sample_stream<T>;
+  if (!smem_limit((const void*)k, sizeof(StreamShared), &done)) return cudaErrorInvalidValue;
+  RowsArgs s;
+  s.a = a;
+  s.slice = ((a.vocab + 1) / 2 + kSegment - 1) / kSegment * kSegment;
+  s.vec = aligned_to(a.logits, 16) && mult(a.ld * (int)sizeof(T), 16);
+  return launch_op(k, (unsigned)a.rows * 2, kStream, sizeof(StreamShared), st, false, 2, s);
+}
+template <typename T>
 cudaError_t launch_t(const dmtp_sample_args& a, cudaStream_t st) {
   const unsigned cluster = a.vocab > 8192 ? 8 : a.vocab > 2048 ? 2 : 1;
+  if (cluster == 8 && a.rows > kManyRows) return launch_stream<T>(a, st);
   return launch<T, 512>(a, cluster, st);
 }
 

@@ -546,12 +546,13 @@ def check_rows(z, u, t, k, p, m):
         assert (ids[i], kept[i]) == want, (i, ids[i], kept[i], want)
 
 
-@pytest.mark.parametrize("V", [1, 2, 31, 512, 513, 2049, 5000, 8193, 32000, 151936, 262144])
+@pytest.mark.parametrize("V,n", [(1, 24), (2, 24), (31, 24), (512, 24), (513, 60), (2049, 24), (5000, 60), (8193, 24),
+                                 (32000, 24), (151936, 24), (262144, 12), (8193, 60), (20001, 39), (32000, 90),
+                                 (151936, 40), (262144, 40)])
 @pytest.mark.parametrize("dtype", [FP, BF])
-def test_sample_rows(V, dtype):
-    """Every mixture of filters, one per row. bf16 logits tie often."""
-    r = np.random.RandomState(V)
-    n = 24
+def test_sample_rows(V, n, dtype):
+    """Every mixture of filters, one per row, for few rows and many. bf16 logits tie often."""
+    r = np.random.RandomState(V + n)
     big = randn((n, V + 3), gen(V), dtype, 2.5)
     z = big[:, :V] if V % 2 else big[:, 3:].clone()
     check_rows(z, r.rand(n), r.choice([0.0, 0.3, 0.7, 1.0, 2.0], n), r.choice([0, 1, 2, 50, 1000, V], n),
@@ -559,7 +560,8 @@ def test_sample_rows(V, dtype):
     check_rows(z, r.rand(n), None, None, None, None)
 
 
-def test_sample_ties_and_flat_rows():
+@pytest.mark.parametrize("copies", [1, 8])
+def test_sample_ties_and_flat_rows(copies):
     V = 9000
     z = torch.zeros((6, V), device="cuda")
     z[1, ::2] = 1.0
@@ -570,11 +572,17 @@ def test_sample_ties_and_flat_rows():
     for k in (0, 1, 7, 4500, 4501):
         for p in (0.0, 0.25, 0.5, 1.0):
             for m in (0.0, 0.5, 1.0):
-                check_rows(z, u, [1.0] * 6, [k] * 6, [p] * 6, [m] * 6)
+                if copies == 1:
+                    check_rows(z, u, [1.0] * 6, [k] * 6, [p] * 6, [m] * 6)
+                    continue
+                ids, kept = run_sample(z.repeat(copies, 1), u * copies, [1.0] * 6 * copies, [k] * 6 * copies,
+                                       [p] * 6 * copies, [m] * 6 * copies)
+                one = run_sample(z, u, [1.0] * 6, [k] * 6, [p] * 6, [m] * 6)
+                assert (ids.reshape(copies, 6) == one[0]).all() and (kept.reshape(copies, 6) == one[1]).all()
 
 
-@pytest.mark.parametrize("V", [100, 20000])
-def test_sample_masked_rows_and_odd_numbers(V):
+@pytest.mark.parametrize("V,copies", [(100, 1), (20000, 1), (20000, 5)])
+def test_sample_masked_rows_and_odd_numbers(V, copies):
     inf, nan = float("inf"), float("nan")
     z = randn((10, V), gen(0), FP, 3.0)
     z[0] = -inf
@@ -587,10 +595,12 @@ def test_sample_masked_rows_and_odd_numbers(V):
     z[6, 1::4] = nan
     z[7] = torch.finfo(FP).max
     z[8, 50] = torch.finfo(FP).max
-    u = [0.5, 0.5, 0.9, 0.3, 0.6, 0.7, 0.2, 0.99, 0.5, 0.5]
+    z[9, :3000] -= 40.0                    # the largest logits come late in the row
+    u = [0.5, 0.5, 0.9, 0.3, 0.6, 0.7, 0.2, 0.99, 0.5, 0.5] * copies
+    n = 10 * copies
     for t in (1.0, 0.0, 1e-38, 1e-3, 1e6):
         for k, p, m in ((0, 1.0, 0.0), (3, 0.9, 0.0), (0, 0.5, 0.1)):
-            check_rows(z, u, [t] * 10, [k] * 10, [p] * 10, [m] * 10)
+            check_rows(z.repeat(copies, 1), u, [t] * n, [k] * n, [p] * n, [m] * n)
     # numbers outside their ranges
     x = z[9:].expand(6, V).contiguous()
     ids, kept = run_sample(x, [-1.0, nan, 1.0, 2.0, inf, 0.0], [1.0] * 6, [50] * 6)

@@ -757,7 +757,8 @@ struct StreamShared {
   unsigned long long table[256];
   unsigned long long seg[DMTP_OPS_MAX_SAMPLE_VOCAB / 2 / kSegment];  // kept weight of a segment
   uint32_t seg_n[DMTP_OPS_MAX_SAMPLE_VOCAB / 2 / kSegment];          // ties of the cut in it
-  uint8_t list[kSlots][kStream];
+  uint8_t list[kSlots][kStream];  // a thread's logits in the neighbourhood: where, and which
+  float value[kSlots][kStream];
   uint32_t edge[3];
   int bins[2];
 };
@@ -789,9 +790,6 @@ __global__ void __launch_bounds__(kStream, 2) k_sample_stream(const RowsArgs sa)
     }
   };
   auto id_of = [&](int seg, int j) { return base + seg * kSegment + j * (32 * X) + lane * X; };
-  auto one = [&](int code) {  // a listed logit of this thread: step, load, element
-    return clean(to_f32(__ldg(lg + id_of((code >> 5) * Sh::kWarps + wid, (code & 31) / X) + code % X)));
-  };
   const float temp = a.temperature ? __ldg(a.temperature + row) : 1.f;
   const int k = a.top_k ? __ldg(a.top_k + row) : 0;
   const float top_p = a.top_p ? __ldg(a.top_p + row) : 1.f;
@@ -826,7 +824,7 @@ __global__ void __launch_bounds__(kStream, 2) k_sample_stream(const RowsArgs sa)
   unsigned long long nvalid = 0;
   while (true) {
     float best = kMasked;
-    uint32_t last = 0, valid = 0;
+    uint32_t last = 0;
     const bool use = binned && from_l > kMasked;
     __syncthreads();  // the histogram is clear
     for (int s = wid; s < segs; s += Sh::kWarps) {
@@ -847,7 +845,6 @@ __global__ void __launch_bounds__(kStream, 2) k_sample_stream(const RowsArgs sa)
         }
       }
     }
-    (void)valid;
     const uint32_t my_top = cl.cta_max(key_of(best));
     unsigned long long l64 = last, pad = 0;
     cl.cta_sum(l64, pad);
@@ -1013,10 +1010,11 @@ __global__ void __launch_bounds__(kStream, 2) k_sample_stream(const RowsArgs sa)
         weights(s, step, cf, [&](unsigned long long w, float x, int code) {
           if (by_k && !(x >= cf)) w = 0;
           sum += w;
-          if (x >= mf) mass += w, ++cnt;
+          const bool over = x >= mf;
+          if (over) mass += w, ++cnt;
           if (deep && x > hf) above += w;
-          if (x >= lf && x <= hf) {
-            if (listed < Sh::kSlots) sh.list[listed][tid] = (uint8_t)code;
+          if (x >= lf && !over && x <= hf) {
+            if (listed < Sh::kSlots) sh.list[listed][tid] = (uint8_t)code, sh.value[listed][tid] = x;
             ++listed;
           }
         });
@@ -1031,7 +1029,7 @@ __global__ void __launch_bounds__(kStream, 2) k_sample_stream(const RowsArgs sa)
       if (!moved && listed <= Sh::kSlots) {
         const float lf = logit_of(lo), hf = logit_of(hi);
         for (int i = 0; i < listed; ++i) {
-          const float x = one(sh.list[i][tid]);
+          const float x = sh.value[i][tid];
           if (x >= lf && x <= hf) cl.add_fine(hi - key_of(x) >> shift, W(x));
         }
       }
@@ -1112,7 +1110,7 @@ __global__ void __launch_bounds__(kStream, 2) k_sample_stream(const RowsArgs sa)
   if (!again)
     for (int i = 0; i < listed; ++i) {
       const int code = sh.list[i][tid];
-      const float x = one(code);
+      const float x = sh.value[i][tid];
       if (x > cf || (x == cf && !partial)) {
         atomicAdd(&sh.seg[(code >> 5) * Sh::kWarps + wid], W(x));
         ++cnt;

@@ -104,7 +104,7 @@ int plan(const dmtp_paged_kv* c, const dmtp_paged_query* a, PagedPlan* pl) {
   const int64_t reach = (int64_t)c->max_blocks * c->page_size;
   const int64_t units = (int64_t)c->n_seqs * c->n_kv_heads * pl->chunks;
   if ((reach + 63) / 64 * units >= (1ll << 31)) return DMTP_EINVAL;
-  pl->whole = reach <= kWholeReach;
+  pl->whole = reach <= (units >= kWholeUnits ? kWholeReachMany : kWholeReach);
   if (pl->whole) {
     pl->grid = (int)units;
     pl->part_o = pl->part_ml = pl->note = pl->bytes = 0;

@@ -5,7 +5,7 @@
 // n_b tiles of 64 keys. A unit is one (sequence, kv head, chunk of at most QN queries); a
 // sequence has U = n_kv_heads x chunks of them.
 //
-// Whole units (tables that reach no further than kWholeReach positions): CTA c takes unit c, and
+// Whole units (short tables, see kWholeReach): CTA c takes unit c, and
 // one launch is all; nothing about the lengths has to be known before.
 //
 // Split units: all units' tiles laid end to end (T in all) are dealt to the G CTAs (G at most
@@ -22,9 +22,12 @@
 
 namespace dmtp {
 
-// Table reach up to which units are not split. Measured with one sequence of that length, 4 kv
-// heads of 128 (32 query heads), us in a captured graph: see paged_attn.cu.
-constexpr int kWholeReach = 1024;
+// Units are not split when the table reaches no further than kWholeReach positions, or, with
+// kWholeUnits units to keep the SMs busy, kWholeReachMany. Measured in a captured graph (us,
+// split / whole; 4 kv heads of 128, 32 query heads, bf16): one sequence of 256 positions
+// 7.8 / 6.8, of 512 7.9 / 9.7, of 1024 8.1 / 14.8; 32 sequences (128 units) of 512 15.1 / 11.6,
+// of 1024 19.3 / 19.1, of 2048 28.6 / 33.7.
+constexpr int kWholeReach = 256, kWholeReachMany = 1024, kWholeUnits = 64;
 
 struct PagedNote {
   int first, last;  // the CTAs of a unit's pieces; last < 0: nothing to join

@@ -16,7 +16,7 @@
 //   64            one of four       64 keys a stage
 //
 // A warp has at most 16 queries: with 32 (and half the conversions of E4M3 rows) only two CTAs fit
-// an SM, and 32 sequences of 2304 E4M3 positions x 64 queries took 77 us instead of V64.
+// an SM, and 32 sequences of 512 to 4096 E4M3 positions x 64 queries took 78 us instead of 65.
 //
 // Weights 2^(s - m) use a running maximum m per query that moves only when a score passes it
 // by 2^8 (so most blocks skip the rescaling). bf16 caches: P as a bf16 pair (16 bits of each
@@ -72,11 +72,11 @@ __device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t a) {
 template <bool F16>
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   if (F16)
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   else
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -99,7 +99,7 @@ __device__ __forceinline__ uint32_t finite_pair(uint32_t u) {
 
 __device__ __forceinline__ uint32_t transpose8(uint32_t u) {  // an 8 x 8 block of 16-bit values
   uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(u));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(u));
   return r;
 }
 // Four E4M3 bytes as two pairs of halves.
@@ -134,9 +134,12 @@ __device__ __forceinline__ void block(const PagedAttn& p, State<HD, NT>& z,
   const int lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3, mi = lane >> 3;
   const uint32_t sK = smem_u32(blk), sV = sK + 16 * RB;
   const float* sS = (const float*)(blk + 32 * RB);
-  float s[NT][4];
+  // (two accumulators a score: half as long a chain of dependent products)
+  float s[NT][4], s1[NT][4];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[n][i] = s1[n][i] = 0.f;
   {  // A fragments of K: rows (keys) 0-7 and 8-15 of two 16-byte steps. A row's steps are
      // permuted by exclusive or, so step k2 is the first one's address with k2's bits flipped.
     const uint32_t a0 = sK + tile_at<RB>((lane & 7) + 8 * (mi & 1), mi >> 1);
@@ -158,7 +161,7 @@ __device__ __forceinline__ void block(const PagedAttn& p, State<HD, NT>& z,
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         mma16816<E8>(s[n], a[0], qf[n][k2][0], qf[n][k2][1]);
-        mma16816<E8>(s[n], a[1], qf[n][k2 + 1][0], qf[n][k2 + 1][1]);
+        mma16816<E8>(s1[n], a[1], qf[n][k2 + 1][0], qf[n][k2 + 1][1]);
       }
     }
   }
@@ -182,7 +185,7 @@ __device__ __forceinline__ void block(const PagedAttn& p, State<HD, NT>& z,
     for (int y = 0; y < 2; ++y)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        float v = s[n][2 * h + y] * z.rowf[n][y];
+        float v = (s[n][2 * h + y] + s1[n][2 * h + y]) * z.rowf[n][y];
         if (E8) v = fmaf(v, kf[h], ve[h]);
         if (EDGE) {
           const int key = g + 8 * h, j = jb + key;

@@ -16,7 +16,8 @@
  * pointers on the current device, and work is enqueued on `stream` (NULL: the default
  * stream), so every call can be captured into a CUDA graph. A workspace belongs to one
  * call at a time: calls (or replays of captured calls) that may overlap on the GPU each
- * need their own. A workspace needs no initialisation.
+ * need their own. A workspace needs no initialisation. The first call of an operator on a
+ * device sets its kernels up and should come before any stream capture.
  *
  * Errors. DMTP_EINVAL is detected on the host before any launch. DMTP_ECUDA: a CUDA call
  * or launch failed, or a CUDA error was already pending on the calling thread (nothing is
@@ -108,7 +109,8 @@ int dmtp_paged_read(const dmtp_paged_kv* c, const int32_t* seq, const int32_t* p
  * gets zeros. q and out: the cache's dtype, strides in elements, head_dim dense; row
  * pointers 16-byte aligned, strides multiples of 16 bytes. Lengths past the block table's
  * reach are cut there and set DMTP_OPS_ERR_POS; a bad page sets DMTP_OPS_ERR_PAGE and its
- * positions are left out.
+ * positions are left out. A NaN or an infinity reaches the rows that see its position and no
+ * other. |scale| <= 1e30.
  * Scores, softmax statistics and sums are fp32; products of bf16 rows run on the tensor
  * cores with the weights as bf16 pairs (16 bits), of E4M3 rows with fp16 weights. Results
  * do not depend on timing: the same call gives the same bits. */
@@ -121,7 +123,8 @@ typedef struct {
   float scale;
 } dmtp_paged_query;
 
-/* Bytes of workspace for dmtp_paged_attention (256-byte aligned) on the current device. */
+/* Bytes of workspace for dmtp_paged_attention (256-byte aligned; 0: none, and workspace may be
+ * NULL). Of `a` only rows and n_heads matter. */
 int dmtp_paged_attention_workspace(const dmtp_paged_kv* c, const dmtp_paged_query* a,
                                    size_t* bytes);
 int dmtp_paged_attention(const dmtp_paged_kv* c, const dmtp_paged_query* a, void* workspace,
@@ -130,7 +133,7 @@ int dmtp_paged_attention(const dmtp_paged_kv* c, const dmtp_paged_query* a, void
 /* x_out = x + y (rounded to x's type), and the unrounded sum's norm as E4M3 rows:
  * h = (x + y) / sqrt(mean((x + y)^2) + eps) * gain, q [rows][d] E4M3 values with row pitch
  * q_row, scale [rows] fp32. x, x_out: x_dtype; y: y_dtype; gain [d]: gain_dtype; row
- * pitches in elements. x_out may be x; y may be NULL (no addition; x_out may then be NULL
+ * pitches in elements. The sum of squares is fp32: |x + y| up to about 1e17. x_out may be x; y may be NULL (no addition; x_out may then be NULL
  * too). Limits: d a multiple of 8 up to DMTP_OPS_MAX_NORM_D; row starts 16-byte aligned
  * (q: 8-byte), pitches >= d and multiples of 8; eps >= 0 and finite. */
 typedef struct {

@@ -85,7 +85,7 @@ int check_query(const dmtp_paged_kv* c, const dmtp_paged_query* a) {
   const int e = check_cache(c);
   if (e) return e;
   if (!a || a->rows < 1 || a->rows > DMTP_OPS_MAX_ROWS || a->n_heads < 1 || a->n_heads > 4096 ||
-      a->n_heads % c->n_kv_heads || a->window < 0 || c->n_seqs > 65535)
+      a->n_heads % c->n_kv_heads || a->window < 0)
     return DMTP_EINVAL;
   return DMTP_OK;
 }
@@ -144,7 +144,7 @@ extern "C" int dmtp_paged_attention(const dmtp_paged_kv* c, const dmtp_paged_que
   const int64_t strides[6] = {a->q_seq, a->q_row, a->q_head, a->o_seq, a->o_row, a->o_head};
   for (int64_t s : strides)
     if (s < 0 || !mult(s * es, 16)) return DMTP_EINVAL;
-  if (a->o_head < hd || !(a->scale > -3.4e38f && a->scale < 3.4e38f)) return DMTP_EINVAL;
+  if (a->o_head < hd || !(a->scale >= -1e30f && a->scale <= 1e30f)) return DMTP_EINVAL;
   PagedPlan pl;
   const int r = plan(c, a, &pl);
   if (r) return r;
@@ -158,6 +158,7 @@ extern "C" int dmtp_paged_attention(const dmtp_paged_kv* c, const dmtp_paged_que
   p.ks = c->k_scale;
   p.vs = c->v_scale;
   p.a = *a;
+  if (p.a.window >= p.m.reach) p.a.window = 0;  // every position lies inside it
   p.err = err;
   p.group = a->n_heads / c->n_kv_heads;
   p.nq = a->rows * p.group;

@@ -4,8 +4,8 @@
 // One pass over the cached rows bounds it: each byte of K and V feeds at most 64 queries of
 // its kv head (rows x query heads), a few hundred operations. So the warps keep rings of
 // 16-key blocks in flight by 16-byte asynchronous copies (the pages of the next 32 blocks in one
-// read of the table) and work on 16-bit fragments with m16n8k16
-// products that need no staging beyond the block itself. Keys are the M side and queries the N
+// read of the table) and work on 16-bit fragments with m16n8k16 products that need no staging
+// beyond the block itself. Keys are the M side and queries the N
 // side of both products (S^T = K Q^T, O^T = V^T P^T), so 8 queries fill an instruction. (The
 // tcgen05 form wants 128 rows of keys and one thread to start each product of the whole CTA;
 // a block would wait for its neighbours, and E4M3 rows would go through shared memory twice.)
@@ -41,7 +41,7 @@ struct Shape {
   static constexpr int QG = QN / (8 * NT);          // warps of a team
   static constexpr int KS = 4 / QG;                 // teams
   static constexpr int RB = HD * (E8 ? 1 : 2);      // bytes of a cached row
-  static constexpr int NSUB = 4 / KS;         // 16-key blocks of a team in a tile
+  static constexpr int NSUB = 4 / KS;               // 16-key blocks of a team in a tile
   static constexpr int kBlock = 2 * 16 * RB + (E8 ? 128 : 0);
   static constexpr int kStage = NSUB * kBlock;      // of a team
   static constexpr int kPitch = HD + 4;             // floats of a joined row: no conflicts

@@ -745,7 +745,10 @@ __global__ void __launch_bounds__(THREADS) k_sample_rows(const RowsArgs sa) {
 // pass. Warps take segments of 1024 consecutive ids, whose kept weights the pick searches.
 // The bins of the first pass hang on the largest of the row's first logits (256 bins above it; a
 // row whose later logits are higher still is counted again).
-constexpr int kManyRows = 38;
+// Rows of 151936 in a captured graph, us, clusters of eight / this: top_k 50 with top_p 0.9, 96
+// rows 82 / 106, 128 rows 109 / 110, 256 rows 204 / 195; top_p 0.9 alone 114 / 142, 150 / 144,
+// 282 / 262.
+constexpr int kManyRows = 128;
 constexpr int kStream = 512, kSegment = 1024, kAhead = 256;
 
 struct StreamShared {
@@ -1202,7 +1205,7 @@ cudaError_t launch(const dmtp_sample_args& a, unsigned cluster, cudaStream_t st)
   static unsigned long long done = 0;
   auto k = k_sample_rows<T, THREADS>;
   constexpr int kFixed = (sizeof(Shared<THREADS>) + 15) / 16 * 16;
-  // a thread's ids: an odd number of pairs, so that the threads' pairs lie in different banks
+  // A thread's ids: an odd number of pairs, so that the threads' pairs lie in different banks
   auto pairs_of = [](int n) {
     const int p = (n + 2 * THREADS - 1) / (2 * THREADS);
     return p + 1 - p % 2;
@@ -1230,7 +1233,7 @@ cudaError_t launch_stream(const dmtp_sample_args& a, cudaStream_t st) {
 template <typename T>
 cudaError_t launch_t(const dmtp_sample_args& a, cudaStream_t st) {
   const unsigned cluster = a.vocab > 8192 ? 8 : a.vocab > 2048 ? 2 : 1;
-  if (cluster == 8 && a.rows > kManyRows) return launch_stream<T>(a, st);
+  if (cluster == 8 && a.rows >= kManyRows) return launch_stream<T>(a, st);
   return launch<T, 512>(a, cluster, st);
 }
 

@@ -270,6 +270,7 @@ class DmtpPagedCache:
     def check(self):
         """Wait for the device and raise DmtpError(DMTP_EDEVICE) if any call since the last
         check met an index out of range; the word is then cleared."""
+        _c().torch.cuda.synchronize(self.device)
         word = int(self.err.item())
         if word:
             self.err.zero_()

@@ -297,6 +297,83 @@ def test_attention_window(dtype, e4m3, window):
 
 
 @pytest.mark.parametrize("dtype,e4m3", KINDS)
+def test_a_window_past_every_position_is_none(dtype, e4m3):
+    c = new_cache(2, 40, 16, 2, 64, dtype, e4m3)
+    g = gen(0)
+    kv = fill_cache(c, [600, 0], g)
+    q = randn((2, 8, 4, 64), g, dtype)
+    a = check_attention(c, q, [600, 0], kv)
+    for window in (640, 2 ** 31 - 1):
+        assert torch.equal(a, c.attention(q, i32([600, 0]), window=window))
+
+
+@pytest.mark.parametrize("dtype,e4m3", [(BF, True), (FP, False)])
+def test_attention_many_sequences(dtype, e4m3):
+    """More sequences than a grid dimension holds, most of them short, some idle."""
+    n, hd, ps = 66000, 64, 16
+    r = np.random.RandomState(1)
+    lens = r.randint(0, ps + 1, n)
+    lens[12345], lens[-1] = 0, 16
+    from mtp_block_draft_gb300 import DmtpPagedCache
+    table = torch.from_numpy(r.permutation(n).astype(np.int32)[:, None]).cuda()
+    c = DmtpPagedCache.alloc(n, ps, 1, hd, table, dtype=dtype, e4m3=e4m3)
+    g = gen(2)
+    x = randn((n * ps, 1, hd), g, dtype)
+    seq, pos = np.repeat(np.arange(n), ps), np.tile(np.arange(ps), n)
+    c.write(x, x.flip(0), i32(seq), i32(pos))
+    q = randn((n, 1, 2, hd), g, dtype)
+    got = np64(c.attention(q, i32(lens)))
+    c.check()
+    k, v = (np64(t).reshape(n, ps, hd) for t in c.read(i32(seq), i32(pos)))
+    s = np.einsum("nhd,nld->nhl", np64(q)[:, 0], k) / 8
+    s = np.where(np.arange(ps)[None, None] < lens[:, None, None], s, -np.inf)
+    w = np.exp(s - np.where(lens > 0, s.max((1, 2)), 0)[:, None, None])
+    w /= np.maximum(w.sum(-1, keepdims=True), 1e-300)
+    ref = np.einsum("nhl,nld->nhd", w, v)[:, None]
+    # as in reference(), with the largest sum of magnitudes of any score
+    mag = np.einsum("nhd,nld->nhl", np.abs(np64(q)[:, 0]), np.abs(k)).max() / 8
+    ew = (2 * math.expm1(2 * (hd + 4) * U * mag) + 2.0 ** -21 + 8 * mag * U
+          + (2.0 ** -11 if e4m3 else 0) + 2 * ps * U)
+    tol = ew * np.einsum("nhl,nld->nhd", w, np.abs(v))[:, None] * 1.01 + HALF[dtype] * np.abs(ref) + 17 * 2.0 ** -25 * 448
+    assert (np.abs(got - ref) <= (tol if e4m3 else tol - 17 * 2.0 ** -25 * 448 + 1e-30)).all()
+    assert (got[lens == 0] == 0).all()
+
+
+def test_two_threads_on_two_streams():
+    """Calls from two host threads, on streams of their own, over one cache."""
+    import threading
+    from mtp_block_draft_gb300 import sample_rows
+    lens = [900, 1700]
+    c = new_cache(2, 110, 16, 2, 128, BF, True)
+    g = gen(6)
+    fill_cache(c, lens, g)
+    q = [randn((2, 1, 8, 128), g) for _ in range(2)]
+    z = randn((4, 30000), g, FP, 3.0)
+    u, k = torch.rand(4, device="cuda", generator=g), i32([5, 0, 40, 9])
+    ln = i32(lens)
+    want = [(c.attention(x, ln), sample_rows(z, u, top_k=k)) for x in q]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(200):
+                a, b = c.attention(q[i], ln), sample_rows(z, u, top_k=k)
+            s.synchronize()
+            if not (torch.equal(a, want[i][0]) and torch.equal(b, want[i][1])):
+                bad.append(i)
+
+    t = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for x in t:
+        x.start()
+    for x in t:
+        x.join()
+    assert not bad
+    c.check()
+
+
+@pytest.mark.parametrize("dtype,e4m3", KINDS)
 def test_attention_one_long_sequence_among_short_ones(dtype, e4m3):
     """One unit split over many CTAs beside units that fit in one; peaked scores."""
     lens = [20000, 3, 0, 190]
@@ -547,8 +624,8 @@ def check_rows(z, u, t, k, p, m):
 
 
 @pytest.mark.parametrize("V,n", [(1, 24), (2, 24), (31, 24), (512, 24), (513, 60), (2049, 24), (5000, 60), (8193, 24),
-                                 (32000, 24), (151936, 24), (262144, 12), (8193, 60), (20001, 39), (32000, 90),
-                                 (151936, 40), (262144, 40)])
+                                 (32000, 24), (151936, 24), (262144, 12), (8193, 130), (20001, 128), (32000, 127),
+                                 (32000, 140), (151936, 129), (262144, 128)])
 @pytest.mark.parametrize("dtype", [FP, BF])
 def test_sample_rows(V, n, dtype):
     """Every mixture of filters, one per row, for few rows and many. bf16 logits tie often."""
@@ -560,7 +637,7 @@ def test_sample_rows(V, n, dtype):
     check_rows(z, r.rand(n), None, None, None, None)
 
 
-@pytest.mark.parametrize("copies", [1, 8])
+@pytest.mark.parametrize("copies", [1, 22])
 def test_sample_ties_and_flat_rows(copies):
     V = 9000
     z = torch.zeros((6, V), device="cuda")
@@ -581,7 +658,7 @@ def test_sample_ties_and_flat_rows(copies):
                 assert (ids.reshape(copies, 6) == one[0]).all() and (kept.reshape(copies, 6) == one[1]).all()
 
 
-@pytest.mark.parametrize("V,copies", [(100, 1), (20000, 1), (20000, 5)])
+@pytest.mark.parametrize("V,copies", [(100, 1), (20000, 1), (20000, 13)])
 def test_sample_masked_rows_and_odd_numbers(V, copies):
     inf, nan = float("inf"), float("nan")
     z = randn((10, V), gen(0), FP, 3.0)

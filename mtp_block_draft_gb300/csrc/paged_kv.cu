@@ -223,13 +223,13 @@ struct ReadArgs {
   unsigned* err;
 };
 
-// A group of lanes copies kHeads heads of one row, 16 bytes of the cache a lane and head: the
-// chain position -> page -> row is walked once for all of them, and their loads are in flight
-// together.
+// A group of lanes copies kHeads heads of one row, 16 bytes of the cache a lane and head (of an
+// E4M3 cache 8, so that a bf16 row is written in whole lines): the chain position -> page -> row
+// is walked once for all of them, and their loads are in flight together.
 constexpr int kHeads = 4;
 template <typename T, bool E8>
 __global__ void __launch_bounds__(256) k_paged_read(const ReadArgs a) {
-  constexpr int E = E8 ? 16 : 16 / (int)sizeof(T);  // values of a lane
+  constexpr int E = E8 ? 8 : 16 / (int)sizeof(T);  // values of a lane
   const int hd = a.m.head_dim, hkv = a.m.n_kv_heads;
   const int gl = threadIdx.x & (a.group - 1), ng = blockDim.x / a.group;
   const int64_t row = (int64_t)blockIdx.x * ng + threadIdx.x / a.group;
@@ -252,8 +252,14 @@ __global__ void __launch_bounds__(256) k_paged_read(const ReadArgs a) {
     if (h2 < 2 * hkv) {
       const bool isv = h2 >= hkv;
       const int64_t line = (int64_t)(isv ? h2 - hkv : h2) * a.m.page_size + off;
-      const int64_t at = ((int64_t)page * a.m.page_stride + line * hd) * (E8 ? 1 : (int)sizeof(T)) + 16 * gl;
-      u[i] = __ldcs(reinterpret_cast<const uint4*>((const char*)(isv ? a.v : a.k) + at));
+      const int64_t at = ((int64_t)page * a.m.page_stride + line * hd) * (E8 ? 1 : (int)sizeof(T)) + (E8 ? 8 : 16) * gl;
+      const char* src = (const char*)(isv ? a.v : a.k) + at;
+      if (E8) {
+        const uint2 w = __ldcs(reinterpret_cast<const uint2*>(src));
+        u[i] = make_uint4(w.x, w.y, 0, 0);
+      } else {
+        u[i] = __ldcs(reinterpret_cast<const uint4*>(src));
+      }
       if (E8) s[i] = __ldg((isv ? a.vs : a.ks) + (int64_t)page * a.m.scale_stride + line);
     }
   }
@@ -264,14 +270,10 @@ __global__ void __launch_bounds__(256) k_paged_read(const ReadArgs a) {
       const bool isv = h2 >= hkv;
       T* dst = (T*)(isv ? a.vo : a.ko) + (row * hkv + (isv ? h2 - hkv : h2)) * hd + E * gl;
       if (E8) {
-        const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-#pragma unroll
-        for (int p = 0; p < 4; p += 2) {
-          const float4 x = e4m3x4_to_f4(w[p]), y = e4m3x4_to_f4(w[p + 1]);
-          const float f[8] = {x.x * s[i], x.y * s[i], x.z * s[i], x.w * s[i],
-                              y.x * s[i], y.y * s[i], y.z * s[i], y.w * s[i]};
-          store8(dst + 4 * p, true, f);
-        }
+        const float4 x = e4m3x4_to_f4(u[i].x), y = e4m3x4_to_f4(u[i].y);
+        const float f[8] = {x.x * s[i], x.y * s[i], x.z * s[i], x.w * s[i],
+                            y.x * s[i], y.y * s[i], y.z * s[i], y.w * s[i]};
+        store8(dst, true, f);
       } else {
         *reinterpret_cast<uint4*>(dst) = u[i];
       }
@@ -406,7 +408,7 @@ extern "C" int dmtp_paged_read(const dmtp_paged_kv* c, const int32_t* seq, const
   a.ko = k_out;
   a.vo = v_out;
   a.n_rows = n_rows;
-  a.lanes = c->head_dim * (c->e4m3 ? 1 : c->dtype ? 2 : 4) / 16;
+  a.lanes = c->head_dim / (c->e4m3 || c->dtype ? 8 : 4);
   a.group = group_of(a.lanes);
   a.err = err;
   const int ng = 256 / a.group, heads = (2 * c->n_kv_heads + kHeads - 1) / kHeads;

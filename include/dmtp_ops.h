@@ -157,8 +157,8 @@ int dmtp_add_rmsnorm_e4m3(const dmtp_norm_args* a, void* stream);
  * at which the running weight exceeds u[r] times the kept weight, u in [0, 1) (values
  * outside, and NaN, are taken as the nearest end, NaN as 0). temperature <= 0 or NaN: the
  * largest logit's id. A logit of -infinity or NaN is never kept; +infinity counts as
- * the largest finite number, a temperature below 1e-30 as 1e-30. A row that keeps nothing gets id -1. kept[r] (optional) is the
- * number of kept tokens. temperature, top_k, top_p, min_p: device arrays [rows], each
+ * the largest finite number; a temperature counts as the nearest in [1e-30, 1e30]. A row that
+ * keeps nothing gets id -1. kept[r] (optional) is the number of kept tokens. temperature, top_k, top_p, min_p: device arrays [rows], each
  * optional (NULL: 1, off, off, off). u: device fp32 [rows]. Weights and their sums are
  * integers (steps of 2^-44 of the largest, computed to about 2^-39), so a row's result depends on nothing
  * but its inputs. Limits: 1 <= vocab <= DMTP_OPS_MAX_SAMPLE_VOCAB, ld >= vocab. */

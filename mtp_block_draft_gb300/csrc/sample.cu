@@ -434,7 +434,7 @@ __global__ void __launch_bounds__(THREADS) k_sample_rows(const RowsArgs sa) {
   W.top = logit_of(top);
   W.table = sh.table;
   // c = log2(e) / T as a pair
-  const float tt = fmaxf(temp, 1e-30f);
+  const float tt = fminf(fmaxf(temp, 1e-30f), 1e30f);
   W.chi = 1.44269502162933349609f / tt;
   W.clo = (fmaf(-W.chi, tt, 1.44269502162933349609f) + 1.92596299112661746887e-08f) / tt;
   W.cb = W.chi * 32.f;
@@ -804,7 +804,7 @@ __global__ void __launch_bounds__(kStream, 2) k_sample_stream(const RowsArgs sa)
   for (int i = tid; i < segs; i += kStream) sh.seg[i] = 0, sh.seg_n[i] = 0;
   Weigh W;
   W.table = sh.table;
-  const float tt = fmaxf(temp, 1e-30f);
+  const float tt = fminf(fmaxf(temp, 1e-30f), 1e30f);
   W.chi = 1.44269502162933349609f / tt;
   W.clo = (fmaf(-W.chi, tt, 1.44269502162933349609f) + 1.92596299112661746887e-08f) / tt;
   W.cb = W.chi * 32.f;

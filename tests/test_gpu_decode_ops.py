@@ -688,6 +688,24 @@ def test_sample_masked_rows_and_odd_numbers(V, copies):
     assert [ids[i] for i in (0, 1, 2, 4, 5)] == [best] * 5 and kept[3] == V
 
 
+@pytest.mark.parametrize("V,copies", [(100, 1), (20000, 1), (20000, 33)])
+def test_sample_temperatures_past_their_range(V, copies):
+    """Above 1e30, infinity among them, a temperature counts as 1e30: ordinary logits weigh the
+    same, the type's lowest value still weighs nothing."""
+    z = randn((4, V), gen(5), FP, 3.0)
+    z[1, ::3] = torch.finfo(FP).min
+    z[2, 1::2] = -float("inf")
+    z[3] = torch.finfo(FP).min
+    n = 4 * copies
+    u = [0.1, 0.5, 0.7, 0.999] * copies
+    for t in (1e30, 1e35, float("inf")):
+        for k, p, m in ((0, 1.0, 0.0), (7, 1.0, 0.0), (0, 0.5, 0.0), (40, 0.9, 0.5)):
+            args = [k] * n, [p] * n, [m] * n
+            ids, kept = run_sample(z.repeat(copies, 1), u, [t] * n, *args)
+            want = [plain_pick(np64(z)[i % 4], float(np.float32(u[i])), 1e30, k, float(np.float32(p)), m) for i in range(4)]
+            assert [(int(a), int(b)) for a, b in zip(ids, kept)] == want * copies, (t, k, p)
+
+
 def test_sample_frequencies():
     """Evenly spread u visit every kept token in proportion to its weight: with n numbers
     (i + 1/2) / n the count of a token is within one of n times its probability."""

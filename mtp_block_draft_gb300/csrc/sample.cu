@@ -189,6 +189,13 @@ struct Cluster {
     else
       __syncthreads();
   }
+  // sync() in two halves: what stands between them does not wait for the others
+  __device__ __forceinline__ void arrive() const {
+    if (size > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  }
+  __device__ __forceinline__ void wait() const {
+    if (size > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
   // Leave (a, b) of this CTA in every CTA's slots (thread t < size sends to CTA t) and wait:
   // afterwards slot[p][r] holds CTA r's pair. Call with a, b valid in threads 0..size-1.
   __device__ __forceinline__ int exchange(unsigned long long a, unsigned long long b) {
@@ -776,6 +783,7 @@ __global__ void __launch_bounds__(kStream, 2) k_sample_stream(const RowsArgs sa)
   unsigned size;
   asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(size));
   Cluster<kStream, Sh> cl{&sh, cluster_rank(), size, 0};
+  cl.arrive();
   const int row = blockIdx.x / size, tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const int base = (int)cl.rank * sa.slice, end = min(a.vocab, base + sa.slice);
   const int segs = end > base ? (end - base + kSegment - 1) / kSegment : 0;
@@ -825,6 +833,7 @@ __global__ void __launch_bounds__(kStream, 2) k_sample_stream(const RowsArgs sa)
   };
   uint32_t top = 0;
   unsigned long long nvalid = 0;
+  cl.wait();  // every CTA of the cluster runs before one writes another's memory
   while (true) {
     float best = kMasked;
     uint32_t last = 0;

@@ -56,7 +56,7 @@ extern "C" {
  * rows (positive normal numbers below 2^127; dmtp_paged_write makes powers of two), likewise v_scale.
  * Position j of sequence s lies in page table[s * table_stride + j / page_size], row
  * j % page_size; 0 <= j < max_blocks * page_size. Entries past a sequence's length are not
- * read. Several entries may name one page (a shared prefix).
+ * read, nor are those whose positions all lie before the window of every row. Several entries may name one page (a shared prefix).
  * Limits: head_dim a multiple of 16 up to DMTP_OPS_MAX_HEAD_DIM; 1 <= page_size <= 65536;
  * max_blocks * page_size < 2^31 - 65536; k and v 16-byte aligned, page_stride
  * >= n_kv_heads page_size head_dim and a multiple of 16 bytes; scale_stride

@@ -51,12 +51,13 @@ __device__ __forceinline__ int seq_len(const PagedAttn& p, int b) {
   const int n = __ldg(p.a.kv_len + b);
   return n < 0 ? 0 : n > p.m.reach ? p.m.reach : n;
 }
-// First position of sequence b's tiles: that any row sees, down to a whole 64.
-__device__ __forceinline__ int seq_first(const PagedAttn& p, int len) {
-  if (p.a.window <= 0) return 0;
-  const int f = len - p.a.rows + 1 - p.a.window;
-  return f > 0 ? f & ~63 : 0;
+// First position that any row of a sequence sees. The pages before it are not looked up: with a
+// window a user may have taken them back.
+__device__ __forceinline__ int seq_low(const PagedAttn& p, int len) {
+  return p.a.window <= 0 ? 0 : max(0, len - p.a.rows + 1 - p.a.window);
 }
+// First position of its tiles: that, down to a whole 64.
+__device__ __forceinline__ int seq_first(const PagedAttn& p, int len) { return seq_low(p, len) & ~63; }
 __device__ __forceinline__ int seq_tiles(const PagedAttn& p, int len) {
   return (len - seq_first(p, len) + 63) / 64;
 }

@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kThreads) k_paged_attn_simt(const PagedAttn p)
       {
         const int j = j0 + tid;
         int64_t at = -1, line = 0;
-        if (j < len) {
+        if (j < len && j >= seq_low(p, len)) {
           int off;
           const int page = page_of(p.m, w.b, j, off, p.err);
           line = (int64_t)kvh * p.m.page_size + off;

@@ -355,7 +355,8 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, E8, QN>::CTAS) k_paged_att
     const int j = prod.first + (win_t + lane / NSUB) * 64 + (team + KS * (lane % NSUB)) * 16;
     win_page = -1;
     // (no further than this CTA's tiles: pages that others read are theirs to report)
-    if (paged16 && j < prod.len && lane / NSUB < prod.end - prod.pos) win_page = page_of(p.m, prod.b, j, win_off, p.err);
+    if (paged16 && j < prod.len && j + 15 >= seq_low(p, prod.len) && lane / NSUB < prod.end - prod.pos)
+      win_page = page_of(p.m, prod.b, j, win_off, p.err);
   };
   int stage_in = 0;
   auto produce = [&]() {
@@ -409,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, E8, QN>::CTAS) k_paged_att
           const int j = jb + (lane & 15);
           int64_t at = -1;
           int64_t sat = 0;
-          if (j < prod.len) {
+          if (j < prod.len && j >= seq_low(p, prod.len)) {
             int o;
             const int pg = page_of(p.m, prod.b, j, o, p.err);
             const int64_t line = (int64_t)kvh * p.m.page_size + o;

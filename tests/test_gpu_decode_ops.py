@@ -297,6 +297,24 @@ def test_attention_window(dtype, e4m3, window):
 
 
 @pytest.mark.parametrize("dtype,e4m3", KINDS)
+@pytest.mark.parametrize("ps", [1, 5, 16, 48, 64])
+@pytest.mark.parametrize("rows,window", [(1, 1), (3, 40), (8, 130)])
+def test_pages_before_the_window_are_not_looked_up(dtype, e4m3, ps, rows, window):
+    """Blocks that no row sees any more, and those past the length, may name pages that are none."""
+    for lens in ([0, 2, 60, 64, 333, 320], [700] * 40):
+        c = new_cache(len(lens), -(-704 // ps), ps, 2, 64, dtype, e4m3, fill=float("nan"))
+        g = gen(window)
+        kv = fill_cache(c, lens, g)
+        table = c.table.cpu()
+        for b, n in enumerate(lens):
+            low = max(0, n - rows + 1 - window)
+            table[b, :low // ps] = -1
+            table[b, -(-n // ps):] = 10 ** 6
+        c.table.copy_(table)
+        check_attention(c, randn((len(lens), rows, 8, 64), g, dtype), lens, kv, window=window)
+
+
+@pytest.mark.parametrize("dtype,e4m3", KINDS)
 def test_a_window_past_every_position_is_none(dtype, e4m3):
     c = new_cache(2, 40, 16, 2, 64, dtype, e4m3)
     g = gen(0)

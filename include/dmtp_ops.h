@@ -112,8 +112,9 @@ int dmtp_paged_read(const dmtp_paged_kv* c, const int32_t* seq, const int32_t* p
  * positions are left out. A NaN or an infinity reaches the rows that see its position and no
  * other. |scale| <= 1e30.
  * Scores, softmax statistics and sums are fp32; products of bf16 rows run on the tensor
- * cores with the weights as bf16 pairs (16 bits), of E4M3 rows with fp16 weights. Results
- * do not depend on timing: the same call gives the same bits. */
+ * cores with the weights as bf16 pairs (16 bits), of E4M3 rows with fp16 weights (v_scale up
+ * to 2^40; values of rows scaled by less than 2^-60 count to 2^-76). Results do not depend on timing:
+ * the same call gives the same bits. */
 typedef struct {
   const void* q;
   void* out;

@@ -171,10 +171,13 @@ __device__ __forceinline__ void block(const PagedAttn& p, State<HD, NT>& z,
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       kf[h] = sS[g + 8 * h];
-      const uint32_t u = __float_as_uint(sS[16 + g + 8 * h]);  // 2^(u >> 23 - 127) times [1, 2)
-      ve[h] = __uint_as_float(0x4b000000u | u >> 23) - 8388735.f;
-      vm[h] = __uint_as_float(0x3f800000u | (u & 0x7fffffu));
-      vi[h] = pow2f(127 - (int)(u >> 23));
+      // 2^ve vm, ve its exponent but at least -60: rows of smaller ones neither lose their weight
+      // in the sum (2^-86 of the largest is the least that counts) nor make it overflow
+      const float vs = sS[16 + g + 8 * h];
+      const uint32_t u = max(__float_as_uint(vs) >> 23, 67u);
+      ve[h] = __uint_as_float(0x4b000000u | u) - 8388735.f;
+      vi[h] = pow2f(127 - (int)u);
+      vm[h] = vs * vi[h];
     }
   }
   uint32_t pk[NT][2], pb[NT][2], lb[NT][2];

@@ -493,6 +493,34 @@ def test_attention_extreme_scores(dtype, e4m3):
     check_attention(c, q, [n], kv, scale=-0.25)
 
 
+@pytest.mark.parametrize("hd,rows", [(64, 1), (128, 8)])
+def test_attention_of_value_rows_of_very_different_sizes(hd, rows):
+    """E4M3 value rows near 0 (scale 2^-126, an fp32 row of 1e-36 as a bf16 one) next to ordinary
+    ones: they add next to nothing to the output, but their weights count in full. Alone, they
+    are good to n 2^-76: a weight times 2^(e + 60) is rounded to fp16, by 2^-25 at most where it
+    is below the normal range, of values up to 448 in units of 2^-60."""
+    lens = [1, 16, 333, 2000]
+    for tiny in ("some", "most", "all"):
+        c = new_cache(len(lens), 40, 64, 2, hd, BF, True, fill=1.0)
+        g = gen(hd)
+        n = sum(lens)
+        seq = np.concatenate([np.full(x, b) for b, x in enumerate(lens)])
+        pos = np.concatenate([np.arange(x) for x in lens])
+        small = torch.rand((n, 2, 1), device="cuda", generator=g) < {"some": 0.5, "most": 0.95, "all": 2}[tiny]
+        v = randn((n, 2, hd), g, FP)
+        v = torch.where(small, v * 1e-36, v)
+        c.write(randn((n, 2, hd), g, BF, 1.5), v.to(BF), i32(seq), i32(pos))
+        kv = stored(c, lens)
+        q = randn((len(lens), rows, 8, hd), g, BF, 1.5)
+        if tiny != "all":
+            check_attention(c, q, lens, kv)
+            continue
+        assert float(c.v_scale.min()) == 2.0 ** -126
+        out = np64(c.attention(q, i32(lens)))
+        ref, _ = reference(np64(q), kv, lens, rows, 0, hd ** -0.5, pair=False)
+        assert (np.abs(out - ref).max((1, 2, 3)) <= np.asarray(lens) * 2.0 ** -76).all()
+
+
 def test_attention_streams_graphs_and_workspaces():
     """On a side stream; two calls captured into two graphs with workspaces of their own,
     replayed at once on two streams with lengths that changed since the capture."""

@@ -144,7 +144,9 @@ extern "C" int dmtp_paged_attention(const dmtp_paged_kv* c, const dmtp_paged_que
   const int64_t strides[6] = {a->q_seq, a->q_row, a->q_head, a->o_seq, a->o_row, a->o_head};
   for (int64_t s : strides)
     if (s < 0 || !mult(s * es, 16)) return DMTP_EINVAL;
-  if (a->o_head < hd || !(a->scale >= -1e30f && a->scale <= 1e30f)) return DMTP_EINVAL;
+  // (output rows of one address)
+  if (a->o_head < hd || (a->rows > 1 && a->o_row < hd) || (c->n_seqs > 1 && a->o_seq < hd)) return DMTP_EINVAL;
+  if (!(a->scale >= -1e30f && a->scale <= 1e30f)) return DMTP_EINVAL;
   PagedPlan pl;
   const int r = plan(c, a, &pl);
   if (r) return r;

@@ -350,7 +350,8 @@ extern "C" int dmtp_paged_write(const dmtp_paged_kv* c, const dmtp_paged_rows* r
     return DMTP_EINVAL;
   if (r->q && (r->n_heads < 1 || r->n_heads > 4096 ||
                !row_ok(r->q, r->q_row, r->q_head, es, hd, r->n_heads) ||
-               !row_ok(r->q_out, r->qo_row, r->qo_head, es, hd, r->n_heads)))
+               !row_ok(r->q_out, r->qo_row, r->qo_head, es, hd, r->n_heads) ||
+               (r->n_rows > 1 && r->qo_row < hd)))  // rows of one address
     return DMTP_EINVAL;
   // theta >= 1: every pair's rate is at most one radian per position, below one turn
   if (!(r->rope_theta == 0.f || (r->rope_theta >= 1.f && r->rope_theta <= 3.4e38f))) return DMTP_EINVAL;
@@ -375,7 +376,7 @@ extern "C" int dmtp_paged_write(const dmtp_paged_kv* c, const dmtp_paged_rows* r
   const int items = (r->q ? r->n_heads : 0) + 2 * c->n_kv_heads, ng = 256 / a.group;
   const int blocks = (items + ng - 1) / ng;
   const bool few = r->n_rows < 304;
-  const dim3 grid(few ? r->n_rows : (r->n_rows + 3) / 4, few ? (blocks < 65535 ? blocks : 65535) : 1);
+  const dim3 grid(few ? r->n_rows : (r->n_rows - 1) / 4 + 1, few ? (blocks < 65535 ? blocks : 65535) : 1);
   const Turns* t = r->rope_theta > 0.f ? &turns_of(r->rope_theta, hd) : nullptr;
   static const Turns none = {};
   auto k = few ? (c->dtype ? (c->e4m3 ? k_paged_write<bf16, true, 1> : k_paged_write<bf16, false, 1>)

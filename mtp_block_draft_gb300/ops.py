@@ -60,6 +60,14 @@ def _bad(what: str):
     raise DmtpError(-1, what)
 
 
+def _pack(s, *args) -> bytes:
+    """The packed struct; a number that its field cannot hold is an argument error."""
+    try:
+        return s.pack(*args)
+    except (struct.error, OverflowError) as e:
+        _bad(str(e))
+
+
 def _dtype(c, t) -> int:
     """dtype code of a float tensor: 0 fp32, 1 bf16."""
     d = t.dtype
@@ -169,22 +177,25 @@ class DmtpPagedCache:
 
     def _rows(self, t, n, heads, what):
         """Row and head strides of t [n, heads, head_dim]."""
-        s0, s1, s2 = t.stride()
-        if t.dtype is not self.dtype or t.shape != (n, heads, self.head_dim) or s2 != 1 or \
-                t.get_device() != self._dev:
-            _bad(f"{what}: [{n}, {heads}, {self.head_dim}] of the cache's dtype and device")
-        return s0, (s1 if heads > 1 else self.head_dim)
+        if t.dtype is self.dtype and t.shape == (n, heads, self.head_dim) and \
+                t.get_device() == self._dev:
+            s0, s1, s2 = t.stride()
+            if s2 == 1:
+                return (s0 if n > 1 else heads * self.head_dim), (s1 if heads > 1 else self.head_dim)
+        _bad(f"{what}: [{n}, {heads}, {self.head_dim}], head_dim dense, of the cache's dtype and device")
 
     def write(self, k, v, seq, pos, q=None, q_out=None, rope_theta: float = 0.0):
         """dmtp_paged_write: rows k, v [n, n_kv_heads, head_dim] to positions pos of
         sequences seq (int32 [n]; seq < 0: skipped), rotated first if rope_theta > 0. With q
         [n, n_heads, head_dim] returns the rotated queries (q_out, or a new tensor)."""
         c, dev = _c(), self._dev
-        n, h = k.shape[0], self.n_kv_heads
+        n, h = len(seq), self.n_kv_heads
         kr, kh = self._rows(k, n, h, "k")
         vr, vh = self._rows(v, n, h, "v")
         qp = qop = qr = qh = qor = qoh = heads = 0
         if q is not None:
+            if q.dim() != 3:
+                _bad("q: [n, n_heads, head_dim]")
             heads = q.shape[1]
             if q_out is None:
                 q_out = c.torch.empty(q.shape, dtype=q.dtype, device=q.device)
@@ -192,9 +203,9 @@ class DmtpPagedCache:
             qor, qoh = self._rows(q_out, n, heads, "q_out")
             qp, qop = q.data_ptr(), q_out.data_ptr()
         _run(c, c.paged_write, dev, "dmtp_paged_write", self._c,
-             _ROWS.pack(qp, k.data_ptr(), v.data_ptr(), qop, qr, qh, kr, kh, vr, vh, qor, qoh,
-                        _vector(seq, c.int32, n, dev, "seq"),
-                        _vector(pos, c.int32, n, dev, "pos"), n, heads, rope_theta), self._err)
+             _pack(_ROWS, qp, k.data_ptr(), v.data_ptr(), qop, qr, qh, kr, kh, vr, vh, qor, qoh,
+                   _vector(seq, c.int32, n, dev, "seq"),
+                   _vector(pos, c.int32, n, dev, "pos"), n, heads, rope_theta), self._err)
         return q_out
 
     def read(self, seq, pos, k_out=None, v_out=None):
@@ -224,6 +235,8 @@ class DmtpPagedCache:
         allocator for this call."""
         c, dev = _c(), self._dev
         shape = q.shape
+        if len(shape) != 4:
+            _bad("q: [n_seqs, rows, n_heads, head_dim]")
         B, rows, heads, hd = shape
         if out is None:
             out = c.torch.empty(shape, dtype=q.dtype, device=q.device)
@@ -242,7 +255,7 @@ class DmtpPagedCache:
             qr = orow = hd
         if heads == 1:
             qh = oh = hd
-        a = _QUERY.pack(q.data_ptr(), out.data_ptr(), qb, qr, qh, ob, orow, oh,
+        a = _pack(_QUERY, q.data_ptr(), out.data_ptr(), qb, qr, qh, ob, orow, oh,
                         _vector(kv_len, c.int32, B, dev, "kv_len"), rows, heads, window,
                         self._scale if scale is None else scale)
         n = self._ws_bytes.get((rows, heads))
@@ -261,7 +274,7 @@ class DmtpPagedCache:
 
     def attention_workspace(self, rows: int, n_heads: int) -> int:
         """Bytes of workspace that attention() needs for q of these rows and heads."""
-        a = _QUERY.pack(0, 0, 0, 0, 0, 0, 0, 0, 0, rows, n_heads, 0, 1.0)
+        a = _pack(_QUERY, 0, 0, 0, 0, 0, 0, 0, 0, 0, rows, n_heads, 0, 1.0)
         size = C.c_size_t()
         _check(_c().paged_attention_workspace(self._c, a, C.byref(size)),
                "dmtp_paged_attention_workspace")
@@ -279,10 +292,11 @@ class DmtpPagedCache:
 
 def _matrix(t, shape, dtype, dev: int, what: str) -> int:
     """Row pitch of a matrix with dense rows."""
-    s0, s1 = t.stride()
-    if t.shape != shape or t.dtype is not dtype or s1 != 1 or t.get_device() != dev:
-        _bad(f"{what}: {dtype} {tuple(shape)} with dense rows on the same device")
-    return s0 if shape[0] > 1 else shape[1]
+    if t.shape == shape and t.dtype is dtype and t.get_device() == dev:
+        s0, s1 = t.stride()
+        if s1 == 1 or shape[1] == 1:
+            return s0 if shape[0] > 1 else shape[1]
+    _bad(f"{what}: {dtype} {tuple(shape)} with dense rows on the same device")
 
 
 def add_rmsnorm_e4m3(x, y, gain, eps: float = 1e-6, x_out=None, q=None, scale=None):
@@ -310,7 +324,7 @@ def add_rmsnorm_e4m3(x, y, gain, eps: float = 1e-6, x_out=None, q=None, scale=No
         scale = c.torch.empty(rows, dtype=c.fp32, device=x.device)
     qr = _matrix(q, shape, c.f8, dev, "q")
     _run(c, c.add_rmsnorm_e4m3, dev, "dmtp_add_rmsnorm_e4m3",
-         _NORM.pack(x.data_ptr(), yp, _vector(gain, gain.dtype, d, dev, "gain"), xop, q.data_ptr(),
+         _pack(_NORM, x.data_ptr(), yp, _vector(gain, gain.dtype, d, dev, "gain"), xop, q.data_ptr(),
                     _vector(scale, c.fp32, rows, dev, "scale"), xr, yr, xor, qr, rows, d, x_dt,
                     y_dt, g_dt, eps))
     return (x if x_out is None else x_out), q, scale
@@ -333,7 +347,7 @@ def sample_rows(logits, u, temperature=None, top_k=None, top_p=None, min_p=None,
         ids = c.torch.empty(rows, dtype=c.int32, device=logits.device)
     f, i = c.fp32, c.int32
     _run(c, c.sample_rows, dev, "dmtp_sample_rows",
-         _SAMPLE.pack(logits.data_ptr(), ld, rows, V, dt, _vector(u, f, rows, dev, "u"),
+         _pack(_SAMPLE, logits.data_ptr(), ld, rows, V, dt, _vector(u, f, rows, dev, "u"),
                       0 if temperature is None else _vector(temperature, f, rows, dev, "temperature"),
                       0 if top_k is None else _vector(top_k, i, rows, dev, "top_k"),
                       0 if top_p is None else _vector(top_p, f, rows, dev, "top_p"),

@@ -172,6 +172,33 @@ def test_sample_refuses(lib, bad):
     assert lib.dmtp_sample_rows(C.byref(sample(**bad)), None) == EINVAL
 
 
+def test_output_rows_of_one_address_are_refused(lib):
+    for bad in (dict(o_row=0, rows=2), dict(o_seq=0)):
+        assert lib.dmtp_paged_attention(C.byref(cache()), C.byref(query(**bad)), PTR, 1 << 40, None,
+                                        None) == EINVAL
+    assert lib.dmtp_paged_write(C.byref(cache()), C.byref(rows(qo_row=0)), None, None) == EINVAL
+
+
+def test_binding_refuses_numbers_and_shapes_that_do_not_fit(lib):
+    from mtp_block_draft_gb300 import add_rmsnorm_e4m3, sample_rows
+    table = torch.zeros((2, 4), dtype=torch.int32)
+    k = torch.zeros((8, 2, 16, 64), dtype=torch.bfloat16)
+    c = DmtpPagedCache(k, k, table)
+    seq = torch.zeros(3, dtype=torch.int32)
+    kv, q = torch.zeros((3, 2, 64), dtype=torch.bfloat16), torch.zeros((2, 1, 4, 64), dtype=torch.bfloat16)
+    x = torch.zeros((2, 64))
+    for call in (lambda: c.attention(q, seq[:2], window=1 << 31), lambda: c.attention(q, seq[:2], scale=1e39),
+                 lambda: c.attention(q[0], seq[:2]), lambda: c.attention(q, seq[:2], out=q[0]),
+                 lambda: c.write(kv, kv, seq, seq, rope_theta=1e39), lambda: c.write(kv[0], kv, seq, seq),
+                 lambda: c.write(kv, kv, seq, seq, q=kv[0]), lambda: c.write(kv[:2], kv, seq, seq),
+                 lambda: c.attention_workspace(0, 4), lambda: c.attention_workspace(1 << 40, 4),
+                 lambda: add_rmsnorm_e4m3(x, None, torch.ones(64), eps=1e39),
+                 lambda: add_rmsnorm_e4m3(x, x[0], torch.ones(64)), lambda: add_rmsnorm_e4m3(x[0], x[0], x[0]),
+                 lambda: sample_rows(x[0], x[0, :1]), lambda: sample_rows(x, x[0])):
+        with pytest.raises(DmtpError):
+            call()
+
+
 def test_binding_refuses_tensors_of_the_wrong_kind(lib):
     table = torch.zeros((2, 4), dtype=torch.int32)
     k = torch.zeros((8, 2, 16, 64), dtype=torch.bfloat16)

@@ -372,11 +372,17 @@ extern "C" int dmtp_paged_write(const dmtp_paged_kv* c, const dmtp_paged_rows* r
                              r->q ? r->q_row : 0, r->q ? r->q_head : 0, r->q ? r->qo_row : 0, r->q ? r->qo_head : 0};
   for (int64_t x : strides) a.wide = a.wide && mult(x * es, 16);
   for (const void* p : {r->k, r->v, r->q, (const void*)r->q_out}) a.wide = a.wide && aligned_to(p, 16);
-  // few rows: one a CTA, its heads spread over CTAs, one a group; many: four rows a CTA
+  // Few rows: one a CTA, its heads spread over CTAs, one a group, so that a row's chain of loads
+  // is walked once. More: four rows a CTA, whose pages and angles are found together, spread over
+  // CTAs while there are fewer than four an SM. Rows of 40 heads of 128, us, few / many: 32 into
+  // bf16 pages 3.1 / 3.3 (not spread 5.1), 256 3.5 / 4.3, 512 5.0 / 5.0, 768 6.5 / 5.7, 1024 7.7 /
+  // 6.7, 2047 14.7 / 10.3; into E4M3 pages 256 4.0 / 4.7, 512 5.7 / 5.7, 768 7.4 / 6.3; of 144
+  // heads 64 3.5 / 3.8, 307 7.2 / 6.9, 600 12.3 / 10.3.
   const int items = (r->q ? r->n_heads : 0) + 2 * c->n_kv_heads, ng = 256 / a.group;
   const int blocks = (items + ng - 1) / ng;
-  const bool few = r->n_rows < 304;
-  const dim3 grid(few ? r->n_rows : (r->n_rows - 1) / 4 + 1, few ? (blocks < 65535 ? blocks : 65535) : 1);
+  const bool few = (int64_t)r->n_rows * blocks <= 608;
+  const int quads = (r->n_rows - 1) / 4 + 1, spread = quads < 608 ? 608 / quads : 1, rounds = (4 * items + ng - 1) / ng;
+  const dim3 grid(few ? r->n_rows : quads, few ? blocks : spread < rounds ? spread : rounds);
   const Turns* t = r->rope_theta > 0.f ? &turns_of(r->rope_theta, hd) : nullptr;
   static const Turns none = {};
   auto k = few ? (c->dtype ? (c->e4m3 ? k_paged_write<bf16, true, 1> : k_paged_write<bf16, false, 1>)

@@ -671,7 +671,8 @@ def check_rows(z, u, t, k, p, m):
 
 @pytest.mark.parametrize("V,n", [(1, 24), (2, 24), (31, 24), (512, 24), (513, 60), (2049, 24), (5000, 60), (8193, 24),
                                  (32000, 24), (151936, 24), (262144, 12), (8193, 130), (20001, 128), (32000, 127),
-                                 (32000, 140), (151936, 129), (262144, 128)])
+                                 (32000, 140), (151936, 129), (262144, 128), (32000, 13), (50176, 24),
+                                 (50177, 30), (32000, 60), (100352, 40), (100353, 40), (50176, 154)])
 @pytest.mark.parametrize("dtype", [FP, BF])
 def test_sample_rows(V, n, dtype):
     """Every mixture of filters, one per row, for few rows and many. bf16 logits tie often."""
@@ -734,7 +735,7 @@ def test_sample_masked_rows_and_odd_numbers(V, copies):
     assert [ids[i] for i in (0, 1, 2, 4, 5)] == [best] * 5 and kept[3] == V
 
 
-@pytest.mark.parametrize("V,copies", [(100, 1), (20000, 1), (20000, 33)])
+@pytest.mark.parametrize("V,copies", [(100, 1), (20000, 1), (20000, 33), (104001, 33)])
 def test_sample_temperatures_past_their_range(V, copies):
     """Above 1e30, infinity among them, a temperature counts as 1e30: ordinary logits weigh the
     same, the type's lowest value still weighs nothing."""
@@ -750,6 +751,31 @@ def test_sample_temperatures_past_their_range(V, copies):
             ids, kept = run_sample(z.repeat(copies, 1), u, [t] * n, *args)
             want = [plain_pick(np64(z)[i % 4], float(np.float32(u[i])), 1e30, k, float(np.float32(p)), m) for i in range(4)]
             assert [(int(a), int(b)) for a, b in zip(ids, kept)] == want * copies, (t, k, p)
+
+
+def test_sample_masked_rows_among_many_of_a_large_vocabulary():
+    inf, nan, V, copies = float("inf"), float("nan"), 104001, 14
+    z = randn((10, V), gen(0), FP, 3.0)
+    z[0] = -inf
+    z[1] = nan
+    z[2, 1:] = -inf
+    z[3, :-1] = torch.finfo(FP).min
+    z[4] = torch.finfo(FP).min
+    z[5, 10], z[5, 20] = inf, inf
+    z[6, ::2] = -inf
+    z[6, 1::4] = nan
+    z[7] = torch.round(z[7])               # large groups of ties
+    z[8, 50] = torch.finfo(FP).max
+    z[9, :3000] -= 40.0                    # the largest logits come late in the row
+    u = [0.5, 0.5, 0.9, 0.3, 0.6, 0.7, 0.2, 0.99, 0.5, 0.5]
+    zz = np64(z)
+    for t in (1.0, 0.0, 1e-3, 1e6):
+        for k, p, m in ((0, 1.0, 0.0), (3, 0.9, 0.0), (5000, 0.7, 0.0), (0, 0.5, 0.1)):
+            n = 10 * copies
+            ids, kept = run_sample(z.repeat(copies, 1), u * copies, [t] * n, [k] * n, [p] * n, [m] * n)
+            want = [plain_pick(zz[i], float(np.float32(u[i])), float(np.float32(t)), k, float(np.float32(p)),
+                               float(np.float32(m))) for i in range(10)]
+            assert [(int(a), int(b)) for a, b in zip(ids, kept)] == want * copies, (t, k, p, m)
 
 
 def test_sample_frequencies():
@@ -817,3 +843,25 @@ def test_the_norm_matches_the_draft_heads_rows():
     want, sc = fp8.quantize_rows(h)
     # float64 and fp32 agree unless a value lies within 4u of a rounding border
     assert (np64(s) == sc).all() and np.mean(np64(q) != want) < 1e-3
+
+
+@pytest.mark.parametrize("hq,hkv", [(8, 1), (32, 4), (128, 8)])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_rows_written_together_and_apart_are_the_same(hq, hkv, e4m3):
+    """Many rows in one call, and the same in calls of a few: the same bits, whatever the form."""
+    n, hd = 1301, 64
+    g = gen(hq)
+    k, v, q = randn((n, hkv, hd), g), randn((n, hkv, hd), g), randn((n, hq, hd), g)
+    caches = [new_cache(3, 28, 16, hkv, hd, BF, e4m3) for _ in range(2)]
+    seq, pos = i32([i % 4 - 1 for i in range(n)]), i32([i // 4 for i in range(n)])
+    a, b = torch.zeros_like(q), torch.zeros_like(q)
+    caches[0].write(k, v, seq, pos, q=q, q_out=a, rope_theta=1e4)
+    for i in range(0, n, 50):
+        s = slice(i, i + 50)
+        caches[1].write(k[s], v[s], seq[s], pos[s], q=q[s], q_out=b[s], rope_theta=1e4)
+    assert torch.equal(a, b)
+    for x, y in ((caches[0].k, caches[1].k), (caches[0].v, caches[1].v)):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+    if e4m3:
+        assert torch.equal(caches[0].k_scale, caches[1].k_scale)
+        assert torch.equal(caches[0].v_scale, caches[1].v_scale)

@@ -8,7 +8,8 @@
 // corrected once in that precision: the factor is the correctly rounded one but for the last
 // bit of about one row in a hundred, so a row's E4M3 values hardly depend on how the sum was
 // split. Sixteen values a thread, so that what every thread does once per row (the reductions,
-// the factor) stays below what it does per value.
+// the factor) stays below what it does per value
+// (with few rows eight, see launch()).
 #include "paged.cuh"
 
 namespace {
@@ -24,38 +25,11 @@ __device__ __forceinline__ F2 add(F2 a, F2 b) {
   F2 s = two_sum(a.hi, b.hi);
   return F2{s.hi, s.lo + (a.lo + b.lo)};
 }
-// Packed single precision: two of a thread's sums of squares side by side.
-typedef unsigned long long f32x2;
-__device__ __forceinline__ f32x2 pack(float a, float b) {
-  f32x2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float2 unpack(f32x2 a) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
-  return r;
-}
-__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
-  f32x2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
-  f32x2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
 // hi += x^2, the part of it that the sum's rounding loses carried over to the next one.
 __device__ __forceinline__ void add_squares(f32x2& hi, f32x2& carry, f32x2 x, f32x2 minus) {
   const f32x2 y = fma2(x, x, carry), s = add2(hi, y);
   carry = fma2(fma2(hi, minus, s), minus, y);  // y - (s - hi)
   hi = s;
-}
-__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
-  f32x2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
 }
 // Eight values as they lie in memory (fp32: two steps of 16 bytes, bf16: one).
 template <typename T>
@@ -251,6 +225,16 @@ cudaError_t launch(const dmtp_norm_args& a, cudaStream_t st) {
   auto grid = [&](int ctas) { return a.rows < 152 * ctas ? a.rows : 152 * ctas; };
 #define DMTP_NORM(NV_, TH_) \
   return launch_op(k_add_rmsnorm_e4m3<TX, TY, NV_, TH_>, grid(ctas_of<TX, TY, NV_, TH_>()), TH_, 0, st, false, 1, a)
+  // A CTA an SM and less: eight values a thread, the row's latency counts. More: sixteen. us, eight /
+  // sixteen: 64 rows of 2048 bf16 2.5 / 2.8, 152 2.6 / 3.0, 608 3.7 / 3.4, 8188 25.3 / 23.1; of 4096
+  // fp32, 64 rows 3.1 / 3.3, 152 3.15 / 3.3, 304 4.7 / 4.2, 8188 77.7 / 69.3; of 8192 bf16, 32 rows
+  // 4.9 (with 1024 threads) / 3.5.
+  if (a.rows <= 152) {
+    if (d8 > 32 && d8 <= 64) DMTP_NORM(1, 64);
+    if (d8 > 64 && d8 <= 128) DMTP_NORM(1, 128);
+    if (d8 > 128 && d8 <= 256) DMTP_NORM(1, 256);
+    if (d8 > 256 && d8 <= 512) DMTP_NORM(1, 512);
+  }
   if (d8 <= 32) DMTP_NORM(1, 32);
   if (d8 <= 64) DMTP_NORM(2, 32);
   if (d8 <= 128) DMTP_NORM(2, 64);

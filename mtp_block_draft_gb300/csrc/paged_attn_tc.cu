@@ -15,6 +15,12 @@
 //   32            2 of two warps    32 keys a stage
 //   64            one of four       64 keys a stage
 //
+// The smallest QN that holds a kv head's queries (of more than 64, chunks of 64). 32 sequences of
+// 512 to 4096 positions, 4 kv heads of 128, us with QN 8 / 16 / 32 / 64: 8 queries in bf16 30.4 /
+// 33.4 / 39.8 / 59.3, in E4M3 23.2 / 29.6 / 37.8 / 55.8; 16 42.5 / 35.8 / 41.6 / 61.0, 34.8 / 31.2 /
+// 39.8 / 57.8; 32 68.5 / 53.0 / 44.5 / 64.3, 58.5 / 48.2 / 41.8 / 59.5; 64 121 / 93.3 / 78.5 / 71.6,
+// 104 / 86.0 / 72.3 / 65.9.
+//
 // A warp has at most 16 queries: with 32 (and half the conversions of E4M3 rows) only two CTAs fit
 // an SM, and 32 sequences of 512 to 4096 E4M3 positions x 64 queries took 78 us instead of 65.
 //
@@ -345,9 +351,9 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, E8, QN>::CTAS) k_paged_att
   constexpr int CPR = RB / 16, RPI = 32 * QG / CPR, NI = RPI < 16 ? 16 / RPI : 1;  // rows of one copy of the team
   const bool copies = RPI <= 16 || (qg * 32 + lane) / CPR < 16;  // (a team may be larger than a block)
   const bool paged16 = p.m.page_size % 16 == 0;  // a block lies in one page
-  // Cached rows pass through L2 once (unless several chunks read them): the tables, lengths and
-  // partial results should outlive them there.
-  const uint64_t stream = p.chunks > 1 ? policy_evict_normal() : policy_evict_first();
+  // Cached rows pass through L2 once: the tables, lengths and partial results should outlive them
+  // there. (With several chunks of queries it makes no difference: 129.3 us, kept like the rest 130.5.)
+  const uint64_t stream = policy_evict_first();
   // Pages of this team's blocks, 32 of them at a time: lane i holds the block of tile
   // win_t + i / NSUB, number i % NSUB, of sequence win_b. One table read serves them all.
   int win_b = -1, win_t = 0, win_page = -1, win_off = 0;

@@ -84,35 +84,6 @@ __device__ __forceinline__ unsigned long long part_of(float f, unsigned long lon
 constexpr int kShift = 44;  // weight 1 is 2^44: 2^18 of them stay below 2^63
 constexpr int kBins = 2048, kFine = 512;
 
-// Two floats in one register pair: Blackwell's packed single-precision instructions.
-typedef unsigned long long f32x2;
-__device__ __forceinline__ f32x2 pack(float a, float b) {
-  f32x2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float2 unpack(f32x2 a) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
-  return r;
-}
-__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
-  f32x2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
-  f32x2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
-  f32x2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ f32x2 both(float a) { return pack(a, a); }
-
 struct Weigh {
   float top, chi, clo, cb;
   const unsigned long long* table;
@@ -755,7 +726,7 @@ __global__ void __launch_bounds__(THREADS) k_sample_rows(const RowsArgs sa) {
 // Rows of 151936 in a captured graph, us, clusters of eight / this: top_k 50 with top_p 0.9, 96
 // rows 82 / 106, 128 rows 109 / 110, 256 rows 204 / 195; top_p 0.9 alone 114 / 142, 150 / 144,
 // 282 / 262.
-constexpr int kManyRows = 128;
+constexpr int kManyRows = 128, kManyVocab = 100352;  // (two CTAs hold a row of as many)
 constexpr int kStream = 512, kSegment = 1024, kAhead = 256;
 
 struct StreamShared {
@@ -1210,7 +1181,7 @@ using namespace dmtp;
 namespace {
 
 template <typename T, int THREADS>
-cudaError_t launch(const dmtp_sample_args& a, unsigned cluster, cudaStream_t st) {
+cudaError_t launch(const dmtp_sample_args& a, cudaStream_t st) {
   static unsigned long long done = 0;
   auto k = k_sample_rows<T, THREADS>;
   constexpr int kFixed = (sizeof(Shared<THREADS>) + 15) / 16 * 16;
@@ -1219,14 +1190,30 @@ cudaError_t launch(const dmtp_sample_args& a, unsigned cluster, cudaStream_t st)
     const int p = (n + 2 * THREADS - 1) / (2 * THREADS);
     return p + 1 - p % 2;
   };
-  const int most = kFixed + 2 * pairs_of(DMTP_OPS_MAX_SAMPLE_VOCAB / 8) * THREADS * 4;
-  if (!smem_limit((const void*)k, most, &done)) return cudaErrorInvalidValue;
+  auto bytes_of = [&](unsigned c) { return kFixed + 2 * pairs_of((a.vocab + (int)c - 1) / (int)c) * THREADS * 4; };
+  constexpr int kMost = 227 * 1024;  // the largest slice: a CTA of its own on an SM
+  if (!smem_limit((const void*)k, kMost, &done)) return cudaErrorInvalidValue;
+  // CTAs of a row. One while a pass over the row is short; else as many as leave each an SM of its
+  // own, up to 8 (the barriers of a cluster cost more where it shares its SMs: above 8 rows only
+  // if the row is long), and if the slices do not fit that way, 8 that share the SMs.
+  // Rows of top_k 50 and top_p 0.9, us with 1 / 2 / 4 / 8 CTAs:
+  //            1 row                      16 rows                    64 rows
+  //   8192     16.5 / 17.2 / 16.4 / 15.9  17.4 / 18.6 / 17.9 / 19.6  17.8 / 18.9 / 22.3 / 40.5
+  //   32768    21.9 / 19.4 / 17.2 / 16.4  24.9 / 22.2 / 19.6 / 21.8  25.2 / 22.8 / 24.8 / 44.2
+  //   100000      - / 30.2 / 23.2 / 20.1     - / 32.0 / 24.8 / 22.8     - / 35.0 / 48.4 / 50.2
+  //   151936      -      - / 24.4 / 19.8     -      - / 28.8 / 23.8     -      - / 61.7 / 57.4
+  // 32 rows of 32768 22.3 with 2, 20.1 with 4, of 100000 25.0 with 4, 26.4 with 8; 127 rows of
+  // 32768 25.7 / 28.8 / 45.8 / 83.4; 256 rows of 32768 51.5 / 53.2 / 85.8 / 161 (streamed 73.7), of
+  // 100000 130.9 with 2 (streamed 153.8).
+  unsigned cluster = a.vocab <= 8192 ? 1 : a.rows <= 8 || a.vocab > 65536 ? 8 : 4;
+  while (cluster > 1 && (unsigned)a.rows * cluster > 152 && bytes_of(cluster / 2) <= kMost) cluster /= 2;
+  if (bytes_of(2) > kMost && (unsigned)a.rows * cluster > 152) cluster = 8;
   RowsArgs s;
   s.a = a;
-  s.slice = 2 * pairs_of((a.vocab + (int)cluster - 1) / (int)cluster) * THREADS;
+  s.slice = (bytes_of(cluster) - kFixed) / 4;
   const int es = sizeof(T);
   s.vec = aligned_to(a.logits, 16) && mult(a.ld * es, 16);
-  return launch_op(k, (unsigned)a.rows * cluster, THREADS, (size_t)(kFixed + s.slice * 4), st, false, cluster, s);
+  return launch_op(k, (unsigned)a.rows * cluster, THREADS, (size_t)bytes_of(cluster), st, false, cluster, s);
 }
 template <typename T>
 cudaError_t launch_stream(const dmtp_sample_args& a, cudaStream_t st) {
@@ -1241,9 +1228,8 @@ cudaError_t launch_stream(const dmtp_sample_args& a, cudaStream_t st) {
 }
 template <typename T>
 cudaError_t launch_t(const dmtp_sample_args& a, cudaStream_t st) {
-  const unsigned cluster = a.vocab > 8192 ? 8 : a.vocab > 2048 ? 2 : 1;
-  if (cluster == 8 && a.rows >= kManyRows) return launch_stream<T>(a, st);
-  return launch<T, 512>(a, cluster, st);
+  if (a.rows >= kManyRows && a.vocab > kManyVocab) return launch_stream<T>(a, st);
+  return launch<T, 512>(a, st);
 }
 
 }  // namespace

@@ -98,7 +98,7 @@ int plan(const dmtp_paged_kv* c, const dmtp_paged_query* a, PagedPlan* pl) {
     pl->grid = paged_tc_grid(hd, c->e4m3 != 0, pl->qn);
   } else {
     pl->qn = 8;
-    pl->grid = paged_simt_grid(hd, c->dtype, c->e4m3 != 0);
+    pl->grid = paged_simt_grid(hd);
   }
   pl->chunks = (nq + pl->qn - 1) / pl->qn;
   const int64_t reach = (int64_t)c->max_blocks * c->page_size;
@@ -176,8 +176,13 @@ extern "C" int dmtp_paged_attention(const dmtp_paged_kv* c, const dmtp_paged_que
                          : paged_attn_simt(p, pl, c->dtype, c->e4m3 != 0, st);
   if (le == cudaSuccess && !pl.whole) {
     const int nq = p.nq < pl.qn ? p.nq : pl.qn, units = p.units * c->n_seqs;
-    // a CTA's 16 warps go by the pieces that a unit has on average, and one more
-    const int pieces = pl.grid / units + 1, per = pieces > 24 ? 1 : pieces > 6 ? 4 : nq > 8 ? 16 : 8;
+    // A CTA's 16 warps go by the pieces that a unit has on average, and one more: all to one query
+    // while that leaves two CTAs an SM at most. The whole attention with 1 / 4 / 8 / 16 queries a
+    // CTA, us: 15 pieces x 32 units of 8 queries 18.5 / 18.9 / 19.5 / 19.5; 58 x 8 of 64 40.7 / 39.8
+    // / 41.7 / 43.1; 115 x 4 of 64 39.3 / 41.5 / 44.6 / 49.1; 10 x 32 of 32 32.0 / 26.3 / 26.8 /
+    // 27.4; 4 x 128 of 8 35.9 / 30.5 / 30.7 / 30.9, of 64 118 / 76.6 / 68.9 / 65.8.
+    const int pieces = pl.grid / units + 1;
+    const int per = pieces > 12 && units * nq <= 304 ? 1 : pieces > 6 ? 4 : nq > 8 ? 16 : 8;
     const dim3 grid(units < 1216 ? units : 1216, (nq + per - 1) / per);
     auto k = c->dtype ? (per == 1   ? k_paged_merge<bf16, 1>
                          : per == 4 ? k_paged_merge<bf16, 4>

@@ -193,6 +193,6 @@ struct PagedPlan {
 cudaError_t paged_attn_tc(const PagedAttn& p, const PagedPlan& pl, bool e8, cudaStream_t st);
 cudaError_t paged_attn_simt(const PagedAttn& p, const PagedPlan& pl, int dtype, bool e8, cudaStream_t st);
 int paged_tc_grid(int head_dim, bool e8, int qn);
-int paged_simt_grid(int head_dim, int dtype, bool e8);
+int paged_simt_grid(int head_dim);
 
 }  // namespace dmtp

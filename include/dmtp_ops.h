@@ -53,7 +53,8 @@ extern "C" {
  * head_dim values: k + p * page_stride is [n_kv_heads][page_size][head_dim] (elements),
  * likewise v. e4m3 = 0: values of `dtype`, k_scale and v_scale unused. e4m3 = 1: E4M3
  * values, and k_scale + p * scale_stride is [n_kv_heads][page_size] fp32 scales of the
- * rows (positive normal numbers below 2^127; dmtp_paged_write makes powers of two), likewise v_scale.
+ * rows (positive normal numbers below 2^127; dmtp_paged_write makes powers of two), likewise
+ * v_scale.
  * Position j of sequence s lies in page table[s * table_stride + j / page_size], row
  * j % page_size; 0 <= j < max_blocks * page_size. Entries past a sequence's length are not
  * read, nor are those whose positions all lie before the window of every row. Several entries may name one page (a shared prefix).
@@ -109,12 +110,12 @@ int dmtp_paged_read(const dmtp_paged_kv* c, const int32_t* seq, const int32_t* p
  * gets zeros. q and out: the cache's dtype, strides in elements, head_dim dense; row
  * pointers 16-byte aligned, strides multiples of 16 bytes. Lengths past the block table's
  * reach are cut there and set DMTP_OPS_ERR_POS; a bad page sets DMTP_OPS_ERR_PAGE and its
- * positions are left out. A NaN or an infinity reaches the rows that see its position and no
- * other. |scale| <= 1e30.
+ * positions are left out. A NaN or an infinity reaches the rows that see its position (a value
+ * whose weight rounds to 0 may not) and no other. |scale| <= 1e30.
  * Scores, softmax statistics and sums are fp32; products of bf16 rows run on the tensor
  * cores with the weights as bf16 pairs (16 bits), of E4M3 rows with fp16 weights (v_scale up
- * to 2^40; values of rows scaled by less than 2^-60 count to 2^-76). Results do not depend on timing:
- * the same call gives the same bits. */
+ * to 2^40; values of rows scaled by less than 2^-60 count to 2^-76). Results do not depend on
+ * timing: the same call gives the same bits. */
 typedef struct {
   const void* q;
   void* out;
@@ -134,8 +135,8 @@ int dmtp_paged_attention(const dmtp_paged_kv* c, const dmtp_paged_query* a, void
 /* x_out = x + y (rounded to x's type), and the unrounded sum's norm as E4M3 rows:
  * h = (x + y) / sqrt(mean((x + y)^2) + eps) * gain, q [rows][d] E4M3 values with row pitch
  * q_row, scale [rows] fp32. x, x_out: x_dtype; y: y_dtype; gain [d]: gain_dtype; row
- * pitches in elements. The sum of squares is fp32: |x + y| up to about 1e17. x_out may be x; y may be NULL (no addition; x_out may then be NULL
- * too). Limits: d a multiple of 8 up to DMTP_OPS_MAX_NORM_D; row starts 16-byte aligned
+ * pitches in elements. The sum of squares is fp32: |x + y| up to about 1e17. x_out may be x;
+ * y may be NULL (no addition; x_out may then be NULL too). Limits: d a multiple of 8 up to DMTP_OPS_MAX_NORM_D; row starts 16-byte aligned
  * (q: 8-byte), pitches >= d and multiples of 8; eps >= 0 and finite. */
 typedef struct {
   const void *x, *y, *gain;
@@ -161,8 +162,8 @@ int dmtp_add_rmsnorm_e4m3(const dmtp_norm_args* a, void* stream);
  * the largest finite number; a temperature counts as the nearest in [1e-30, 1e30]. A row that
  * keeps nothing gets id -1. kept[r] (optional) is the number of kept tokens. temperature, top_k, top_p, min_p: device arrays [rows], each
  * optional (NULL: 1, off, off, off). u: device fp32 [rows]. Weights and their sums are
- * integers (steps of 2^-44 of the largest, computed to about 2^-39), so a row's result depends on nothing
- * but its inputs. Limits: 1 <= vocab <= DMTP_OPS_MAX_SAMPLE_VOCAB, ld >= vocab. */
+ * integers (steps of 2^-44 of the largest, computed to about 2^-39), so a row's result depends
+ * on nothing but its inputs. Limits: 1 <= vocab <= DMTP_OPS_MAX_SAMPLE_VOCAB, ld >= vocab. */
 typedef struct {
   const void* logits;
   int64_t ld;

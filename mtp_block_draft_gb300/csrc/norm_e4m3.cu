@@ -10,6 +10,9 @@
 // split. Sixteen values a thread, so that what every thread does once per row (the reductions,
 // the factor) stays below what it does per value
 // (with few rows eight, see launch()).
+//
+// 8188 rows of 2048 bf16 take 22.9 us (117 MB, 0.75 of the copy rate; 70% of the issue slots used),
+// 32 rows of fp32 2.6 us, which is latency.
 #include "paged.cuh"
 
 namespace {
@@ -31,49 +34,6 @@ __device__ __forceinline__ void add_squares(f32x2& hi, f32x2& carry, f32x2 x, f3
   carry = fma2(fma2(hi, minus, s), minus, y);  // y - (s - hi)
   hi = s;
 }
-// Eight values as they lie in memory (fp32: two steps of 16 bytes, bf16: one).
-template <typename T>
-struct Raw {
-  uint4 u[sizeof(T) / 2];
-};
-template <typename T>
-__device__ __forceinline__ Raw<T> fetch(const T* p) {
-  Raw<T> r;
-#pragma unroll
-  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.u[i] = __ldcs(reinterpret_cast<const uint4*>(p) + i);
-  return r;
-}
-__device__ __forceinline__ void get8(const Raw<float>& r, float (&f)[8]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    f[4 * i] = __uint_as_float(r.u[i].x);
-    f[4 * i + 1] = __uint_as_float(r.u[i].y);
-    f[4 * i + 2] = __uint_as_float(r.u[i].z);
-    f[4 * i + 3] = __uint_as_float(r.u[i].w);
-  }
-}
-__device__ __forceinline__ void get8(const Raw<bf16>& r, float (&f)[8]) {
-  const uint32_t w[4] = {r.u[0].x, r.u[0].y, r.u[0].z, r.u[0].w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-}
-__device__ __forceinline__ void put8(float* p, const float (&f)[8]) {
-  *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
-  *reinterpret_cast<float4*>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
-}
-__device__ __forceinline__ void put8(bf16* p, const float (&f)[8]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&h);
-  }
-  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-}
-
 // CTAs of an SM: what the registers of a row and the next one allow. Measured on 8188 rows of
 // 2048 bf16 values: 512, 768, 1024, 1280, 1536 threads an SM 28.0, 24.5, 22.7, 26.4, 30.0 us.
 template <typename TX, typename TY, int NV, int THREADS>
@@ -95,8 +55,8 @@ __global__ void __launch_bounds__(THREADS, ctas_of<TX, TY, NV, THREADS>()) k_add
     for (int k = 0; k < NV; ++k) {
       const int i = threadIdx.x + k * THREADS;
       if (i < d8) {
-        rx[k] = fetch((const TX*)a.x + row * a.x_row + 8 * i);
-        if (a.y) ry[k] = fetch((const TY*)a.y + row * a.y_row + 8 * i);
+        fetch((const TX*)a.x + row * a.x_row + 8 * i, true, rx[k]);
+        if (a.y) fetch((const TY*)a.y + row * a.y_row + 8 * i, true, ry[k]);
       }
     }
   };
@@ -113,10 +73,10 @@ __global__ void __launch_bounds__(THREADS, ctas_of<TX, TY, NV, THREADS>()) k_add
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[k][e] = 0.f;
       if (i < d8) {
-        get8(rx[k], v[k]);
+        values(rx[k], v[k]);
         if (a.y) {
           float w[8];
-          get8(ry[k], w);
+          values(ry[k], w);
 #pragma unroll
           for (int e = 0; e < 8; e += 2) {
             const float2 s = unpack(add2(pack(v[k][e], v[k][e + 1]), pack(w[e], w[e + 1])));
@@ -130,7 +90,7 @@ __global__ void __launch_bounds__(THREADS, ctas_of<TX, TY, NV, THREADS>()) k_add
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int i = threadIdx.x + k * THREADS;
-      if (a.x_out && i < d8) put8((TX*)a.x_out + row * a.xo_row + 8 * i, v[k]);
+      if (a.x_out && i < d8) store8((TX*)a.x_out + row * a.xo_row + 8 * i, true, v[k]);
 #pragma unroll
       for (int e = 0; e < 8; e += 2) add_squares(hi2, lo2, pack(v[k][e], v[k][e + 1]), minus);
     }
@@ -167,9 +127,9 @@ __global__ void __launch_bounds__(THREADS, ctas_of<TX, TY, NV, THREADS>()) k_add
       if (i < d8) {
         float g[8];
         if (a.gain_dtype)
-          get8(Raw<bf16>{__ldg((const uint4*)a.gain + i)}, g);
+          values(Raw<bf16>{__ldg((const uint4*)a.gain + i)}, g);
         else
-          get8(Raw<float>{__ldg((const uint4*)a.gain + 2 * i), __ldg((const uint4*)a.gain + 2 * i + 1)}, g);
+          values(Raw<float>{__ldg((const uint4*)a.gain + 2 * i), __ldg((const uint4*)a.gain + 2 * i + 1)}, g);
 #pragma unroll
         for (int e = 0; e < 8; e += 2) {
           const float2 h = unpack(mul2(mul2(pack(v[k][e], v[k][e + 1]), r2), pack(g[e], g[e + 1])));

@@ -124,6 +124,59 @@ __device__ __forceinline__ float4 e4m3x4_to_f4(uint32_t u) {
   return make_float4(a.x, a.y, b.x, b.y);
 }
 
+// Eight consecutive values as they lie in memory; `wide`: at a 16-byte boundary (else fp32 at
+// one, bf16 at 8 bytes).
+template <typename T>
+struct Raw {
+  uint4 u[sizeof(T) / 2];
+};
+__device__ __forceinline__ void fetch(const float* p, bool, Raw<float>& r) {
+  r.u[0] = __ldcs(reinterpret_cast<const uint4*>(p));
+  r.u[1] = __ldcs(reinterpret_cast<const uint4*>(p + 4));
+}
+__device__ __forceinline__ void fetch(const bf16* p, bool wide, Raw<bf16>& r) {
+  if (wide) {
+    r.u[0] = __ldcs(reinterpret_cast<const uint4*>(p));
+  } else {
+    const uint2 a = __ldcs(reinterpret_cast<const uint2*>(p)), b = __ldcs(reinterpret_cast<const uint2*>(p + 4));
+    r.u[0] = make_uint4(a.x, a.y, b.x, b.y);
+  }
+}
+__device__ __forceinline__ void values(const Raw<float>& r, float (&f)[8]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    f[4 * i] = __uint_as_float(r.u[i].x);
+    f[4 * i + 1] = __uint_as_float(r.u[i].y);
+    f[4 * i + 2] = __uint_as_float(r.u[i].z);
+    f[4 * i + 3] = __uint_as_float(r.u[i].w);
+  }
+}
+__device__ __forceinline__ void values(const Raw<bf16>& r, float (&f)[8]) {
+  const uint32_t w[4] = {r.u[0].x, r.u[0].y, r.u[0].z, r.u[0].w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void store8(float* p, bool wide, const float (&f)[8]) {
+  *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+  *reinterpret_cast<float4*>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
+}
+__device__ __forceinline__ void store8(bf16* p, bool wide, const float (&f)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  if (wide) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+    *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    *reinterpret_cast<uint2*>(p + 4) = make_uint2(w[2], w[3]);
+  }
+}
 // 16-byte asynchronous copy global -> shared; bytes = 0 writes zeros instead.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)

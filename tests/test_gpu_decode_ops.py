@@ -865,3 +865,61 @@ def test_rows_written_together_and_apart_are_the_same(hq, hkv, e4m3):
     if e4m3:
         assert torch.equal(caches[0].k_scale, caches[1].k_scale)
         assert torch.equal(caches[0].v_scale, caches[1].v_scale)
+
+
+@pytest.mark.parametrize("hq,hkv,rows", [(24, 1, 1), (17, 1, 1), (8, 2, 8), (32, 4, 8), (33, 1, 5), (48, 2, 8)])
+@pytest.mark.parametrize("ps,window", [(16, 0), (64, 0), (5, 0), (64, 1), (16, 70), (48, 200)])
+def test_attention_of_many_queries(hq, hkv, rows, ps, window):
+    """More than 16 queries of a kv head in E4M3: steps of one and two tiles, split and whole."""
+    for lens in ([0, 1, rows, 63, 64, 65, 127, 128, 129, 191, 250], [1400, 3, 2111, 640, 0, 1]):
+        g = gen(hq + ps + window)
+        c = new_cache(len(lens), -(-max(lens) // ps), ps, hkv, 128, BF, True, fill=float("nan"))
+        kv = fill_cache(c, lens, g)
+        q = randn((len(lens), rows, hq, 128), g, BF, 1.5)
+        a = check_attention(c, q, lens, kv, window=window)
+        assert torch.equal(a, c.attention(q, i32(lens), window=window))
+
+
+@pytest.mark.parametrize("rows,window", [(8, 0), (4, 40), (3, 300)])
+def test_attention_of_many_queries_keeps_odd_values_to_the_rows_that_see_them(rows, window):
+    n, hq = 1000, 24
+    g = gen(7)
+    where = [n - 1, n - 2] if not window else [n - rows - window + 1, n - rows - window + 2]
+    c = new_cache(1, 63, 16, 2, 128, BF, True)
+    fill_cache(c, [n], g)
+    q = randn((1, rows, hq, 128), g)
+    clean = c.attention(q, i32([n]), window=window)
+    k, v = c.read(i32([0, 0]), i32(where))
+    k[0], v[0] = float("nan"), float("inf")
+    v[1, 0, 3:5] = float("nan")
+    c.write(k, v, i32([0, 0]), i32(where))
+    got = c.attention(q, i32([n]), window=window)
+    c.check()
+    for i in range(rows):
+        p = n - rows + i
+        sees = [j <= p and (not window or j > p - window) for j in where]
+        assert torch.equal(got[0, i], clean[0, i]) == (not any(sees)), i
+        if sees[0]:
+            assert torch.isnan(got[0, i]).all()
+        elif sees[1]:
+            assert torch.isnan(got[0, i, :12, 3:5]).all() and torch.isfinite(got[0, i, 12:]).all()
+
+
+def test_attention_of_many_queries_leaves_bad_pages_out():
+    lens, rows = [700, 64, 333], 8
+    g = gen(9)
+    c = new_cache(3, 44, 16, 2, 128, BF, True)
+    kv = fill_cache(c, lens, g)
+    q = randn((3, rows, 16, 128), g)
+    good = c.attention(q, i32(lens))
+    c.check()
+    c.table[0, 10] = -5
+    out = c.attention(q, i32(lens))
+    from mtp_block_draft_gb300 import DmtpError
+    with pytest.raises(DmtpError) as e:
+        c.check()
+    assert e.value.word == 16 and torch.equal(out[1:], good[1:])
+    keep = np.r_[0:160, 176:700]
+    cut = [[x[:, keep] for x in kv[0]]]
+    ref, tol = reference(np64(q[:1]), cut, [684], rows, 0, 128 ** -0.5, False)
+    assert (np.abs(np64(out[:1]) - ref) <= tol * 1.01 + HALF[BF] * np.abs(ref) + 1e-30).all()

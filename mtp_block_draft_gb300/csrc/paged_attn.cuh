@@ -125,7 +125,7 @@ __device__ __forceinline__ Tiles my_tiles(const PagedAttn& p, Deal& d, int threa
     w.end = c < busy ? d.begin(c + 1) : 0;
     w.b = w.unit = w.t = w.n = w.len = w.first = 0;
     if (w.pos < w.end) {
-      int before = 0;  // tiles of the sequences before this round
+      int before = 0;  // tiles of the sequences before these 32
       for (int b0 = 0; b0 < n; b0 += 32) {
         const int t = b0 + lane < n ? seq_tiles(p, seq_len(p, b0 + lane)) * p.units : 0;
         int inc = t;

@@ -26,6 +26,7 @@
 #include <math.h>
 
 #include "paged.cuh"
+#include "sample_keys.h"
 
 namespace {
 
@@ -52,15 +53,6 @@ struct RowsArgs {
 __device__ __forceinline__ float clean(float l) {  // NaN: masked; +infinity: the largest number
   return fminf(fmaxf(l, kMasked), 3.402823466e38f);
 }
-// Unsigned keys in the order of the logits (+-0 alike), to search and split ranges.
-__device__ __forceinline__ uint32_t key_of(float l) {
-  const uint32_t u = __float_as_uint(l + 0.f);
-  return u & 0x80000000u ? ~u : u | 0x80000000u;
-}
-__device__ __forceinline__ float logit_of(uint32_t key) {
-  return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
-}
-
 // floor(f t) of 0 <= f < 1 (up: the next integer if that is not exact): the whole product,
 // 24 by 64 bits, so that a border that f t meets exactly is met here too.
 __device__ __forceinline__ unsigned long long part_of(float f, unsigned long long t, bool up) {
@@ -329,7 +321,7 @@ struct Cluster {
 // one of which it holds); one warp searches 32 places at a time.
 template <typename F>
 __device__ __forceinline__ uint32_t first_key(uint32_t top, F yes) {
-  uint32_t lo = 0x007fffffu, hi = top;  // minus infinity
+  uint32_t lo = kMaskedKey, hi = top;
   const int lane = threadIdx.x & 31;
   while (hi - lo > 1) {
     const uint32_t x = lo + (uint32_t)((unsigned long long)(hi - lo) * (lane + 1) / 33);
@@ -395,7 +387,7 @@ __global__ void __launch_bounds__(THREADS) k_sample_rows(const RowsArgs sa) {
   const float u = __ldg(a.u + row);
   cl.sync();  // every CTA of the cluster runs before one writes another's memory
   const uint32_t top = cl.max(key_of(best));
-  const bool none = top == key_of(kMasked);
+  const bool none = top == kMaskedKey;
   if (none || !(temp > 0.f)) {
     uint32_t id = 0;  // of the largest logit, the lowest: 2^32 - 1 - id is maximal
     const float t = logit_of(top);
@@ -420,7 +412,7 @@ __global__ void __launch_bounds__(THREADS) k_sample_rows(const RowsArgs sa) {
   const float2* own = reinterpret_cast<const float2*>(vals + tid * E);  // this thread's ids, E even
   const bool by_p = top_p < 1.f;
   // the smallest logit that stays, as a key; `ties` of its ids stay, all of them unless `partial`
-  uint32_t cut = 0x00800000u;
+  uint32_t cut = kLowestKey;
   unsigned long long ties = 0;
   bool partial = false;
   bool by_k = false;
@@ -469,7 +461,7 @@ __global__ void __launch_bounds__(THREADS) k_sample_rows(const RowsArgs sa) {
       __syncthreads();
       uint32_t lo = sh.edge[0], hi = sh.edge[1];
       while (want != cnt && lo != hi) {
-        const int shift = max(0, 32 - __clz((int)(hi - lo)) - 11);
+        const int shift = range_shift(lo, hi, 11);
         const float lf = logit_of(lo), hf = logit_of(hi);
         for (int i = 0; i < E / 2; ++i) {
           const float2 x = own[i];
@@ -480,8 +472,7 @@ __global__ void __launch_bounds__(THREADS) k_sample_rows(const RowsArgs sa) {
         int f;
         cl.find_count(want, f, before, cnt);
         want -= before;
-        hi -= (uint32_t)f << shift;
-        lo = hi - lo < (1u << shift) ? lo : hi - ((1u << shift) - 1);
+        take_bin(lo, hi, shift, (uint32_t)f);
       }
       cut = lo;
       partial = want != cnt;
@@ -514,7 +505,7 @@ __global__ void __launch_bounds__(THREADS) k_sample_rows(const RowsArgs sa) {
     uint32_t lo = max(sh.edge[0], least_key), hi = max(sh.edge[1], lo);
     // every weight once: all, above the neighbourhood, and inside it by finer bins
     unsigned long long sum = 0, above = 0;
-    int shift = max(0, 32 - __clz((int)(hi - lo)) - 9);
+    int shift = range_shift(lo, hi, 9);
     from = hi;
     listed = 0;
     {
@@ -597,8 +588,7 @@ __global__ void __launch_bounds__(THREADS) k_sample_rows(const RowsArgs sa) {
       } else {
         const int f = (int)sh.found[0];
         above = sh.found[1];
-        hi -= (uint32_t)f << shift;
-        lo = hi - lo < (1u << shift) ? lo : hi - ((1u << shift) - 1);
+        take_bin(lo, hi, shift, (uint32_t)f);
         const unsigned long long c = sh.found[2];
         if (c == 1 || lo == hi) {
           const unsigned long long wl = c == 1 ? 0ull : sh.found[3] / c;
@@ -609,7 +599,7 @@ __global__ void __launch_bounds__(THREADS) k_sample_rows(const RowsArgs sa) {
           break;
         }
       }
-      shift = max(0, 32 - __clz((int)(hi - lo)) - 9);
+      shift = range_shift(lo, hi, 9);
       __syncthreads();  // found has been read, the histogram cleared
       const float lf = logit_of(lo), hf = logit_of(hi);
       if (!moved && listed <= Sh::kSlots) {
@@ -840,7 +830,7 @@ __global__ void __launch_bounds__(kStream, 2) k_sample_stream(const RowsArgs sa)
       lasts += sh.slot[p][r][1];
     }
     nvalid = lasts;  // and the bins' counts, below
-    if (!binned || top == key_of(kMasked)) break;
+    if (!binned || top == kMaskedKey) break;
     if (use && bin_of(logit_of(top)) >= 0) break;
     // the first logits were far below the largest, or masked: hang the bins on that one
     from_l = logit_of(top);
@@ -849,7 +839,7 @@ __global__ void __launch_bounds__(kStream, 2) k_sample_stream(const RowsArgs sa)
     for (int i = tid; i < kBins; i += kStream) sh.hist[i] = 0;
   }
   W.top = logit_of(top);
-  const bool none = top == key_of(kMasked);
+  const bool none = top == kMaskedKey;
   if (none || greedy) {
     uint32_t id = 0;  // of the largest logit, the lowest: 2^32 - 1 - id is maximal
     if (!none)
@@ -873,13 +863,13 @@ __global__ void __launch_bounds__(kStream, 2) k_sample_stream(const RowsArgs sa)
     return;
   }
   // the smallest logit that stays, as a key; `ties` of its ids stay, all of them unless `partial`
-  uint32_t cut = 0x00800000u;
+  uint32_t cut = kLowestKey;
   unsigned long long ties = 0;
   bool partial = false, by_k = false;
   // The smallest key of bins 0..b, top + 1 if none is that high. One warp.
   auto bin_edge = [&](int b) {
     auto in = [&](float x) { return bin_of(x) <= b; };
-    return b >= kBins - 1 ? 0x00800000u : b >= 0 && in(W.top) ? first_key(top, in) : top + 1;
+    return b >= kBins - 1 ? kLowestKey : b >= 0 && in(W.top) ? first_key(top, in) : top + 1;
   };
   // every logit in [lo, hi]
   auto each_in = [&](uint32_t lo, uint32_t hi, auto&& f) {
@@ -922,14 +912,13 @@ __global__ void __launch_bounds__(kStream, 2) k_sample_stream(const RowsArgs sa)
       __syncthreads();
       uint32_t lo = sh.edge[0], hi = sh.edge[1];
       while (want != cnt && lo != hi) {
-        const int shift = max(0, 32 - __clz((int)(hi - lo)) - 11);
+        const int shift = range_shift(lo, hi, 11);
         each_in(lo, hi, [&](float x) { atomicAdd(&sh.hist[hi - key_of(x) >> shift], 1u); });
         cl.sum_hist();
         int f;
         cl.find_count(want, f, before, cnt);
         want -= before;
-        hi -= (uint32_t)f << shift;
-        lo = hi - lo < (1u << shift) ? lo : hi - ((1u << shift) - 1);
+        take_bin(lo, hi, shift, (uint32_t)f);
       }
       cut = lo;
       partial = want != cnt;
@@ -981,7 +970,7 @@ __global__ void __launch_bounds__(kStream, 2) k_sample_stream(const RowsArgs sa)
     uint32_t lo = max(sh.edge[0], least_key), hi = max(sh.edge[1], lo);
     // every weight once: all, above the neighbourhood, and a list of the neighbourhood
     unsigned long long sum = 0, above = 0;
-    int shift = max(0, 32 - __clz((int)(hi - lo)) - 9);
+    int shift = range_shift(lo, hi, 9);
     from = hi;
     listed = 0;
     {
@@ -1060,8 +1049,7 @@ __global__ void __launch_bounds__(kStream, 2) k_sample_stream(const RowsArgs sa)
       } else {
         const int f = (int)sh.found[0];
         above = sh.found[1];
-        hi -= (uint32_t)f << shift;
-        lo = hi - lo < (1u << shift) ? lo : hi - ((1u << shift) - 1);
+        take_bin(lo, hi, shift, (uint32_t)f);
         const unsigned long long n = sh.found[2];
         if (n == 1 || lo == hi) {
           const unsigned long long wl = n == 1 ? 0ull : sh.found[3] / n;
@@ -1072,7 +1060,7 @@ __global__ void __launch_bounds__(kStream, 2) k_sample_stream(const RowsArgs sa)
           break;
         }
       }
-      shift = max(0, 32 - __clz((int)(hi - lo)) - 9);
+      shift = range_shift(lo, hi, 9);
       __syncthreads();  // found has been read
     }
     if (moved) {  // the cut came out elsewhere: count again

@@ -1,0 +1,58 @@
+"""The decode-step operators at the ends of what they document: numbers, sizes and calls where
+one part of a kernel hands over to another. Plain forms and bounds are those of
+test_gpu_decode_ops.py."""
+
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_decode_ops import check_rows, np64, plain_pick, run_sample
+
+pytestmark = pytest.mark.gpu
+
+f32 = lambda x: float(np.float32(x))
+
+
+# ---- sampling -------------------------------------------------------------------------
+
+def near_zero_rows(V, seed):
+    """Logits around zero in the smallest steps of fp32: no two of the numbers are far enough apart
+    to fall into different bins of weight, so that the cut is found by the numbers' bits alone."""
+    r = np.random.RandomState(seed)
+    z = np.zeros((6, V), np.float32)
+    z[0] = -1e-40 * r.randint(0, 4, V)
+    z[0, 0] = 1.9999999
+    z[1] = 1.4e-45 * r.randint(-3, 4, V)
+    z[2] = -1.4e-45 * r.randint(0, 3, V)
+    z[3] = np.where(r.rand(V) < 0.5, -0.0, -1e-38)
+    z[4] = np.where(r.rand(V) < 0.9, 0.0, -3e-39)
+    z[5] = -r.rand(V) * 1e-37
+    return z
+
+
+@pytest.mark.parametrize("V", [7, 100, 3000, 20000])
+@pytest.mark.parametrize("t", [1.0, 1000.0])
+def test_sample_zeros_beside_the_smallest_negative_logits(V, t):
+    z = torch.from_numpy(near_zero_rows(V, V)).cuda()
+    u = [0.1, 0.3, 0.5, 0.7, 0.9, 0.99]
+    for k in sorted({0, 1, V // 7, V // 2, V - 2}):
+        for p in (1.0, 0.37, 0.913):
+            for m in (0.0, 1.0):
+                check_rows(z, u, [t] * 6, [k] * 6, [p] * 6, [m] * 6)
+
+
+def check_copies(z, copies, u, t, k, p, m=0.0):
+    """The rows of z, each `copies` times in one call, against the plain form of each."""
+    n = z.shape[0]
+    ids, kept = run_sample(z.repeat(copies, 1), list(u) * copies, [t] * n * copies, [k] * n * copies,
+                           [p] * n * copies, [m] * n * copies)
+    zz = np64(z)
+    want = [plain_pick(zz[i], f32(u[i]), f32(t), k, f32(p), f32(m)) for i in range(n)]
+    assert [(int(a), int(b)) for a, b in zip(ids, kept)] == want * copies, (t, k, p, m)
+
+
+def test_sample_zeros_beside_the_smallest_negative_logits_of_many_large_rows():
+    V = 104001
+    z = torch.from_numpy(near_zero_rows(V, 1)).cuda()
+    for k, p in ((0, 0.37), (3, 1.0), (V // 2, 1.0), (V // 2, 0.913), (V - 5, 0.5)):
+        check_copies(z, 22, [0.1, 0.3, 0.5, 0.7, 0.9, 0.99], 1.0, k, p)

@@ -135,7 +135,7 @@ struct Shared {
   unsigned long long found[4];
   static constexpr int kSlots = 4096 / THREADS;
   uint8_t list[kSlots][THREADS];      // where a thread's ids in the neighbourhood are
-  uint32_t edge[3];
+  uint32_t edge[5];  // keys: top-k's bin, min_p's cut, top-p's neighbourhood
   int bins[2];
   unsigned long long table[256];
 };
@@ -496,13 +496,13 @@ __global__ void __launch_bounds__(THREADS) k_sample_rows(const RowsArgs sa) {
       if (wid < 2) {
         const int b = wid ? sh.bins[0] - 1 : sh.bins[1];
         const uint32_t f = b < 0 ? top + 1 : first_key(top, [&](float x) { return W.bin(x) <= b; });
-        if (lane == 0) sh.edge[wid] = wid ? f - 1 : f;
+        if (lane == 0) sh.edge[3 + wid] = wid ? f - 1 : f;  // (others may still read top-k's)
       }
       __syncthreads();
     }
     if (min_p > 0.f) min_key = sh.edge[2];
     const uint32_t least_key = partial ? cut + 1 : cut;  // below it, only the cut's own ties
-    uint32_t lo = max(sh.edge[0], least_key), hi = max(sh.edge[1], lo);
+    uint32_t lo = max(sh.edge[3], least_key), hi = max(sh.edge[4], lo);
     // every weight once: all, above the neighbourhood, and inside it by finer bins
     unsigned long long sum = 0, above = 0;
     int shift = range_shift(lo, hi, 9);
@@ -731,7 +731,7 @@ struct StreamShared {
   uint32_t seg_n[DMTP_OPS_MAX_SAMPLE_VOCAB / 2 / kSegment];          // ties of the cut in it
   uint8_t list[kSlots][kStream];  // a thread's logits in the neighbourhood: where, and which
   float value[kSlots][kStream];
-  uint32_t edge[3];
+  uint32_t edge[5];  // keys: top-k's bin, min_p's cut, top-p's neighbourhood
   int bins[2];
 };
 
@@ -930,7 +930,7 @@ __global__ void __launch_bounds__(kStream, 2) k_sample_stream(const RowsArgs sa)
   // the neighbourhood's ends and min_p as keys
   if (wid < 2 && by_p) {
     const uint32_t f = bin_edge(wid ? sh.bins[0] - 1 : sh.bins[1]);
-    if (lane == 0) sh.edge[wid] = wid ? f - 1 : f;
+    if (lane == 0) sh.edge[3 + wid] = wid ? f - 1 : f;  // (others may still read top-k's)
   }
   if (wid == 2 && min_p > 0.f) {
     const unsigned long long least = min_p < 1.f ? part_of(min_p, 1ull << kShift, true) : 1ull << kShift;
@@ -967,7 +967,7 @@ __global__ void __launch_bounds__(kStream, 2) k_sample_stream(const RowsArgs sa)
   uint32_t cnt = 0, from = 0xffffffffu;  // kept logits, so far those above `from`
   int listed = -1;                       // >= 0: the others are in this thread's list, so many
   if (by_p) {
-    uint32_t lo = max(sh.edge[0], least_key), hi = max(sh.edge[1], lo);
+    uint32_t lo = max(sh.edge[3], least_key), hi = max(sh.edge[4], lo);
     // every weight once: all, above the neighbourhood, and a list of the neighbourhood
     unsigned long long sum = 0, above = 0;
     int shift = range_shift(lo, hi, 9);

@@ -56,3 +56,24 @@ def test_sample_zeros_beside_the_smallest_negative_logits_of_many_large_rows():
     z = torch.from_numpy(near_zero_rows(V, 1)).cuda()
     for k, p in ((0, 0.37), (3, 1.0), (V // 2, 1.0), (V // 2, 0.913), (V - 5, 0.5)):
         check_copies(z, 22, [0.1, 0.3, 0.5, 0.7, 0.9, 0.99], 1.0, k, p)
+
+
+@pytest.mark.parametrize("V,copies", [(60, 1), (20000, 2), (20000, 33), (104001, 33)])
+def test_sample_top_p_right_after_a_top_k_that_takes_whole_bins(V, copies):
+    """top_k ends at a bin's end, or in a bin of one number's ties, so that nothing has to be split
+    before top_p's search begins; the same call gives the same rows each time."""
+    r = np.random.RandomState(V)
+    z = np.zeros((4, V), np.float32)
+    z[0] = -(np.arange(V) % 20)                 # groups of ties, bins apart
+    z[1] = -(np.arange(V) // (V // 4))
+    z[2] = r.permutation(np.where(np.arange(V) < V // 3, 7.0, -1.0))
+    z[3] = 1e4 * r.randint(0, 3, V)
+    zz, z = z.astype(np.float64), torch.from_numpy(z).cuda()
+    u = [0.15, 0.45, 0.65, 0.85]
+    for t in (1.0, 1e-9):
+        for k in (V // 20, V // 4, V // 3, 2, V // 2):
+            want = [plain_pick(zz[i], f32(u[i]), f32(t), k, f32(0.613), 0.0) for i in range(4)]
+            for _ in range(10):
+                ids, kept = run_sample(z.repeat(copies, 1), u * copies, [t] * 4 * copies, [k] * 4 * copies,
+                                       [0.613] * 4 * copies, None)
+                assert [(int(a), int(b)) for a, b in zip(ids, kept)] == want * copies, (t, k)

@@ -75,7 +75,7 @@ __device__ __forceinline__ unsigned long long part_of(float f, unsigned long lon
 }
 
 constexpr int kShift = 44;  // weight 1 is 2^44: 2^18 of them stay below 2^63
-constexpr int kBins = 2048, kFine = 512;
+constexpr int kBins = 2048, kFine = kBins / 4;  // (a fine bin has four words)
 
 struct Weigh {
   float top, chi, clo, cb;
@@ -129,7 +129,11 @@ struct Weigh {
 template <int THREADS>
 struct Shared {
   static constexpr int kWarps = THREADS / 32;
-  uint32_t hist[kBins], all[kBins];
+  alignas(16) uint32_t hist[kBins];
+  union {  // of the cluster, by sum_hist() or sum_fine()
+    uint32_t all[kBins];
+    unsigned long long fine[kFine][2];  // weight, count
+  };
   unsigned long long slot[2][16][2];  // one pair of each CTA of the cluster, twice
   unsigned long long warp[kWarps][2];
   unsigned long long found[4];
@@ -230,6 +234,29 @@ struct Cluster {
     sync();
     for (int i = threadIdx.x; i < kBins; i += THREADS) s->hist[i] = 0;
   }
+  // The same of histograms filled by add_fine(): every CTA gets the cluster's count and weight of
+  // each fine bin in `fine`.
+  __device__ __forceinline__ void sum_fine() {
+    sync();
+    const int per = kFine / (int)size;
+    for (int i = threadIdx.x; i < per; i += THREADS) {
+      const int at = (int)rank * per + i;
+      uint32_t n = 0;
+      unsigned long long w = 0;
+      for (unsigned r = 0; r < size; ++r) {
+        uint32_t c, x, y, z;
+        asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(c), "=r"(x), "=r"(y), "=r"(z) : "r"(smem_in_rank(smem_u32(&s->hist[4 * at]), r)) : "memory");
+        n += c;
+        w += (unsigned long long)x + ((unsigned long long)y << 15) + ((unsigned long long)z << 30);
+      }
+      for (unsigned r = 0; r < size; ++r)
+        asm volatile("st.shared::cluster.v2.u64 [%0], {%1, %2};" ::"r"(smem_in_rank(smem_u32(&s->fine[at][0]), r)),
+                     "l"(w), "l"((unsigned long long)n) : "memory");
+    }
+    sync();
+    for (int i = threadIdx.x; i < kBins; i += THREADS) s->hist[i] = 0;
+  }
   // Exclusive sum over the CTA's threads, and the total; all threads call it.
   __device__ __forceinline__ unsigned long long scan(unsigned long long v, unsigned long long& total) {
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
@@ -307,7 +334,7 @@ struct Cluster {
     __syncthreads();
   }
   // 2^-44 weights as three 15-bit parts and a count in bins of the histogram: 32-bit sums hold
-  // the 2^16 logits a CTA has at most.
+  // the 2^17 logits that a CTA has at most (of the cluster's 2^18 they would not).
   __device__ __forceinline__ void add_fine(int i, unsigned long long w) {
     uint32_t* h = &s->hist[4 * i];
     atomicAdd(h, 1u);
@@ -551,21 +578,20 @@ __global__ void __launch_bounds__(THREADS) k_sample_rows(const RowsArgs sa) {
     // the first logit from above at which the running weight reaches the goal
     bool moved = false;  // out of the neighbourhood
     while (true) {
-      cl.sum_hist();
+      cl.sum_fine();
       constexpr int FE = kFine / THREADS > 1 ? kFine / THREADS : 1;
       unsigned long long m[FE], mine_m = 0, total;
 #pragma unroll
       for (int e = 0; e < FE; ++e) {
         const int i = tid * FE + e;
-        const uint32_t* c = sh.all + 4 * i;
-        m[e] = i < kFine ? (unsigned long long)c[1] + ((unsigned long long)c[2] << 15) + ((unsigned long long)c[3] << 30) : 0ull;
+        m[e] = i < kFine ? sh.fine[i][0] : 0ull;
         mine_m += m[e];
       }
       unsigned long long at = above + cl.scan(mine_m, total);
 #pragma unroll
       for (int e = 0; e < FE; ++e) {
         if (at < goal && goal <= at + m[e])
-          sh.found[0] = tid * FE + e, sh.found[1] = at, sh.found[2] = sh.all[4 * (tid * FE + e)], sh.found[3] = m[e];
+          sh.found[0] = tid * FE + e, sh.found[1] = at, sh.found[2] = sh.fine[tid * FE + e][1], sh.found[3] = m[e];
         at += m[e];
       }
       __syncthreads();
@@ -722,7 +748,11 @@ constexpr int kStream = 512, kSegment = 1024, kAhead = 256;
 
 struct StreamShared {
   static constexpr int kWarps = kStream / 32, kSlots = 16;
-  uint32_t hist[kBins], all[kBins];
+  alignas(16) uint32_t hist[kBins];
+  union {  // of the cluster, by sum_hist() or sum_fine()
+    uint32_t all[kBins];
+    unsigned long long fine[kFine][2];  // weight, count
+  };
   unsigned long long slot[2][16][2];
   unsigned long long warp[kWarps][2];
   unsigned long long found[4];
@@ -1023,12 +1053,12 @@ __global__ void __launch_bounds__(kStream, 2) k_sample_stream(const RowsArgs sa)
         goal = part_of(fmaxf(top_p, 0.f), sum, true);
         goal = goal ? goal : 1ull;
       }
-      cl.sum_hist();
-      const uint32_t* c = sh.all + 4 * tid;
-      const unsigned long long m = (unsigned long long)c[1] + ((unsigned long long)c[2] << 15) + ((unsigned long long)c[3] << 30);
+      cl.sum_fine();
+      static_assert(kFine == kStream, "a fine bin a thread");
+      const unsigned long long m = sh.fine[tid][0];
       unsigned long long total;
       const unsigned long long at = above + cl.scan(m, total);
-      if (at < goal && goal <= at + m) sh.found[0] = tid, sh.found[1] = at, sh.found[2] = c[0], sh.found[3] = m;
+      if (at < goal && goal <= at + m) sh.found[0] = tid, sh.found[1] = at, sh.found[2] = sh.fine[tid][1], sh.found[3] = m;
       __syncthreads();
       if (above >= goal) {  // the goal lies above this range
         lo = hi + 1;

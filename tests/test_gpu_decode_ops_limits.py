@@ -77,3 +77,26 @@ def test_sample_top_p_right_after_a_top_k_that_takes_whole_bins(V, copies):
                 ids, kept = run_sample(z.repeat(copies, 1), u * copies, [t] * 4 * copies, [k] * 4 * copies,
                                        [0.613] * 4 * copies, None)
                 assert [(int(a), int(b)) for a, b in zip(ids, kept)] == want * copies, (t, k)
+
+
+def tied_rows(V):
+    """Rows of which nearly every logit has the same weight, with many bits set in it."""
+    z = np.zeros((5, V), np.float32)
+    z[1, 5:] = -0.25
+    z[2, 1:] = -2.5
+    z[3, V // 3:] = -0.7
+    z[4] = np.where(np.arange(V) % 1000 == 7, 3.0, 2.9375)
+    return z
+
+
+@pytest.mark.parametrize("V", [131073, 151936, 200003, 262144])
+@pytest.mark.parametrize("copies", [1, 26])
+def test_sample_large_vocabularies_of_ties(V, copies):
+    """More than 2^17 logits of one weight: the weights of a bin add up past 32 bits in each part."""
+    z = torch.from_numpy(tied_rows(V)).cuda()
+    u = [0.1, 0.35, 0.6, 0.85, 0.999]
+    for k, p, m in ((0, 0.9, 0.0), (0, 0.31, 0.5), (V - 3, 0.77, 0.0)):
+        check_copies(z, copies, u, 1.0, k, p, m)
+    if copies == 1:  # the same logits in bf16
+        zb = z.to(torch.bfloat16)
+        check_copies(zb, 1, u, 0.7, 0, 0.9)

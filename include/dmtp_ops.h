@@ -113,9 +113,12 @@ int dmtp_paged_read(const dmtp_paged_kv* c, const int32_t* seq, const int32_t* p
  * positions are left out. A NaN or an infinity reaches the rows that see its position (a value
  * whose weight rounds to 0 may not) and no other. |scale| <= 1e30.
  * Scores, softmax statistics and sums are fp32; products of bf16 rows run on the tensor
- * cores with the weights as bf16 pairs (16 bits), of E4M3 rows with fp16 weights (v_scale up
- * to 2^40; values of rows scaled by less than 2^-60 count to 2^-76). Results do not depend on
- * timing: the same call gives the same bits. */
+ * cores with the weights as bf16 pairs (16 bits), of E4M3 rows with fp16 weights (11 bits): a
+ * weight times its v_scale is rounded against the largest such product of the query so far, in
+ * which value rows of zeros with a v_scale of at least 1 (dmtp_paged_write gives them 1) do not
+ * count (v_scale up to 2^40; values of rows scaled by less than 2^-60 count to 2^-76). The sum of
+ * weights times values is fp32 before it is divided by the sum of weights: it must stay below
+ * 2^120 or so. Results do not depend on timing: the same call gives the same bits. */
 typedef struct {
   const void* q;
   void* out;

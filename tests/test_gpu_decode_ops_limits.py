@@ -6,7 +6,8 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_decode_ops import check_rows, np64, plain_pick, run_sample
+from test_gpu_decode_ops import (BF, check_attention, check_rows, gen, i32, new_cache, np64, plain_pick, randn,
+                                 run_sample, stored)
 
 pytestmark = pytest.mark.gpu
 
@@ -100,3 +101,34 @@ def test_sample_large_vocabularies_of_ties(V, copies):
     if copies == 1:  # the same logits in bf16
         zb = z.to(torch.bfloat16)
         check_copies(zb, 1, u, 0.7, 0, 0.9)
+
+
+# ---- attention ------------------------------------------------------------------------
+
+@pytest.mark.parametrize("hd,hq,rows", [(64, 2, 1), (128, 2, 1), (128, 16, 1), (64, 8, 4), (128, 16, 8)])
+@pytest.mark.parametrize("size", [1.0, 1e-3, 1e-6, 1e-9])
+@pytest.mark.parametrize("zeros", ["first", "one", "last", "half", "sink"])
+def test_attention_of_small_values_beside_rows_of_zeros(hd, hq, rows, size, zeros):
+    """E4M3 value rows of zeros have scale 1 whatever the others' size. They weigh in the sum of
+    weights alone: what the other rows add is as exact as without them."""
+    lens = [40, 333, 1500]
+    c = new_cache(len(lens), 24, 64, 2, hd, BF, True, fill=1.0)
+    g = gen(hd + rows)
+    n = sum(lens)
+    seq = np.concatenate([np.full(x, b) for b, x in enumerate(lens)])
+    pos = np.concatenate([np.arange(x) for x in lens])
+    k, v = randn((n, 2, hd), g), (randn((n, 2, hd), g, torch.float32) * size).to(BF)
+    q = randn((len(lens), rows, hq, hd), g, BF, 1.5)
+    if zeros == "half":
+        v[torch.rand((n, 2), device="cuda", generator=g) < 0.5] = 0
+    else:
+        at = {"first": 0, "one": 17, "last": -rows, "sink": 3}[zeros]
+        at = [int(np.flatnonzero(seq == b)[at]) for b in range(len(lens))]
+        v[at] = 0
+        if zeros == "sink":  # a score some 15 above the others', for every query
+            q[..., 0], k[:, :, 0] = 8.0, 0.0
+            k[at] = 0
+            k[at, :, 0] = 1.9 * hd ** 0.5
+    c.write(k, v, i32(seq), i32(pos))
+    assert (np64(c.v_scale) == 1).any() and (size > 1e-3 or float(c.v_scale.min()) < 2.0 ** -15)
+    check_attention(c, q, lens, stored(c, lens))

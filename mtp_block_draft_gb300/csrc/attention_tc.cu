@@ -37,6 +37,7 @@
 // cache; the drafter sees its anchor-relative window and the whole 8-slot block.
 // Every mbarrier wait is bounded; on a timeout the error word is set, in-flight copies
 // and MMAs are drained and TMEM is freed before the CTA returns.
+#include "attn_tiles.h"
 #include "common.cuh"
 #include "ops.h"
 
@@ -243,10 +244,10 @@ __global__ void __launch_bounds__(320, 1)
   };
   uint64_t* kv_full = bars;             // [NST]
   uint64_t* kv_empty = bars + NST;      // [NST]
-  uint64_t* s_full = bars + 2 * NST;    // [2] (S is double-buffered in TMEM)
-  uint64_t* q_full = s_full + 2;        // the 256 softmax threads wrote a piece's queries
-  uint64_t* p_full = q_full + 1;        // the 256 softmax threads wrote this tile's P
-  uint64_t* o_full = p_full + 1;        // one commit per tile's P V
+  uint64_t* s_full = bars + 2 * NST;    // [2] a tile's scores (S is double-buffered in TMEM)
+  uint64_t* p_full = s_full + kTileBars;  // [2] the 256 softmax threads wrote a tile's P
+  uint64_t* q_full = p_full + kTileBars;  // the 256 softmax threads wrote a piece's queries
+  uint64_t* o_full = q_full + 1;        // one commit per tile's P V
   uint64_t* pfin = o_full + 1;          // a piece's last P V completed
   uint64_t* o_drained = pfin + 1;       // the 256 softmax threads read a piece's O
   uint64_t* fin = o_drained + 1;
@@ -258,10 +259,11 @@ __global__ void __launch_bounds__(320, 1)
       mbar_init(smem_u32(&kv_full[i]), 1);
       mbar_init(smem_u32(&kv_empty[i]), 1);
     }
-    mbar_init(smem_u32(&s_full[0]), 1);
-    mbar_init(smem_u32(&s_full[1]), 1);
+    for (int i = 0; i < kTileBars; ++i) {
+      mbar_init(smem_u32(&s_full[i]), 1);
+      mbar_init(smem_u32(&p_full[i]), 256);
+    }
     mbar_init(smem_u32(q_full), 256);
-    mbar_init(smem_u32(p_full), 256);
     mbar_init(smem_u32(o_full), 1);
     mbar_init(smem_u32(pfin), 1);
     mbar_init(smem_u32(o_drained), 256);
@@ -281,11 +283,9 @@ __global__ void __launch_bounds__(320, 1)
   // Up to here the CTA read only the sequences' base positions, which the launch before
   // this one (the RoPE / KV-row writer) does not write and lets this launch begin only
   // after its own wait; the queries and the K/V tiles come after the wait. The merge may begin
-  // only at the CTA's end, below: with the trigger here as well as this kernel's own early
-  // start, the softmax warps of a CTA stalled now and then until the bounded waits gave up (2 s,
-  // the wait bit set; about every second run of some 2000 rounds). Without the early trigger, or
-  // without the early start, 8 and 7 of such runs were clean; it costs 0.4% of a B32 round,
-  // the other 2%.
+  // only at the CTA's end, below: begun here, its CTAs make the issuing thread late now and then,
+  // which a single barrier for the weights of all tiles did not bear (attn_tiles.h); it costs 0.4%
+  // of a B32 round.
   pdl_wait();
   const uint32_t tmem = *tmem_slot;
   const uint32_t tO = tmem + 2 * TK;
@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(320, 1)
             umma_bf16_ta(tmem + (xg & 1) * TK, tQ + kb * 32 + kk * 8, dk + 2 * kk, id_qk,
                          (kb | kk) ? 1u : 0u);
         }
-        umma_commit(smem_u32(&s_full[xg & 1]));
+        umma_commit(smem_u32(&s_full[tile_bar(xg)]));
         return true;
       };
       int gt = 0, p = 0;
@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(320, 1)
               break;
             }
           }
-          if (!mbar_wait(smem_u32(p_full), xg & 1, err)) {
+          if (!mbar_wait(smem_u32(&p_full[tile_bar(xg)]), tile_parity(xg), err)) {
             ok = false;
             break;
           }
@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(320, 1)
       for (int t = 0; t < nt; ++t) {
         const int xg = gt + t;
         if (ok) {
-          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&s_full[xg & 1]), (xg >> 1) & 1, err));
+          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&s_full[tile_bar(xg)]), tile_parity(xg), err));
           tc_fence_after();
         }
         const int kt = (kt0 + t) * TK;
@@ -567,7 +567,7 @@ __global__ void __launch_bounds__(320, 1)
           fence_proxy_async();
           tc_fence_before();
         }
-        mbar_arrive(smem_u32(p_full));
+        mbar_arrive(smem_u32(&p_full[tile_bar(xg)]));
       }
       // ---- end of the piece ----
       // the next piece's queries into the other Q buffer first, so that its first S is

@@ -108,6 +108,27 @@ __global__ void __launch_bounds__(THREADS, ctas_of<TX, TY, NV, THREADS>()) k_add
       for (int o = THREADS / 64; o > 0; o >>= 1)
         ss = add(ss, F2{__shfl_xor_sync(0xffffffffu, ss.hi, o), __shfl_xor_sync(0xffffffffu, ss.lo, o)});
     }
+    if (!(ss.hi <= 3.402823466e38f)) {
+      // an infinity or NaN (or squares past fp32): what the sum carries along, infinity less infinity,
+      // made it a NaN if anything came after. The plain sum tells the two apart: next to an
+      // infinity finite values become 0, next to a NaN all are NaN.
+      float plain = 0.f;
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) plain = fmaf(v[k][e], v[k][e], plain);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) plain += __shfl_xor_sync(0xffffffffu, plain, o);
+      if (THREADS > 32) {
+        __syncthreads();
+        if (lane == 0) red2[turn][wid].x = plain;
+        __syncthreads();
+        plain = 0.f;
+#pragma unroll
+        for (int w = 0; w < THREADS / 32; ++w) plain += red2[turn][w].x;
+      }
+      ss = F2{plain, 0.f};
+    }
     // mean + eps as a pair: S / d by the reciprocal, then the quotient's remainder
     const float n = (float)a.d, q0 = ss.hi * rn;
     F2 ms = two_sum(q0, a.eps);
@@ -117,7 +138,7 @@ __global__ void __launch_bounds__(THREADS, ctas_of<TX, TY, NV, THREADS>()) k_add
     const float rr = r0 * r0, rl = fmaf(r0, r0, -rr);
     const float p = ms.hi * rr;
     const float res = (1.f - p) - (fmaf(ms.hi, rr, -p) + ms.hi * rl + ms.lo * rr);
-    // a sum that overflowed, or no non-zero element and eps 0: the plain value
+    // an infinite sum, or no non-zero element and eps 0: the plain value
     const float r = fabsf(res) < 0.25f ? fmaf(0.5f * r0, res, r0) : rsqrtf(ss.hi / n + a.eps);
     const f32x2 r2 = pack(r, r);
     uint32_t top = 0;  // largest magnitude, as bits: an infinity or NaN is above every number

@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_decode_ops import (BF, check_attention, check_rows, gen, i32, new_cache, np64, plain_pick, randn,
+from test_gpu_decode_ops import (BF, F8, FP, check_attention, check_rows, gen, i32, new_cache, np64, plain_pick, randn,
                                  run_sample, stored)
 
 pytestmark = pytest.mark.gpu
@@ -132,3 +132,49 @@ def test_attention_of_small_values_beside_rows_of_zeros(hd, hq, rows, size, zero
     c.write(k, v, i32(seq), i32(pos))
     assert (np64(c.v_scale) == 1).any() and (size > 1e-3 or float(c.v_scale.min()) < 2.0 ** -15)
     check_attention(c, q, lens, stored(c, lens))
+
+
+# ---- norm -----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("rows", [40, 200])
+@pytest.mark.parametrize("d", [64, 520, 2048, 4104, 8200])
+@pytest.mark.parametrize("xt,yt", [(FP, None), (BF, BF), (FP, BF)])
+def test_norm_of_rows_with_infinities_and_nan(rows, d, xt, yt):
+    """An infinity makes the row's mean infinite: finite values become 0 and it itself NaN, wherever it
+    stands; a NaN (or infinities that cancel in x + y) makes all of the row NaN."""
+    from mtp_block_draft_gb300 import add_rmsnorm_e4m3
+    r = np.random.RandomState(rows + d)
+    x = randn((rows, d), gen(d), xt)
+    y = None if yt is None else randn((rows, d), gen(d + 1), yt)
+    odd = torch.zeros((rows, d), dtype=torch.bool)
+    nan = torch.zeros(rows, dtype=torch.bool)
+    for i in range(rows):
+        at = i * 8 // rows + 8 * r.randint(0, d // 8) if i % 4 else r.randint(0, d)  # each place of eight
+        if i % 5 == 4:
+            continue                           # an ordinary row
+        odd[i, at] = True
+        into = y if y is not None and i % 2 else x
+        into[i, at] = float("inf") if i % 3 else -float("inf")
+        if i % 5 == 3:
+            nan[i] = True
+            if y is not None and i % 2 == 0:
+                y[i, at] = -x[i, at]           # infinity less infinity
+            else:
+                x[i, (at + 11) % d] = float("nan")
+        elif i % 5 == 2:                       # several of them
+            odd[i, ::7] = True
+            x[i, ::7] = float("inf")
+            if y is not None:
+                y[i, ::7] = 1.0
+    gain = torch.rand(d, device="cuda", generator=gen(2)) + 0.5
+    xo, q, s = add_rmsnorm_e4m3(x, y, gain, 1e-6)
+    v, s = q.float().cpu(), s.cpu()
+    plain = torch.arange(rows) % 5 == 4
+    assert torch.isnan(v[nan]).all()
+    rest = ~nan & ~plain
+    assert (torch.isnan(v[rest]) == odd[rest]).all()
+    assert (v[rest][~odd[rest]] == 0).all() and (s[rest] == 1).all()
+    assert torch.isfinite(v[plain]).all() and bool((v[plain] != 0).any())
+    one = [add_rmsnorm_e4m3(x[i:i + 1], None if y is None else y[i:i + 1], gain, 1e-6)[1] for i in range(4, rows, 35)]
+    for i, t in zip(range(4, rows, 35), one):  # a row is what it is alone
+        assert torch.equal(t.view(torch.uint8), q[i:i + 1].view(torch.uint8))

@@ -68,9 +68,10 @@ def _pack(s, *args) -> bytes:
         _bad(str(e))
 
 
+# (What is no tensor at all fails an attribute below: the checks cost a call nothing then.)
 def _dtype(c, t) -> int:
     """dtype code of a float tensor: 0 fp32, 1 bf16."""
-    d = t.dtype
+    d = getattr(t, "dtype", type(t))
     if d is c.bf16:
         return 1
     if d is not c.fp32:
@@ -80,10 +81,24 @@ def _dtype(c, t) -> int:
 
 def _vector(t, dtype, n: int, dev: int, what: str) -> int:
     """Address of a dense vector of n elements."""
-    if t.dtype is not dtype or t.shape != (n,) or t.get_device() != dev or (
-            n > 1 and t.stride() != (1,)):
-        _bad(f"{what}: a dense {dtype} tensor of {n} on the same device is wanted")
-    return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.shape == (n,) and t.get_device() == dev and (
+                n <= 1 or t.stride() == (1,)):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _bad(f"{what}: a dense {dtype} tensor of {n} on the same device is wanted")
+
+
+def _shape(t, dims: int, what: str):
+    """Shape of a tensor of so many dimensions."""
+    try:
+        t.data_ptr
+        if len(t.shape) == dims:
+            return t.shape
+    except AttributeError:
+        pass
+    _bad(what)
 
 
 def _run(c, f, dev: int, what: str, *args):
@@ -112,12 +127,15 @@ class DmtpPagedCache:
     def __init__(self, k, v, table, k_scale=None, v_scale=None, dtype=None):
         c = _c()
         torch = c.torch
-        e8 = k.dtype is c.f8
 
         def need(ok, what):
             if not ok:
                 _bad(what)
 
+        need(all(isinstance(t, torch.Tensor) for t in (k, v, table)) and
+             all(t is None or isinstance(t, torch.Tensor) for t in (k_scale, v_scale)),
+             "k, v, table and scales are tensors")
+        e8 = k.dtype is c.f8
         need(k.dim() == 4 and v.shape == k.shape and v.dtype is k.dtype and
              v.stride() == k.stride(), "k and v: the same 4-d shape, strides and dtype")
         n, h, ps, hd = k.shape
@@ -164,6 +182,8 @@ class DmtpPagedCache:
     def alloc(cls, n_pages, page_size, n_kv_heads, head_dim, table, dtype=None, e4m3=False):
         """A cache of its own zeroed pages on the table's device."""
         torch = _c().torch
+        if not isinstance(table, torch.Tensor):
+            _bad("table: int32 [n_seqs, max_blocks]")
         dtype = torch.bfloat16 if dtype is None else dtype
         shape = (n_pages, n_kv_heads, page_size, head_dim)
         kw = {"device": table.device}
@@ -177,11 +197,14 @@ class DmtpPagedCache:
 
     def _rows(self, t, n, heads, what):
         """Row and head strides of t [n, heads, head_dim]."""
-        if t.dtype is self.dtype and t.shape == (n, heads, self.head_dim) and \
-                t.get_device() == self._dev:
-            s0, s1, s2 = t.stride()
-            if s2 == 1:
-                return (s0 if n > 1 else heads * self.head_dim), (s1 if heads > 1 else self.head_dim)
+        try:
+            if t.dtype is self.dtype and t.shape == (n, heads, self.head_dim) and \
+                    t.get_device() == self._dev:
+                s0, s1, s2 = t.stride()
+                if s2 == 1:
+                    return (s0 if n > 1 else heads * self.head_dim), (s1 if heads > 1 else self.head_dim)
+        except AttributeError:
+            pass
         _bad(f"{what}: [{n}, {heads}, {self.head_dim}], head_dim dense, of the cache's dtype and device")
 
     def write(self, k, v, seq, pos, q=None, q_out=None, rope_theta: float = 0.0):
@@ -189,14 +212,12 @@ class DmtpPagedCache:
         sequences seq (int32 [n]; seq < 0: skipped), rotated first if rope_theta > 0. With q
         [n, n_heads, head_dim] returns the rotated queries (q_out, or a new tensor)."""
         c, dev = _c(), self._dev
-        n, h = len(seq), self.n_kv_heads
+        n, h = _shape(seq, 1, "seq: int32 [n]")[0], self.n_kv_heads
         kr, kh = self._rows(k, n, h, "k")
         vr, vh = self._rows(v, n, h, "v")
         qp = qop = qr = qh = qor = qoh = heads = 0
         if q is not None:
-            if q.dim() != 3:
-                _bad("q: [n, n_heads, head_dim]")
-            heads = q.shape[1]
+            heads = _shape(q, 3, "q: [n, n_heads, head_dim]")[1]
             if q_out is None:
                 q_out = c.torch.empty(q.shape, dtype=q.dtype, device=q.device)
             qr, qh = self._rows(q, n, heads, "q")
@@ -212,14 +233,14 @@ class DmtpPagedCache:
         """dmtp_paged_read: positions pos of sequences seq (int32 [n]) as dense rows
         [n, n_kv_heads, head_dim]; returns (k, v)."""
         c, dev = _c(), self._dev
-        n = seq.shape[0]
+        n = _shape(seq, 1, "seq: int32 [n]")[0]
         shape = (n, self.n_kv_heads, self.head_dim)
         if k_out is None:
             k_out = c.torch.empty(shape, dtype=self.dtype, device=self.device)
         if v_out is None:
             v_out = c.torch.empty(shape, dtype=self.dtype, device=self.device)
         for t in (k_out, v_out):
-            if t.shape != shape or t.dtype is not self.dtype or not t.is_contiguous() or \
+            if _shape(t, 3, "k_out, v_out: [n, n_kv_heads, head_dim]") != shape or t.dtype is not self.dtype or not t.is_contiguous() or \
                     t.get_device() != dev:
                 _bad(f"k_out, v_out: dense {shape} of the cache's dtype and device")
         _run(c, c.paged_read, dev, "dmtp_paged_read", self._c,
@@ -234,16 +255,14 @@ class DmtpPagedCache:
         attention_workspace() bytes that no overlapping call uses; None: taken from PyTorch's
         allocator for this call."""
         c, dev = _c(), self._dev
-        shape = q.shape
-        if len(shape) != 4:
-            _bad("q: [n_seqs, rows, n_heads, head_dim]")
+        shape = _shape(q, 4, "q: [n_seqs, rows, n_heads, head_dim]")
         B, rows, heads, hd = shape
         if out is None:
             out = c.torch.empty(shape, dtype=q.dtype, device=q.device)
         if B != self.n_seqs or hd != self.head_dim or q.dtype is not self.dtype or \
                 q.get_device() != dev:
             _bad(f"q: [{self.n_seqs}, rows, n_heads, {self.head_dim}] of the cache's dtype and device")
-        if out.shape != shape or out.dtype is not self.dtype or out.get_device() != dev:
+        if _shape(out, 4, "out: the shape of q") != shape or out.dtype is not self.dtype or out.get_device() != dev:
             _bad("out: the shape, dtype and device of q")
         qb, qr, qh, q1 = q.stride()
         ob, orow, oh, o1 = out.stride()
@@ -262,6 +281,7 @@ class DmtpPagedCache:
         if n is None:
             n = self._ws_bytes[rows, heads] = self.attention_workspace(rows, heads)
         if workspace is not None:
+            _shape(workspace, 1, "workspace: a dense uint8 tensor")
             if workspace.dtype is not c.torch.uint8 or workspace.get_device() != dev or \
                     not workspace.is_contiguous():
                 _bad("workspace: a dense uint8 tensor on the cache's device")
@@ -292,10 +312,13 @@ class DmtpPagedCache:
 
 def _matrix(t, shape, dtype, dev: int, what: str) -> int:
     """Row pitch of a matrix with dense rows."""
-    if t.shape == shape and t.dtype is dtype and t.get_device() == dev:
-        s0, s1 = t.stride()
-        if s1 == 1 or shape[1] == 1:
-            return s0 if shape[0] > 1 else shape[1]
+    try:
+        if t.shape == shape and t.dtype is dtype and t.get_device() == dev:
+            s0, s1 = t.stride()
+            if s1 == 1 or shape[1] == 1:
+                return s0 if shape[0] > 1 else shape[1]
+    except AttributeError:
+        pass
     _bad(f"{what}: {dtype} {tuple(shape)} with dense rows on the same device")
 
 
@@ -303,11 +326,8 @@ def add_rmsnorm_e4m3(x, y, gain, eps: float = 1e-6, x_out=None, q=None, scale=No
     """dmtp_add_rmsnorm_e4m3: x_out = x + y, and E4M3 rows of RMSNorm(x + y) * gain. x, y
     [rows, d] bf16 or fp32 (y None: no addition); x_out may be x (None: a new tensor, or x
     where y is None). Returns (x_out, q float8_e4m3fn [rows, d], scale fp32 [rows])."""
-    c, dev = _c(), x.get_device()
-    shape = x.shape
-    if len(shape) != 2:
-        _bad("x: [rows, d]")
-    rows, d = shape
+    c, shape = _c(), _shape(x, 2, "x: [rows, d]")
+    dev, (rows, d) = x.get_device(), shape
     x_dt, y_dt, g_dt = _dtype(c, x), 0, _dtype(c, gain)
     xr = _matrix(x, shape, x.dtype, dev, "x")
     yp = yr = xop = xor = 0
@@ -336,11 +356,8 @@ def sample_rows(logits, u, temperature=None, top_k=None, top_p=None, min_p=None,
     with the uniform numbers u (fp32 [rows]) under temperature, top_k (int32), top_p and
     min_p (fp32 [rows] each, None: off). Returns ids (int32 [rows]; -1 where nothing may be
     chosen); kept (int32 [rows], optional) receives how many tokens passed the filters."""
-    c, dev = _c(), logits.get_device()
-    shape = logits.shape
-    if len(shape) != 2:
-        _bad("logits: [rows, vocab]")
-    rows, V = shape
+    c, shape = _c(), _shape(logits, 2, "logits: [rows, vocab]")
+    dev, (rows, V) = logits.get_device(), shape
     dt = _dtype(c, logits)
     ld = _matrix(logits, shape, logits.dtype, dev, "logits")
     if ids is None:

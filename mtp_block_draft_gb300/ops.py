@@ -114,12 +114,22 @@ def _run(c, f, dev: int, what: str, *args):
         raise DmtpError(r, what)
 
 
+def _dense_pages(t) -> bool:
+    """All but the first dimension dense (the stride of a dimension of one element says nothing)."""
+    want = 1
+    for size, stride in zip(t.shape[:0:-1], t.stride()[:0:-1]):
+        if size > 1 and stride != want:
+            return False
+        want *= size
+    return True
+
+
 class DmtpPagedCache:
     """A paged K/V cache of one layer over the caller's tensors.
 
     k, v: [n_pages, n_kv_heads, page_size, head_dim], bf16 or fp32, or float8_e4m3fn with
     k_scale and v_scale [n_pages, n_kv_heads, page_size] fp32; the pages may be strided (a
-    pool that holds several layers), the rest is dense. table: int32 [n_seqs, max_blocks],
+    pool that holds several layers), k's and v's alike, the rest is dense. table: int32 [n_seqs, max_blocks],
     the page of each block of each sequence. dtype: the type of the rows given and returned
     (bf16 or fp32; of a cache that is not E4M3, its own). The tensors may be updated between
     calls; they are the ones given here, not copies."""
@@ -136,16 +146,17 @@ class DmtpPagedCache:
              all(t is None or isinstance(t, torch.Tensor) for t in (k_scale, v_scale)),
              "k, v, table and scales are tensors")
         e8 = k.dtype is c.f8
-        need(k.dim() == 4 and v.shape == k.shape and v.dtype is k.dtype and
-             v.stride() == k.stride(), "k and v: the same 4-d shape, strides and dtype")
+        need(k.dim() == 4 and v.shape == k.shape and v.dtype is k.dtype,
+             "k and v: the same 4-d shape and dtype")
         n, h, ps, hd = k.shape
-        need(k.stride()[1:] == (ps * hd, hd, 1), "pages must be dense")
+        need(_dense_pages(k) and _dense_pages(v) and (n <= 1 or v.stride(0) == k.stride(0)),
+             "pages must be dense, and k's and v's as far apart")
         if e8:
             self.dtype = c.bf16 if dtype is None else dtype
             need(k_scale is not None and v_scale is not None, "an E4M3 cache has scales")
             for s in (k_scale, v_scale):
                 need(s.shape == (n, h, ps) and s.dtype is c.fp32 and
-                     s.stride()[1:] == (ps, 1) and s.stride(0) == k_scale.stride(0),
+                     _dense_pages(s) and (n <= 1 or s.stride(0) == k_scale.stride(0)),
                      "scales: fp32 [n_pages, n_kv_heads, page_size], pages dense")
         else:
             self.dtype = k.dtype

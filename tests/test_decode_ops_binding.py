@@ -61,3 +61,34 @@ def test_tensors_of_other_ranks_are_argument_errors():
                  lambda: sample_rows(torch.zeros(()), torch.zeros(())), lambda: add_rmsnorm_e4m3(one, None, one)):
         with pytest.raises(DmtpError):
             call()
+
+
+def single_dimensions():
+    """Dense pages whose dimensions of one element have strides of their own."""
+    one_head = torch.zeros((8, 16, 1, 64), dtype=BF).transpose(1, 2)
+    one_row = torch.zeros((8, 1, 4, 64), dtype=BF).transpose(1, 2)
+    big = torch.zeros((3, 2, 16, 64), dtype=BF)
+    return [(one_head, one_head.contiguous()), (one_head.contiguous(), one_head), (one_row, one_row.clone()),
+            (big[:1], big.clone()[::2][:1])]
+
+
+@pytest.mark.parametrize("i", range(4))
+def test_strides_of_single_elements_do_not_count(i):
+    k, v = single_dimensions()[i]
+    c = DmtpPagedCache(k, v, torch.zeros((1, 2), dtype=I32))
+    n, h, ps, hd = k.shape
+    assert c.c.page_stride == (k.stride(0) if n > 1 else h * ps * hd)
+    k8, v8 = (t.to(FP).to(torch.float8_e4m3fn).as_strided(t.shape, t.stride()) for t in (k.contiguous(), v.contiguous()))
+    ks = torch.ones((n, ps, h)).transpose(1, 2) if h == 1 else torch.ones((n, h, ps))
+    DmtpPagedCache(k8, v8, torch.zeros((1, 2), dtype=I32), ks, torch.ones((n, h, ps)))
+
+
+def test_pages_that_are_not_dense_or_differ_are_refused():
+    t = torch.zeros((1, 2), dtype=I32)
+    k = torch.zeros((8, 4, 16, 64), dtype=BF)
+    wide = torch.zeros((8, 4, 16, 128), dtype=BF)
+    for a, b in ((k[:, :, ::2], k[:, :, ::2]), (wide[..., :64], wide[..., :64]), (k[:, ::2], k[:, ::2]),
+                 (k[::2], k[:4]), (k[:, :2], k[:, :2].contiguous())):
+        with pytest.raises(DmtpError):
+            DmtpPagedCache(a, b, t)
+    DmtpPagedCache(k[:, :2], k[:, 2:], t)      # two layers of a pool, page by page

@@ -134,6 +134,26 @@ def test_attention_of_small_values_beside_rows_of_zeros(hd, hq, rows, size, zero
     check_attention(c, q, lens, stored(c, lens))
 
 
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("hkv,ps", [(1, 16), (4, 1)])
+def test_pages_of_one_head_or_one_row_with_other_strides(dtype, hkv, ps):
+    """A pool kept as [pages, rows, heads, head_dim] is dense page by page when one of the two is 1."""
+    from mtp_block_draft_gb300 import DmtpPagedCache
+    hd, n = 64, 90
+    blocks = -(-n // ps)
+    table = torch.arange(blocks, dtype=torch.int32, device="cuda").flip(0)[None]
+    made = [torch.zeros((blocks, ps, hkv, hd), dtype=dtype, device="cuda").transpose(1, 2) for _ in range(2)]
+    c = DmtpPagedCache(made[0], made[1], table)
+    d = DmtpPagedCache.alloc(blocks, ps, hkv, hd, table, dtype=dtype)
+    g = gen(hkv)
+    k, v, q = randn((n, hkv, hd), g, dtype), randn((n, hkv, hd), g, dtype), randn((1, 2, 8, hd), g, dtype)
+    for x in (c, d):
+        x.write(k, v, i32([0] * n), i32(range(n)), rope_theta=1e4)
+    a, b = (x.attention(q, i32([n])) for x in (c, d))
+    assert torch.equal(c.k, d.k) and torch.equal(c.v, d.v) and torch.equal(a, b)
+    check_attention(c, q, [n], stored(c, [n]))
+
+
 # ---- norm -----------------------------------------------------------------------------
 
 @pytest.mark.parametrize("rows", [40, 200])

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes as C
 import struct
+import threading
 
 from .binding import (DmtpError, _check, dmtp_norm_args, dmtp_paged_kv, dmtp_paged_query,
                       dmtp_paged_rows, dmtp_sample_args, load_library)
@@ -129,10 +130,11 @@ class DmtpPagedCache:
 
     k, v: [n_pages, n_kv_heads, page_size, head_dim], bf16 or fp32, or float8_e4m3fn with
     k_scale and v_scale [n_pages, n_kv_heads, page_size] fp32; the pages may be strided (a
-    pool that holds several layers), k's and v's alike, the rest is dense. table: int32 [n_seqs, max_blocks],
-    the page of each block of each sequence. dtype: the type of the rows given and returned
-    (bf16 or fp32; of a cache that is not E4M3, its own). The tensors may be updated between
-    calls; they are the ones given here, not copies."""
+    pool that holds several layers), k's and v's alike, the rest is dense. table: int32
+    [n_seqs, max_blocks], the page of each block of each sequence. dtype: the type of the rows
+    given and returned (bf16 or fp32; of a cache that is not E4M3, its own). The tensors may be
+    updated between calls; they are the ones given here, not copies. A cache is made outside
+    stream captures; its calls may come from any stream and thread."""
 
     def __init__(self, k, v, table, k_scale=None, v_scale=None, dtype=None):
         c = _c()
@@ -184,6 +186,11 @@ class DmtpPagedCache:
         p.n_seqs, p.max_blocks = self.n_seqs, self.max_blocks
         p.dtype, p.e4m3 = int(self.dtype is c.bf16), int(e8)
         self.err = torch.zeros(1, dtype=c.int32, device=k.device)
+        if self._dev >= 0 and not torch.cuda.is_current_stream_capturing():
+            # calls may come on any stream: the word is 0 before the first of them sets a bit
+            torch.cuda.current_stream(k.device).synchronize()
+        self._lock = threading.Lock()
+        self._word = torch.zeros(1, dtype=torch.int64, device=k.device)  # index of the word in err
         self._err = self.err.data_ptr()
         self._c = bytes(p)
         self._scale = hd ** -0.5
@@ -313,11 +320,16 @@ class DmtpPagedCache:
 
     def check(self):
         """Wait for the device and raise DmtpError(DMTP_EDEVICE) if any call since the last
-        check met an index out of range; the word is then cleared."""
-        _c().torch.cuda.synchronize(self.device)
-        word = int(self.err.item())
+        check met an index out of range; the bits that it reports are then cleared."""
+        torch = _c().torch
+        with self._lock:
+            torch.cuda.synchronize(self.device)
+            word = int(self.err.item())
+            if word:
+                # taken off by an atomic addition: a bit that a call on another stream sets after
+                # the word was read stays for the next check
+                self.err.index_add_(0, self._word, torch.full_like(self.err, -word))
         if word:
-            self.err.zero_()
             raise DmtpError(-5, "paged cache", word)
 
 

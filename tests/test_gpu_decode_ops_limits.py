@@ -154,6 +154,56 @@ def test_pages_of_one_head_or_one_row_with_other_strides(dtype, hkv, ps):
     check_attention(c, q, [n], stored(c, [n]))
 
 
+# ---- the error word -------------------------------------------------------------------
+
+def test_the_error_word_is_clear_before_a_call_on_another_stream():
+    """The stream that is current when a cache is made may be busy; a call on another one may come first."""
+    from mtp_block_draft_gb300 import DmtpError
+    k = torch.zeros((1, 2, 64), dtype=BF, device="cuda")
+    seq, pos, table = i32([7]), i32([0]), i32([[0, 1], [2, 3]])
+    from mtp_block_draft_gb300 import DmtpPagedCache
+    side = torch.cuda.Stream()
+    for _ in range(2):                         # (kernels are loaded at their first call, which waits)
+        c = DmtpPagedCache.alloc(4, 16, 2, 64, table)
+        with torch.cuda.stream(side):
+            c.write(k, k, i32([0]), pos)
+        c.check()
+    torch.cuda._sleep(200_000_000)             # about 0.1 s of the current stream
+    c = DmtpPagedCache.alloc(4, 16, 2, 64, table)
+    with torch.cuda.stream(side):
+        c.write(k, k, seq, pos)                # no such sequence
+    with pytest.raises(DmtpError) as e:
+        c.check()
+    assert e.value.word == 32
+    c.check()
+
+
+def test_check_clears_what_it_reports_and_nothing_else():
+    """A call that goes wrong between check()'s reading of the word and its clearing counts for the next."""
+    from mtp_block_draft_gb300 import DmtpError
+    c = new_cache(2, 2, 16, 2, 64)
+    k = torch.zeros((1, 2, 64), dtype=BF, device="cuda")
+    bad_pos, bad_seq, at = (i32([0]), i32([32])), i32([7]), i32([0])
+    read, late = c.err.item, []
+
+    def item():
+        word = read()
+        if not late:
+            late.append(1)
+            c.write(k, k, bad_seq, at)
+            c.write(k, k, *bad_pos)
+            torch.cuda.synchronize()
+        return word
+
+    c.write(k, k, *bad_pos)
+    c.err.item = item
+    for word in (2, 32):
+        with pytest.raises(DmtpError) as e:
+            c.check()
+        assert e.value.word == word
+    c.check()
+
+
 # ---- norm -----------------------------------------------------------------------------
 
 @pytest.mark.parametrize("rows", [40, 200])

@@ -3,7 +3,8 @@
 Argument checks and marshalling only: every call enqueues the library's kernels on the
 current stream of the tensors' device. Argument errors raise DmtpError(DMTP_EINVAL) before
 anything is launched; what only the device can see (an index out of range) is collected in
-the cache's error word, which check() reads.
+the cache's error word, which check() reads. The operators are for inference: results carry no
+gradient, whatever the inputs require.
 """
 from __future__ import annotations
 
@@ -47,6 +48,9 @@ class _Calls:
         self.device = torch._C._cuda_getDevice
 
 
+# What the checks below run into with an argument that is no tensor, or has too few dimensions.
+_NO_TENSOR = (AttributeError, IndexError, TypeError)
+
 _calls = None
 
 
@@ -69,7 +73,6 @@ def _pack(s, *args) -> bytes:
         _bad(str(e))
 
 
-# (What is no tensor at all fails an attribute below: the checks cost a call nothing then.)
 def _dtype(c, t) -> int:
     """dtype code of a float tensor: 0 fp32, 1 bf16."""
     d = getattr(t, "dtype", type(t))
@@ -86,20 +89,9 @@ def _vector(t, dtype, n: int, dev: int, what: str) -> int:
         if t.dtype is dtype and t.shape == (n,) and t.get_device() == dev and (
                 n <= 1 or t.stride() == (1,)):
             return t.data_ptr()
-    except AttributeError:
+    except _NO_TENSOR:
         pass
     _bad(f"{what}: a dense {dtype} tensor of {n} on the same device is wanted")
-
-
-def _shape(t, dims: int, what: str):
-    """Shape of a tensor of so many dimensions."""
-    try:
-        t.data_ptr
-        if len(t.shape) == dims:
-            return t.shape
-    except AttributeError:
-        pass
-    _bad(what)
 
 
 def _run(c, f, dev: int, what: str, *args):
@@ -221,7 +213,7 @@ class DmtpPagedCache:
                 s0, s1, s2 = t.stride()
                 if s2 == 1:
                     return (s0 if n > 1 else heads * self.head_dim), (s1 if heads > 1 else self.head_dim)
-        except AttributeError:
+        except _NO_TENSOR:
             pass
         _bad(f"{what}: [{n}, {heads}, {self.head_dim}], head_dim dense, of the cache's dtype and device")
 
@@ -230,14 +222,18 @@ class DmtpPagedCache:
         sequences seq (int32 [n]; seq < 0: skipped), rotated first if rope_theta > 0. With q
         [n, n_heads, head_dim] returns the rotated queries (q_out, or a new tensor)."""
         c, dev = _c(), self._dev
-        n, h = _shape(seq, 1, "seq: int32 [n]")[0], self.n_kv_heads
+        qp = qop = qr = qh = qor = qoh = heads = 0
+        try:
+            n, h = seq.shape[0], self.n_kv_heads
+            if q is not None:
+                heads = q.shape[1]
+                if q_out is None:
+                    q_out = c.torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        except _NO_TENSOR:
+            _bad("seq: int32 [n]; q: [n, n_heads, head_dim]")
         kr, kh = self._rows(k, n, h, "k")
         vr, vh = self._rows(v, n, h, "v")
-        qp = qop = qr = qh = qor = qoh = heads = 0
         if q is not None:
-            heads = _shape(q, 3, "q: [n, n_heads, head_dim]")[1]
-            if q_out is None:
-                q_out = c.torch.empty(q.shape, dtype=q.dtype, device=q.device)
             qr, qh = self._rows(q, n, heads, "q")
             qor, qoh = self._rows(q_out, n, heads, "q_out")
             qp, qop = q.data_ptr(), q_out.data_ptr()
@@ -251,16 +247,19 @@ class DmtpPagedCache:
         """dmtp_paged_read: positions pos of sequences seq (int32 [n]) as dense rows
         [n, n_kv_heads, head_dim]; returns (k, v)."""
         c, dev = _c(), self._dev
-        n = _shape(seq, 1, "seq: int32 [n]")[0]
-        shape = (n, self.n_kv_heads, self.head_dim)
-        if k_out is None:
-            k_out = c.torch.empty(shape, dtype=self.dtype, device=self.device)
-        if v_out is None:
-            v_out = c.torch.empty(shape, dtype=self.dtype, device=self.device)
-        for t in (k_out, v_out):
-            if _shape(t, 3, "k_out, v_out: [n, n_kv_heads, head_dim]") != shape or t.dtype is not self.dtype or not t.is_contiguous() or \
-                    t.get_device() != dev:
-                _bad(f"k_out, v_out: dense {shape} of the cache's dtype and device")
+        try:
+            n = seq.shape[0]
+            shape = (n, self.n_kv_heads, self.head_dim)
+            if k_out is None:
+                k_out = c.torch.empty(shape, dtype=self.dtype, device=self.device)
+            if v_out is None:
+                v_out = c.torch.empty(shape, dtype=self.dtype, device=self.device)
+            for t in (k_out, v_out):
+                if t.shape != shape or t.dtype is not self.dtype or not t.is_contiguous() or \
+                        t.get_device() != dev:
+                    _bad(f"k_out, v_out: dense {shape} of the cache's dtype and device")
+        except _NO_TENSOR:
+            _bad("seq: int32 [n]; k_out, v_out: [n, n_kv_heads, head_dim]")
         _run(c, c.paged_read, dev, "dmtp_paged_read", self._c,
              _vector(seq, c.int32, n, dev, "seq"), _vector(pos, c.int32, n, dev, "pos"), n,
              k_out.data_ptr(), v_out.data_ptr(), self._err)
@@ -273,17 +272,22 @@ class DmtpPagedCache:
         attention_workspace() bytes that no overlapping call uses; None: taken from PyTorch's
         allocator for this call."""
         c, dev = _c(), self._dev
-        shape = _shape(q, 4, "q: [n_seqs, rows, n_heads, head_dim]")
-        B, rows, heads, hd = shape
-        if out is None:
-            out = c.torch.empty(shape, dtype=q.dtype, device=q.device)
-        if B != self.n_seqs or hd != self.head_dim or q.dtype is not self.dtype or \
-                q.get_device() != dev:
-            _bad(f"q: [{self.n_seqs}, rows, n_heads, {self.head_dim}] of the cache's dtype and device")
-        if _shape(out, 4, "out: the shape of q") != shape or out.dtype is not self.dtype or out.get_device() != dev:
-            _bad("out: the shape, dtype and device of q")
-        qb, qr, qh, q1 = q.stride()
-        ob, orow, oh, o1 = out.stride()
+        try:
+            shape = q.shape
+            if len(shape) != 4:
+                _bad("q: [n_seqs, rows, n_heads, head_dim]")
+            B, rows, heads, hd = shape
+            if out is None:
+                out = c.torch.empty(shape, dtype=q.dtype, device=q.device)
+            if B != self.n_seqs or hd != self.head_dim or q.dtype is not self.dtype or \
+                    q.get_device() != dev:
+                _bad(f"q: [{self.n_seqs}, rows, n_heads, {self.head_dim}] of the cache's dtype and device")
+            if out.shape != shape or out.dtype is not self.dtype or out.get_device() != dev:
+                _bad("out: the shape, dtype and device of q")
+            qb, qr, qh, q1 = q.stride()
+            ob, orow, oh, o1 = out.stride()
+        except _NO_TENSOR:
+            _bad("q, out: [n_seqs, rows, n_heads, head_dim]")
         if q1 != 1 or o1 != 1:
             _bad("head_dim must be dense")
         if B == 1:  # (the stride of a dimension of one element says nothing)
@@ -299,9 +303,12 @@ class DmtpPagedCache:
         if n is None:
             n = self._ws_bytes[rows, heads] = self.attention_workspace(rows, heads)
         if workspace is not None:
-            _shape(workspace, 1, "workspace: a dense uint8 tensor")
-            if workspace.dtype is not c.torch.uint8 or workspace.get_device() != dev or \
-                    not workspace.is_contiguous():
+            try:
+                ok = workspace.dtype is c.torch.uint8 and workspace.get_device() == dev and \
+                    workspace.is_contiguous()
+            except _NO_TENSOR:
+                ok = False
+            if not ok:
                 _bad("workspace: a dense uint8 tensor on the cache's device")
             n = workspace.numel()
         elif n and dev >= 0:  # on the stream that the kernels are enqueued on
@@ -340,7 +347,7 @@ def _matrix(t, shape, dtype, dev: int, what: str) -> int:
             s0, s1 = t.stride()
             if s1 == 1 or shape[1] == 1:
                 return s0 if shape[0] > 1 else shape[1]
-    except AttributeError:
+    except _NO_TENSOR:
         pass
     _bad(f"{what}: {dtype} {tuple(shape)} with dense rows on the same device")
 
@@ -349,8 +356,14 @@ def add_rmsnorm_e4m3(x, y, gain, eps: float = 1e-6, x_out=None, q=None, scale=No
     """dmtp_add_rmsnorm_e4m3: x_out = x + y, and E4M3 rows of RMSNorm(x + y) * gain. x, y
     [rows, d] bf16 or fp32 (y None: no addition); x_out may be x (None: a new tensor, or x
     where y is None). Returns (x_out, q float8_e4m3fn [rows, d], scale fp32 [rows])."""
-    c, shape = _c(), _shape(x, 2, "x: [rows, d]")
-    dev, (rows, d) = x.get_device(), shape
+    c = _c()
+    try:
+        dev, shape = x.get_device(), x.shape
+    except _NO_TENSOR:
+        _bad("x: [rows, d]")
+    if len(shape) != 2:
+        _bad("x: [rows, d]")
+    rows, d = shape
     x_dt, y_dt, g_dt = _dtype(c, x), 0, _dtype(c, gain)
     xr = _matrix(x, shape, x.dtype, dev, "x")
     yp = yr = xop = xor = 0
@@ -379,8 +392,14 @@ def sample_rows(logits, u, temperature=None, top_k=None, top_p=None, min_p=None,
     with the uniform numbers u (fp32 [rows]) under temperature, top_k (int32), top_p and
     min_p (fp32 [rows] each, None: off). Returns ids (int32 [rows]; -1 where nothing may be
     chosen); kept (int32 [rows], optional) receives how many tokens passed the filters."""
-    c, shape = _c(), _shape(logits, 2, "logits: [rows, vocab]")
-    dev, (rows, V) = logits.get_device(), shape
+    c = _c()
+    try:
+        dev, shape = logits.get_device(), logits.shape
+    except _NO_TENSOR:
+        _bad("logits: [rows, vocab]")
+    if len(shape) != 2:
+        _bad("logits: [rows, vocab]")
+    rows, V = shape
     dt = _dtype(c, logits)
     ld = _matrix(logits, shape, logits.dtype, dev, "logits")
     if ids is None:

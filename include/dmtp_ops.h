@@ -11,6 +11,7 @@
  *   dmtp_add_rmsnorm_e4m3  residual addition, RMS norm, E4M3 rows (the draft heads' 8-bit
  *                          row format)
  *   dmtp_sample_rows       temperature, top-k, top-p and min-p from given random numbers
+ * They are for inference: none has a backward pass.
  *
  * Memory. The caller owns every buffer; nothing is allocated. Pointers are device
  * pointers on the current device, and work is enqueued on `stream` (NULL: the default
@@ -75,10 +76,11 @@ typedef struct {
 /* New rows: row r of k and v (both [n_rows][n_kv_heads][head_dim], with the given strides
  * in elements; head_dim dense) belongs at position pos[r] of sequence seq[r] (device
  * int32). A row with seq[r] < 0 is skipped (padding); its q_out row is left as it was. A
- * position that two rows of one call name gets the values of one of them, or a mixture.
+ * position that two rows of one call name gets the values of one of them, or a mixture (in an
+ * E4M3 cache bytes of one may meet the other's scale): a call's positions should differ.
  * rope_theta > 0: k (and q) are rotated first, pairs (i, i + head_dim / 2) by the angle
- * pos * rope_theta^(-2 i / head_dim), formed to 2^-30 turns or better at any position;
- * 0: stored as they are. q (optional, NULL): [n_rows][n_heads][head_dim], rotated into
+ * pos * rope_theta^(-2 i / head_dim), formed to pos 2^-53 turns (2^-30 at position 2^23, 2^-22
+ * at the last); 0: stored as they are. q (optional, NULL): [n_rows][n_heads][head_dim], rotated into
  * q_out [n_rows][n_heads][head_dim] (both may be the same memory with the same strides).
  * All are of the cache's dtype. Row pointers and strides are multiples of four elements
  * (bf16: 8 bytes, fp32: 16 bytes). The rotation is computed in fp32 from fp32 sines. */
@@ -113,7 +115,8 @@ int dmtp_paged_read(const dmtp_paged_kv* c, const int32_t* seq, const int32_t* p
  * positions are left out. A NaN or an infinity reaches the rows that see its position (a value
  * whose weight rounds to 0 may not) and no other. |scale| <= 1e30.
  * Scores, softmax statistics and sums are fp32; products of bf16 rows run on the tensor
- * cores with the weights as bf16 pairs (16 bits), of E4M3 rows with fp16 weights (11 bits): a
+ * cores with the weights as bf16 pairs (16 bits), of E4M3 rows with fp16 queries (scaled; exact but
+ * for elements below 2^-29 of a query's largest) and fp16 weights (11 bits): a
  * weight times its v_scale is rounded against the largest such product of the query so far, in
  * which value rows of zeros with a v_scale of at least 1 (dmtp_paged_write gives them 1) do not
  * count (v_scale up to 2^40; values of rows scaled by less than 2^-60 count to 2^-76). The sum of
@@ -139,9 +142,9 @@ int dmtp_paged_attention(const dmtp_paged_kv* c, const dmtp_paged_query* a, void
  * h = (x + y) / sqrt(mean((x + y)^2) + eps) * gain, q [rows][d] E4M3 values with row pitch
  * q_row, scale [rows] fp32. x, x_out: x_dtype; y: y_dtype; gain [d]: gain_dtype; row
  * pitches in elements. The sum of squares is fp32: |x + y| up to about 1e17. An infinite
- * x + y makes the row's finite values 0, a NaN all of them NaN. x_out may be x;
- * y may be NULL (no addition; x_out may then be NULL too). Limits: d a multiple of 8 up to DMTP_OPS_MAX_NORM_D; row starts 16-byte aligned
- * (q: 8-byte), pitches >= d and multiples of 8; eps >= 0 and finite. */
+ * x + y makes the row's finite values 0, a NaN all of them NaN. x_out may be x; y may be NULL (no
+ * addition; x_out may then be NULL too). Limits: d a multiple of 8 up to DMTP_OPS_MAX_NORM_D; row
+ * starts 16-byte aligned (q: 8-byte), pitches >= d and multiples of 8; eps >= 0 and finite. */
 typedef struct {
   const void *x, *y, *gain;
   void *x_out, *q;

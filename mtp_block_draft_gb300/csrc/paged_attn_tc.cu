@@ -9,7 +9,7 @@
 // side of both products (S^T = K Q^T, O^T = V^T P^T), so 8 queries fill an instruction. (The
 // tcgen05 form wants 128 rows of keys and one thread to start each product of the whole CTA;
 // a block would wait for its neighbours, and E4M3 rows would go through shared memory twice: built
-// for 64 queries, one CTA of eight warps an SM, it took 96 us where this takes 65.)
+// for 64 queries, one CTA of eight warps an SM, it took 96 us where this takes 66.)
 //
 //   QN queries    teams             a team's ring
 //   8, 16         4 of one warp     16 keys a stage, no barrier but the warp's own
@@ -20,12 +20,12 @@
 // 512 to 4096 positions, 4 kv heads of 128, us with QN 8 / 16 / 32 / 64: 8 queries in bf16 30.4 /
 // 33.4 / 39.8 / 59.3, in E4M3 23.2 / 29.6 / 37.8 / 55.8; 16 42.5 / 35.8 / 41.6 / 61.0, 34.8 / 31.2 /
 // 39.8 / 57.8; 32 68.5 / 53.0 / 44.5 / 64.3, 58.5 / 48.2 / 41.8 / 59.5; 64 121 / 93.3 / 78.5 / 71.6,
-// 104 / 86.0 / 72.3 / 65.9.
+// 104 / 86.0 / 72.3 / 65.9 (E4M3 before its stages were looked through for rows of zeros: 1% more now).
 //
 // Times (us in a captured graph, the merge included): 32 sequences of 512 to 4096 bf16 positions,
-// 8 queries a kv head, 30.2 (151 MB, 0.74 of the copy rate; with longer contexts each further byte
+// 8 queries a kv head, 30.3 (151 MB, 0.74 of the copy rate; with longer contexts each further byte
 // costs what a copy would, 8 us do not grow); 4 sequences of 32768 in E4M3 31.2 (0.65, issue 50%);
-// 64 queries in E4M3 65.4: dependent instructions of 12 warps an SM (issue 49%, tensor pipe 30%).
+// 64 queries in E4M3 66.4: dependent instructions of 12 warps an SM (issue 47%, tensor pipe 29%).
 //
 // A warp has at most 16 queries: with 32 (and half the conversions of E4M3 rows) only two CTAs fit
 // an SM, and 32 sequences of 512 to 4096 E4M3 positions x 64 queries took 78 us instead of 65.
@@ -33,10 +33,13 @@
 // Weights 2^(s - m) use a running maximum m per query that moves only when a score passes it
 // by 2^8 (so most blocks skip the rescaling). bf16 caches: P as a bf16 pair (16 bits of each
 // weight), two products a fragment. E4M3 caches: rows become fp16 exactly, the queries too
-// after a power-of-two scale per query, and P carries the value row's scale: with v = 2^e c
+// after a power-of-two scale per query (but elements below 2^-29 of the query's largest, which
+// keep 2^-37 of that), and P carries the value row's scale: with v = 2^e c
 // and weight w, m follows log2(w 2^e) and P = w 2^(e - m), so what is rounded to fp16 is the
 // row's contribution relative to the largest one; the sum of weights undoes the exponent in
-// fp32. (e stops at -60, and rows of zeros do not set m, see below.)
+// fp32. A weight's 11 bits stand against the 4 of a cached value; with fp16 pairs, as bf16 caches
+// have them, 64 queries would take 73.9 us instead of 66.4, 32 48.6 instead of 42.3, 8 24.4
+// instead of 23.5. (e stops at -60, and rows of zeros do not set m, see below.)
 #include <cuda_fp16.h>
 
 #include "paged_attn.cuh"

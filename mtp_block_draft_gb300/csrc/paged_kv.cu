@@ -8,10 +8,11 @@
 // rate, two thirds of the issue slots used); 32 rows into E4M3 pages 3.0 us, which is latency.
 //
 // Angles. Position p turns pair i by p f_i turns, f_i = theta^(-2i/hd) / 2 pi < 1. The host
-// forms f_i in double and passes round(f_i 2^64); p times that, modulo 2^64, is the angle's
-// fraction of a turn in fixed point, with no loss at far positions (error p 2^-55 from
-// f_i's own 53 bits) and without the GPU's slow double arithmetic. The fraction
-// goes to the sine as a 24-bit value and a first-order correction for the rest.
+// forms f_i in double and passes f_i 2^64 as an integer; p times that, modulo 2^64, is the angle's
+// fraction of a turn in fixed point, which loses nothing more at far positions and needs none of
+// the GPU's slow double arithmetic. What is left is f_i's own error: its power is off by
+// (ln(theta) 2i/hd + 4) 2^-53 of itself at most, in turns less than 2^-53, so p 2^-53 at
+// position p. The fraction goes to the sine as a 24-bit value and a first-order correction for the rest.
 #include <math.h>
 
 #include <cuda_fp16.h>
@@ -175,8 +176,8 @@ struct ReadArgs {
 // A group of lanes copies kHeads heads of one row, 16 bytes of the cache a lane and head (of an
 // E4M3 cache 8, so that a bf16 row is written in whole lines): the chain position -> page -> row
 // is walked once for all of them, and their loads are in flight together. 8 prefixes of 4096 rows of
-// 2 x 2 heads of 128, E4M3 to bf16, take 11.5 us (51 MB, 0.65 of the copy rate): one wave of CTAs,
-// each behind that chain of loads. 37 rows take 2.5 us.
+// 2 x 2 heads of 128, E4M3 to bf16, take 11.5 us (51 MB, 0.65 of the copy rate): 2048 CTAs, 1.7
+// waves, each behind that chain of loads. 37 rows take 2.5 us.
 constexpr int kHeads = 4;
 template <typename T, bool E8>
 __global__ void __launch_bounds__(256) k_paged_read(const ReadArgs a) {
@@ -267,7 +268,7 @@ int check_cache(const dmtp_paged_kv* c) {
 using namespace dmtp;
 
 namespace {
-// round(theta^(-2i/hd) / (2 pi) * 2^64) for a head's pairs; a thread that keeps calling with
+// theta^(-2i/hd) / (2 pi) * 2^64 for a head's pairs; a thread that keeps calling with
 // one base and head size forms them once.
 const Turns& turns_of(float theta, int hd) {
   static thread_local Turns t;

@@ -142,7 +142,7 @@ int dmtp_paged_attention(const dmtp_paged_kv* c, const dmtp_paged_query* a, void
  * h = (x + y) / sqrt(mean((x + y)^2) + eps) * gain, q [rows][d] E4M3 values with row pitch
  * q_row, scale [rows] fp32. x, x_out: x_dtype; y: y_dtype; gain [d]: gain_dtype; row
  * pitches in elements. The sum of squares is fp32: |x + y| up to about 1e17 (and, with an
- * eps below about 1e-30, the row's largest not below 1e-17 unless it is 0). An infinite
+ * eps below about 1e-30, the row's largest from 1e-17 on; of zeros with eps 0 it is 0 / 0). An infinite
  * x + y makes the row's finite values 0, a NaN all of them NaN. x_out may be x; y may be NULL (no
  * addition; x_out may then be NULL too). Limits: d a multiple of 8 up to DMTP_OPS_MAX_NORM_D; row
  * starts 16-byte aligned (q: 8-byte), pitches >= d and multiples of 8; eps >= 0 and finite. */

@@ -8,8 +8,8 @@ its CUDA sources (``csrc/``), the in-tree build (``build.py``) and the ctypes bi
 """
 from .binding import (DmtpError, DmtpGate, DmtpRound, DmtpVocabList, default_max_ctx,
                       load_library, make_config, make_weights)
-from .ops import DmtpPagedCache, add_rmsnorm_e4m3, sample_rows
+from .ops import DmtpPagedCache, DmtpRope, add_rmsnorm_e4m3, sample_rows
 
-__all__ = ["DmtpError", "DmtpGate", "DmtpPagedCache", "DmtpRound", "DmtpVocabList",
+__all__ = ["DmtpError", "DmtpGate", "DmtpPagedCache", "DmtpRope", "DmtpRound", "DmtpVocabList",
            "add_rmsnorm_e4m3", "default_max_ctx", "load_library", "make_config", "make_weights",
            "sample_rows"]

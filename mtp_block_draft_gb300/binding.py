@@ -35,7 +35,9 @@ EXPORTS = ("dmtp_workspace_size", "dmtp_init", "dmtp_round", "dmtp_round_host",
            "dmtp_vocab_picked", "dmtp_vocab_ids", "dmtp_vocab_mask", "dmtp_vocab_counts",
            "dmtp_vocab_stats_read", "dmtp_vocab_free",
            "dmtp_paged_write", "dmtp_paged_read", "dmtp_paged_attention_workspace",
-           "dmtp_paged_attention", "dmtp_add_rmsnorm_e4m3", "dmtp_sample_rows")
+           "dmtp_paged_attention", "dmtp_paged_write_rope", "dmtp_paged_attention_scores",
+           "dmtp_paged_prompt_workspace", "dmtp_paged_prompt_attention",
+           "dmtp_add_rmsnorm_e4m3", "dmtp_sample_rows")
 
 DMTP_GATE_MAX_DRAFTS = 32
 DMTP_GATE_MAX_ROWS = 64
@@ -130,6 +132,24 @@ class dmtp_paged_query(C.Structure):
                    ("window", C.c_int), ("scale", C.c_float)])
 
 
+class dmtp_rope(C.Structure):
+    _fields_ = ([(f, C.c_double) for f in ("theta", "factor", "orig_len", "low", "high")]
+                + [("dims", C.c_int), ("interleaved", C.c_int), ("scaling", C.c_int),
+                   ("amplitude", C.c_float)])
+
+
+class dmtp_paged_scores(C.Structure):
+    _fields_ = [("cap", C.c_float), ("slopes", C.c_void_p)]
+
+
+class dmtp_paged_prompt(C.Structure):
+    _fields_ = ([("q", C.c_void_p), ("out", C.c_void_p)]
+                + [(f, C.c_int64) for f in ("q_row", "q_head", "o_row", "o_head")]
+                + [(f, C.c_void_p) for f in ("row_start", "kv_len", "first", "end")]
+                + [("n_rows", C.c_int), ("n_heads", C.c_int), ("window", C.c_int),
+                   ("scale", C.c_float), ("scores", dmtp_paged_scores)])
+
+
 class dmtp_norm_args(C.Structure):
     _fields_ = ([(f, C.c_void_p) for f in ("x", "y", "gain", "x_out", "q", "scale")]
                 + [(f, C.c_int64) for f in ("x_row", "y_row", "xo_row", "q_row")]
@@ -216,10 +236,17 @@ def load_library(path: str = LIB_PATH):
     lib.dmtp_paged_attention_workspace.argtypes = [KV, C.POINTER(dmtp_paged_query),
                                                    C.POINTER(C.c_size_t)]
     lib.dmtp_paged_attention.argtypes = [KV, C.POINTER(dmtp_paged_query), P, C.c_size_t, P, P]
+    lib.dmtp_paged_write_rope.argtypes = [KV, C.POINTER(dmtp_paged_rows), C.POINTER(dmtp_rope), P, P]
+    lib.dmtp_paged_attention_scores.argtypes = [KV, C.POINTER(dmtp_paged_query),
+                                                C.POINTER(dmtp_paged_scores), P, C.c_size_t, P, P]
+    lib.dmtp_paged_prompt_workspace.argtypes = [KV, C.POINTER(dmtp_paged_prompt),
+                                                C.POINTER(C.c_size_t)]
+    lib.dmtp_paged_prompt_attention.argtypes = [KV, C.POINTER(dmtp_paged_prompt), P, C.c_size_t, P, P]
     lib.dmtp_add_rmsnorm_e4m3.argtypes = [C.POINTER(dmtp_norm_args), P]
     lib.dmtp_sample_rows.argtypes = [C.POINTER(dmtp_sample_args), P]
     for f in ("paged_write", "paged_read", "paged_attention_workspace", "paged_attention",
-              "add_rmsnorm_e4m3", "sample_rows"):
+              "paged_write_rope", "paged_attention_scores", "paged_prompt_workspace",
+              "paged_prompt_attention", "add_rmsnorm_e4m3", "sample_rows"):
         getattr(lib, "dmtp_" + f).restype = C.c_int
     _lib = lib
     return lib

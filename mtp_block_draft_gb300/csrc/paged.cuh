@@ -2,11 +2,17 @@
 // device-side page lookups, E4M3 row helpers, row loads, and the launch helpers.
 #pragma once
 
+#include <cuda_fp16.h>
+
 #include "../../include/dmtp_ops.h"
 #include "common.cuh"
 #include "ops.h"
 
 namespace dmtp {
+
+// How a cache's rows are stored: values of its dtype, or with scales.
+enum Rows { kRaw, kE4M3, kE2M1 };
+inline Rows rows_of(const dmtp_paged_kv& c) { return c.e4m3 == DMTP_OPS_E2M1 ? kE2M1 : c.e4m3 ? kE4M3 : kRaw; }
 
 // ---- host -----------------------------------------------------------------------------
 // Launch on `st`; `after`: a kernel of the same call precedes it and it calls pdl_wait()
@@ -53,6 +59,9 @@ inline bool smem_limit(const void* k, int bytes, unsigned long long* done) {
 inline bool mult(int64_t v, int64_t of) { return v % of == 0; }
 // The checks of dmtp_ops.h that every call makes of its cache.
 int check_cache(const dmtp_paged_kv* c);
+// dmtp_paged_read of a cache of E2M1 rows, its arguments checked.
+cudaError_t read_e2m1(const dmtp_paged_kv* c, const int32_t* seq, const int32_t* pos, int n_rows, void* k_out,
+                      void* v_out, uint32_t* err, cudaStream_t st);
 
 }  // namespace dmtp
 
@@ -122,6 +131,55 @@ __device__ __forceinline__ float2 h2_to_f2(uint32_t h) {
 __device__ __forceinline__ float4 e4m3x4_to_f4(uint32_t u) {
   const float2 a = h2_to_f2(e4m3x2_to_h2(u & 0xffffu)), b = h2_to_f2(e4m3x2_to_h2(u >> 16));
   return make_float4(a.x, a.y, b.x, b.y);
+}
+
+// E2M1 rows: the row's scale, as above (2688 = 6 * 448 = 1.3125 * 2^11).
+__device__ __forceinline__ int e2m1_exponent(float amax) {
+  const uint32_t u = __float_as_uint(amax);
+  if (u == 0) return 0;
+  const int e = (int)(u >> 23) - 127 - 11 + ((u & 0x7fffffu) > 0x280000u ? 1 : 0);
+  return e < -126 ? -126 : e;
+}
+// Byte of a page at which the block scales begin.
+__device__ __forceinline__ int64_t e2m1_blocks(const PageMap& m) {
+  return (int64_t)m.n_kv_heads * m.page_size * (m.head_dim / 2);
+}
+__device__ __forceinline__ uint32_t e4m3_byte(float x) {
+  return __nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
+}
+// Eight values (larger ones saturate) as E2M1, the first in the lowest bits.
+__device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
+  uint32_t r;
+  asm("{.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};}"
+      : "=r"(r)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  return r;
+}
+// Eight E2M1 values as pairs of exact halves, in order.
+__device__ __forceinline__ void e2m1x8_to_h2(uint32_t u, uint32_t (&h)[4]) {
+  asm("{.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(u));
+}
+__device__ __forceinline__ void e2m1x8_to_f8(uint32_t u, float (&f)[8]) {
+  uint32_t h[4];
+  e2m1x8_to_h2(u, h);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = h2_to_f2(h[i]);
+    f[2 * i] = x.x;
+    f[2 * i + 1] = x.y;
+  }
 }
 
 // Eight consecutive values as they lie in memory; `wide`: at a 16-byte boundary (else fp32 at
@@ -204,6 +262,25 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// tanh(y) to about 3e-7 of its value: near 0 y + y^3 P(y^2), P fitted to the least largest
+// relative error (4e-9) on |y| <= 0.625; further out 1 - 2 / (1 + e^2y), whose error of 2e-7 is no
+// longer large beside it.
+__device__ __forceinline__ float soft_tanh(float y) {
+  const float t = y * y;
+  float p = fmaf(t, -0.005704984068870544f, 0.0206390842795372f);
+  p = fmaf(t, p, -0.05373971536755562f);
+  p = fmaf(t, p, 0.13331441581249237f);
+  p = fmaf(t, p, -0.3333328068256378f);
+  const float near = fmaf(y * t, p, y);
+  const float far = fmaf(-2.f, rcp(1.f + ex2(y * 2.8853900817779268f)), 1.f);
+  return fabsf(y) <= 0.625f ? near : far;
 }
 
 // Two floats in one register pair: Blackwell's packed single-precision instructions, which halve

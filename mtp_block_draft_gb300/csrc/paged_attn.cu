@@ -96,7 +96,7 @@ int plan(const dmtp_paged_kv* c, const dmtp_paged_query* a, PagedPlan* pl) {
   pl->tc = c->dtype == 1 && (hd == 64 || hd == 128);
   if (pl->tc) {
     pl->qn = nq <= 8 ? 8 : nq <= 16 ? 16 : nq <= 32 ? 32 : 64;
-    pl->grid = paged_tc_grid(hd, c->e4m3 != 0, pl->qn);
+    pl->grid = paged_tc_grid(hd, rows_of(*c), pl->qn);
   } else {
     pl->qn = 8;
     pl->grid = paged_simt_grid(hd);
@@ -135,8 +135,15 @@ extern "C" int dmtp_paged_attention_workspace(const dmtp_paged_kv* c, const dmtp
 
 extern "C" int dmtp_paged_attention(const dmtp_paged_kv* c, const dmtp_paged_query* a, void* workspace,
                                     size_t ws_bytes, uint32_t* err, void* stream) {
+  return dmtp_paged_attention_scores(c, a, nullptr, workspace, ws_bytes, err, stream);
+}
+
+extern "C" int dmtp_paged_attention_scores(const dmtp_paged_kv* c, const dmtp_paged_query* a,
+                                           const dmtp_paged_scores* s, void* workspace, size_t ws_bytes,
+                                           uint32_t* err, void* stream) {
   const int e = check_query(c, a);
   if (e) return e;
+  if (s && !scores_ok(*s)) return DMTP_EINVAL;
   const int es = c->dtype ? 2 : 4, hd = c->head_dim;
   if (!a->q || !a->out || !a->kv_len) return DMTP_EINVAL;
   if (!aligned_to(a->q, 16) || !aligned_to(a->out, 16) || !aligned_to(a->kv_len, 4) ||
@@ -172,9 +179,13 @@ extern "C" int dmtp_paged_attention(const dmtp_paged_kv* c, const dmtp_paged_que
   p.part_ml = (float2*)((char*)workspace + pl.part_ml);
   p.note = pl.whole ? nullptr : (PagedNote*)((char*)workspace + pl.note);
   p.scale2 = a->scale * 1.4426950408889634f;
+  p.capl = s ? s->cap * 1.4426950408889634f : 0.f;
+  p.cap_inv = p.capl > 0.f ? 1.f / p.capl : 0.f;
+  p.slopes = s ? s->slopes : nullptr;
+  const bool mod = p.capl > 0.f || p.slopes;
   cudaStream_t st = (cudaStream_t)stream;
-  cudaError_t le = pl.tc ? paged_attn_tc(p, pl, c->e4m3 != 0, st)
-                         : paged_attn_simt(p, pl, c->dtype, c->e4m3 != 0, st);
+  cudaError_t le = pl.tc ? paged_attn_tc(p, pl, rows_of(*c), mod, st)
+                         : paged_attn_simt(p, pl, c->dtype, rows_of(*c), mod, st);
   if (le == cudaSuccess && !pl.whole) {
     const int nq = p.nq < pl.qn ? p.nq : pl.qn, units = p.units * c->n_seqs;
     // A CTA's 16 warps go by the pieces that a unit has on average, and one more: all to one query

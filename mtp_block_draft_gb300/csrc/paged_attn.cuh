@@ -44,6 +44,8 @@ struct PagedAttn {
   float2* part_ml;                   // [G][2][qn] (max in base 2, sum)
   PagedNote* note;                   // [n_seqs units]; null: whole units
   float scale2;                      // scale log2(e)
+  float capl, cap_inv;               // cap log2(e) (0: scores are not capped), and 1 / that
+  const float* slopes;               // null: no bias
 };
 
 // Length of sequence b inside the table's reach.
@@ -183,6 +185,10 @@ __device__ __forceinline__ int queries_of(const PagedAttn& p, int unit) {
   return left < p.qn ? left : p.qn;
 }
 
+inline bool scores_ok(const dmtp_paged_scores& s) {
+  return (s.cap == 0.f || (s.cap >= 1e-30f && s.cap <= 1e30f)) && aligned_to(s.slopes, 4);
+}
+
 // Which kernel takes a call: the tensor cores (paged_attn_tc.cu) or the CUDA cores
 // (paged_attn_simt.cu), with tiles of 64 keys.
 struct PagedPlan {
@@ -190,9 +196,13 @@ struct PagedPlan {
   int qn, chunks, grid;
   size_t part_o, part_ml, note, bytes;  // workspace offsets
 };
-cudaError_t paged_attn_tc(const PagedAttn& p, const PagedPlan& pl, bool e8, cudaStream_t st);
-cudaError_t paged_attn_simt(const PagedAttn& p, const PagedPlan& pl, int dtype, bool e8, cudaStream_t st);
-int paged_tc_grid(int head_dim, bool e8, int qn);
+cudaError_t paged_attn_tc(const PagedAttn& p, const PagedPlan& pl, Rows f, bool mod, cudaStream_t st);
+cudaError_t paged_attn_tc_e2m1(const PagedAttn& p, int grid, cudaStream_t st);
+cudaError_t paged_attn_tc_scores(const PagedAttn& p, int grid, Rows f, cudaStream_t st);
+cudaError_t paged_attn_tc_e2m1_scores(const PagedAttn& p, int grid, cudaStream_t st);
+cudaError_t paged_attn_simt(const PagedAttn& p, const PagedPlan& pl, int dtype, Rows f, bool mod, cudaStream_t st);
+cudaError_t paged_attn_simt_scores(const PagedAttn& p, int grid, int dtype, Rows f, cudaStream_t st);
+int paged_tc_grid(int head_dim, Rows f, int qn);
 int paged_simt_grid(int head_dim);
 
 }  // namespace dmtp

@@ -6,34 +6,14 @@
 // bytes moved are the rows once in and once out; nothing else is read but the positions.
 // 8188 rows of 32 + 2 x 4 heads of 128 into bf16 pages take 31.8 us (167 MB, 0.78 of the copy
 // rate, two thirds of the issue slots used); 32 rows into E4M3 pages 3.0 us, which is latency.
-//
-// Angles. Position p turns pair i by p f_i turns, f_i = theta^(-2i/hd) / 2 pi < 1. The host
-// forms f_i in double and passes f_i 2^64 as an integer; p times that, modulo 2^64, is the angle's
-// fraction of a turn in fixed point, which loses nothing more at far positions and needs none of
-// the GPU's slow double arithmetic. What is left is f_i's own error: its power is off by
-// (ln(theta) 2i/hd + 4) 2^-53 of itself at most, in turns less than 2^-53, so p 2^-53 at
-// position p. The fraction goes to the sine as a 24-bit value and a first-order correction for the rest.
 #include <math.h>
 
 #include <cuda_fp16.h>
 
 #include "paged.cuh"
+#include "paged_rope.cuh"
 
 namespace {
-
-struct Turns {
-  unsigned long long f[DMTP_OPS_MAX_HEAD_DIM / 2];
-};
-
-__device__ __forceinline__ float2 cos_sin_turns(unsigned long long frac) {
-  const int hi = (int)(frac >> 32);                       // signed: [-1/2, 1/2) turns
-  const float xh = __int2float_rn(hi);
-  const long long rest = (long long)(frac - ((unsigned long long)(long long)xh << 32));
-  const float d = __ll2float_rn(rest) * 3.4061215800304e-19f;  // 2 pi 2^-64
-  float s, c;
-  sincospif(xh * 4.656612873077393e-10f, &s, &c);          // 2 * 2^-32 half turns
-  return make_float2(fmaf(-s, d, c), fmaf(c, d, s));
-}
 
 struct WriteArgs {
   PageMap m;
@@ -245,7 +225,8 @@ namespace dmtp {
 
 int check_cache(const dmtp_paged_kv* c) {
   if (!c || !c->k || !c->v || !c->table) return DMTP_EINVAL;
-  if ((c->dtype != 0 && c->dtype != 1) || (c->e4m3 != 0 && c->e4m3 != 1)) return DMTP_EINVAL;
+  if ((c->dtype != 0 && c->dtype != 1) || (c->e4m3 != 0 && c->e4m3 != 1 && c->e4m3 != DMTP_OPS_E2M1))
+    return DMTP_EINVAL;
   if (c->e4m3 && (!c->k_scale || !c->v_scale)) return DMTP_EINVAL;
   if (c->head_dim < 16 || c->head_dim > DMTP_OPS_MAX_HEAD_DIM || c->head_dim % 16) return DMTP_EINVAL;
   if (c->n_pages < 1 || c->n_kv_heads < 1 || c->n_kv_heads > 4096 || c->n_seqs < 1 || c->max_blocks < 1)
@@ -254,7 +235,9 @@ int check_cache(const dmtp_paged_kv* c) {
   if ((int64_t)c->max_blocks * c->page_size >= (1ll << 31) - 65536) return DMTP_EINVAL;
   const int64_t lines = (int64_t)c->n_kv_heads * c->page_size;
   const int es = c->e4m3 ? 1 : c->dtype ? 2 : 4;
-  if (c->page_stride < lines * c->head_dim || !mult(c->page_stride * es, 16)) return DMTP_EINVAL;
+  const int64_t values = lines * c->head_dim;
+  if (c->page_stride < (c->e4m3 == DMTP_OPS_E2M1 ? values / 16 * 9 : values) || !mult(c->page_stride * es, 16))
+    return DMTP_EINVAL;
   if (c->e4m3 && c->scale_stride < lines) return DMTP_EINVAL;
   if (c->table_stride < c->max_blocks) return DMTP_EINVAL;
   if (!aligned_to(c->k, 16) || !aligned_to(c->v, 16)) return DMTP_EINVAL;
@@ -294,6 +277,7 @@ extern "C" int dmtp_paged_write(const dmtp_paged_kv* c, const dmtp_paged_rows* r
                                 void* stream) {
   int e = check_cache(c);
   if (e) return e;
+  if (c->e4m3 == DMTP_OPS_E2M1) return dmtp_paged_write_rope(c, r, nullptr, err, stream);
   if (!r || r->n_rows < 0) return DMTP_EINVAL;
   if (r->n_rows == 0) return DMTP_OK;
   const int es = c->dtype ? 2 : 4, hd = c->head_dim;
@@ -356,6 +340,10 @@ extern "C" int dmtp_paged_read(const dmtp_paged_kv* c, const int32_t* seq, const
       !aligned_to(k_out, 16) || !aligned_to(v_out, 16) || (err && !aligned_to(err, 4)))
     return DMTP_EINVAL;
   if (cudaPeekAtLastError() != cudaSuccess) return DMTP_ECUDA;
+  if (c->e4m3 == DMTP_OPS_E2M1)
+    return read_e2m1(c, seq, pos, n_rows, k_out, v_out, err, (cudaStream_t)stream) == cudaSuccess
+               ? DMTP_OK
+               : (cudaGetLastError(), DMTP_ECUDA);
   ReadArgs a;
   a.m = page_map(*c);
   a.k = c->k;

@@ -52,6 +52,7 @@ extern "C" {
 
 /* bits of the operators' error word */
 #define DMTP_OPS_ERR_POS 2u   /* a position or length outside the block table's reach */
+#define DMTP_OPS_ERR_WAIT 4u  /* a wait inside a kernel gave up: its results are not there */
 #define DMTP_OPS_ERR_PAGE 16u /* a block table entry outside [0, n_pages)             */
 #define DMTP_OPS_ERR_SEQ 32u  /* a sequence index >= n_seqs                           */
 #define DMTP_OPS_ERR_ROWS 64u /* a sequence's rows that are none of the call's        */

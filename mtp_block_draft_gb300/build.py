@@ -22,7 +22,7 @@ SOURCES = ["dmtp.cu", "elementwise.cu", "attention.cu", "gemm_simt.cu", "gemm_tc
            "paged_kv.cu", "paged_rows.cu", "paged_attn.cu", "paged_attn_simt.cu",
            "paged_attn_simt_scores.cu", "paged_attn_tc.cu", "paged_attn_tc_scores.cu",
            "paged_attn_tc_e2m1.cu", "paged_attn_tc_e2m1_scores.cu", "paged_prompt.cu",
-           "paged_prompt_simt.cu",
+           "paged_prompt_simt.cu", "paged_prompt_tc.cu", "paged_prompt_tc_scaled.cu",
            "norm_e4m3.cu", "sample.cu"]
 # host-only units whose double arithmetic must round the same on every host: no fused
 # multiply-adds (aarch64 compilers contract them by default)

@@ -54,14 +54,14 @@ int check_prompt(const dmtp_paged_kv* c, const dmtp_paged_prompt* a) {
 
 int plan(const dmtp_paged_kv* c, const dmtp_paged_prompt* a, PromptPlan* pl) {
   const int64_t nq = (int64_t)a->n_rows * (a->n_heads / c->n_kv_heads);
-  pl->tc = false;
-  pl->tile = 64;
+  pl->tc = c->dtype == 1 && c->head_dim <= 128;
+  pl->tile = pl->tc ? 256 : 64;
   const int64_t tiles = nq / pl->tile + (c->n_seqs < a->n_rows ? c->n_seqs : a->n_rows);
   const int64_t units = tiles * c->n_kv_heads, reach = (int64_t)c->max_blocks * c->page_size;
   if (tiles >= (1ll << 31)) return DMTP_EINVAL;
   pl->tiles = (int)tiles;
-  int64_t s = units ? 304 / units : 1;
-  const int64_t most = reach / 256;
+  int64_t s = units ? (pl->tc ? 152 : 304) / units : 1;
+  const int64_t most = reach / 512;
   s = s > most ? most : s;
   pl->splits = s < 1 ? 1 : s > 64 ? 64 : (int)s;
   pl->part_o = pl->part_ml = pl->bytes = 0;
@@ -125,7 +125,8 @@ extern "C" int dmtp_paged_prompt_attention(const dmtp_paged_kv* c, const dmtp_pa
   p.part_o = (float*)((char*)workspace + pl.part_o);
   p.part_ml = (float2*)((char*)workspace + pl.part_ml);
   cudaStream_t st = (cudaStream_t)stream;
-  cudaError_t le = paged_prompt_simt(p, pl, c->dtype, rows_of(*c), st);
+  const bool mod = p.capl > 0.f || a->scores.slopes;
+  cudaError_t le = pl.tc ? paged_prompt_tc(p, pl, rows_of(*c), mod, st) : paged_prompt_simt(p, pl, c->dtype, rows_of(*c), st);
   if (le == cudaSuccess && pl.splits > 1) {
     const dim3 grid(pl.tiles, c->n_kv_heads, pl.tile / 8);
     le = launch_op(c->dtype ? k_prompt_merge<bf16> : k_prompt_merge<float>, grid, 256, 0, st, true, 1, p);

@@ -33,6 +33,8 @@ struct PromptPlan {
   int tile, tiles, splits;  // queries of a tile; tiles at most
   size_t part_o, part_ml, bytes;
 };
+cudaError_t paged_prompt_tc(const PagedPrompt& p, const PromptPlan& pl, Rows f, bool mod, cudaStream_t st);
+cudaError_t paged_prompt_tc_scaled(const PagedPrompt& p, const PromptPlan& pl, Rows f, bool mod, cudaStream_t st);
 cudaError_t paged_prompt_simt(const PagedPrompt& p, const PromptPlan& pl, int dtype, Rows f, cudaStream_t st);
 
 // A tile: `count` queries from query q0 on of sequence b, whose rows are row0 .. row0 + n - 1 of the
@@ -99,6 +101,31 @@ __device__ __forceinline__ PromptQuery prompt_query(const PagedPrompt& p, const 
   if (p.a.window > 0 && q.pos >= p.a.window) q.lo = max(q.lo, q.pos - p.a.window + 1);
   q.hi = min(p.a.end ? __ldg(p.a.end + q.row) : q.pos + 1, w.len);
   return q;
+}
+
+// Eight columns of a cached row as fp32: of row `line` of a page, times s (rows with scales).
+template <typename T, Rows F>
+__device__ __forceinline__ void load8(const PagedPrompt& p, const void* base, int64_t page, int64_t line, int c, float s,
+                                      float (&f)[8]) {
+  const int hd = p.m.head_dim;
+  if constexpr (F == kRaw) {
+    Raw<T> r;
+    const T* src = (const T*)base + page * p.m.page_stride + line * hd + c;
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(T) / 2); ++i) r.u[i] = __ldg(reinterpret_cast<const uint4*>(src) + i);
+    values(r, f);
+  } else if constexpr (F == kE4M3) {
+    const uint2 u = __ldg(reinterpret_cast<const uint2*>((const uint8_t*)base + page * p.m.page_stride + line * hd + c));
+    const float4 a = e4m3x4_to_f4(u.x), b = e4m3x4_to_f4(u.y);
+    f[0] = a.x * s, f[1] = a.y * s, f[2] = a.z * s, f[3] = a.w * s;
+    f[4] = b.x * s, f[5] = b.y * s, f[6] = b.z * s, f[7] = b.w * s;
+  } else {
+    const uint8_t* pg = (const uint8_t*)base + page * p.m.page_stride;
+    e2m1x8_to_f8(__ldg(reinterpret_cast<const uint32_t*>(pg + line * (hd / 2) + c / 2)), f);
+    const float b = h2_to_f2(e4m3x2_to_h2(__ldg(pg + e2m1_blocks(p.m) + line * (hd / 16) + c / 16))).x;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = f[e] * b * s;
+  }
 }
 
 }  // namespace dmtp

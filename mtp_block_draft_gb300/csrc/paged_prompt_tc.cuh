@@ -1,0 +1,649 @@
+// Attention of many rows over a paged cache on the 5th-generation tensor cores: bf16 rows of head
+// sizes up to 128.
+//
+// A CTA has a unit: 256 queries of one kv head as two halves of 128, and goes through its keys 128 at a
+// time. Per block of keys and half
+//   S = Q K^T   tcgen05, M = 128 queries, N = 128 keys; Q and K from shared memory
+//   softmax     a warpgroup, a thread a query: P = 2^(s - m) as bf16 over S's place in TMEM
+//   O += P V    tcgen05, A = P from TMEM, B = V as its rows lie (keys by columns, MN-major)
+// S and O of both halves fill TMEM's 512 columns; while one half's softmax runs, the tensor cores
+// work for the other. The reference m of a query moves only when a score passes it by 2^8, so that O
+// is hardly ever rescaled. Loader warps bring K and V (of E4M3 and E2M1 rows as bf16) into a ring of
+// shared-memory slots by the page, row for row, which leaves page sizes and strides free; one
+// thread issues the products.
+//
+// A row may see any interval of positions: a block that not every query of a warp sees whole is
+// masked there. In such a block a weight is 0 where a value may be infinite or NaN, and the tensor
+// cores' 0 * inf would reach rows that do not see it: the loader looks through those blocks' values,
+// and a unit with one that is not finite, or with a page that is none, is computed again row by row.
+#pragma once
+
+#include "paged_prompt.cuh"
+
+using namespace dmtp;
+
+namespace {
+
+constexpr int kTile = 256, kKeys = 128;
+
+template <int HD, Rows F>
+struct Shape {
+  static constexpr int LW = F == kRaw ? 4 : 8;               // loader warps
+  static constexpr int kThreads = 32 * (8 + LW + 1);
+  static constexpr uint32_t kSlot = kKeys * HD * 2;          // 128 rows of K or V
+  static constexpr int NS = HD == 64 ? 8 : F == kRaw ? 5 : 4;
+  static constexpr uint32_t kQ = 2 * 128 * HD * 2;
+  static constexpr uint32_t kHead = 512 + (LW / 4) * kKeys * 8;
+  static constexpr uint32_t kSmem = kHead + 1024 + kQ + NS * kSlot;
+  static_assert(kSmem <= 232448, "shared memory");
+};
+
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// byte offset of the 16-byte chunk c (0..7) of row r inside a 128-byte-swizzled block
+__device__ __forceinline__ uint32_t sw128(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
+// D[tmem] (+)= A[tmem] B[smem], bf16, fp32 accumulate.
+__device__ __forceinline__ void umma_bf16_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// V as its rows lie: 64 columns (128 bytes) of 8 keys are a swizzled kilobyte, the next 8 keys
+// follow, the next 64 columns are kKeys rows further.
+__device__ __forceinline__ uint64_t umma_desc_mn(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(kKeys * 128 >> 4) << 16;  // leading byte offset: along the columns
+  d |= (uint64_t)(1024 >> 4) << 32;         // stride byte offset: along the keys
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+// 32 columns of this warp's 32 lanes, without a wait.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));  // no use moves above the wait
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ bool odd_pair(uint32_t u) {  // an infinity or NaN among two bf16
+  return (u & 0x7f80u) == 0x7f80u || (u & 0x7f800000u) == 0x7f800000u;
+}
+// Output columns d .. d + 3 of query t of a tile: final, or a part of a split unit.
+__device__ __forceinline__ bf16* out_row(const PagedPrompt& p, const PromptTile& w, int kvh, int t) {
+  const int r = (w.q0 + t) / p.group, head = kvh * p.group + (w.q0 + t - r * p.group);
+  return (bf16*)p.a.out + (int64_t)(w.row0 + r) * p.a.o_row + (int64_t)head * p.a.o_head;
+}
+
+// The queries of a unit over the positions [j_lo, j_hi), row by row on the CUDA cores: a warp takes a
+// query, a lane a key of 32 and then eight columns.
+template <Rows F>
+__device__ __noinline__ void row_by_row(const PagedPrompt& p, const PromptTile& w, int kvh, int j_lo, int j_hi,
+                                        int64_t part, int warps) {
+  const int lane = threadIdx.x & 31, hd = p.m.head_dim;
+  for (int t = threadIdx.x >> 5; t < w.count; t += warps) {
+    const PromptQuery q = prompt_query(p, w, t);
+    const int head = kvh * p.group + q.head;
+    const bf16* src = (const bf16*)p.a.q + (int64_t)q.row * p.a.q_row + (int64_t)head * p.a.q_head;
+    const float slope = p.a.scores.slopes ? __ldg(p.a.scores.slopes + head) * 1.4426950408889634f : 0.f;
+    float m = -INFINITY, l = 0.f, o[8] = {};
+    const int last = min(q.hi, j_hi);
+    for (int j0 = max(q.lo, j_lo); j0 < last; j0 += 32) {
+      const int j = j0 + lane;
+      int page = -1, off = 0;
+      if (j < last) page = page_of(p.m, w.b, j, off, p.err);
+      const int64_t line = (int64_t)kvh * p.m.page_size + off;
+      float x = -INFINITY;
+      if (page >= 0) {
+        const float s = F == kRaw ? 1.f : __ldg(p.ks + (int64_t)page * p.m.scale_stride + line);
+        x = 0.f;
+        for (int c = 0; c < hd; c += 8) {
+          float k[8], a[8];
+          load8<bf16, F>(p, p.k, page, line, c, s, k);
+          Raw<bf16> raw;
+          raw.u[0] = __ldg(reinterpret_cast<const uint4*>(src + c));
+          values(raw, a);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x = fmaf(a[e], k[e], x);
+        }
+        x *= p.scale2;
+        if (p.capl > 0.f) x = p.capl * soft_tanh(x * p.cap_inv);
+        x = fmaf(-slope, (float)abs(q.pos - j), x);
+      }
+      const float n = fmaxf(m, warp_max(x)), ref = n == -INFINITY ? 0.f : n, fix = ex2(m - ref);
+      m = n;
+      const float weight = ex2(x - ref);
+      l = l * fix + weight;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] *= fix;
+      for (int k = 0; k < 32; ++k) {
+        const float a = __shfl_sync(0xffffffffu, weight, k);
+        const int pg = __shfl_sync(0xffffffffu, page, k);
+        const int64_t ln = __shfl_sync(0xffffffffu, line, k);
+        if (a != 0.f && pg >= 0 && 8 * lane < hd) {
+          float v[8];
+          load8<bf16, F>(p, p.v, pg, ln, 8 * lane, F == kRaw ? 1.f : __ldg(p.vs + (int64_t)pg * p.m.scale_stride + ln), v);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[e] = fmaf(a, v[e], o[e]);
+        }
+      }
+    }
+    l = warp_sum(l);
+    if (8 * lane < hd) {
+      if (p.splits > 1) {
+        float* to = p.part_o + (part + t) * hd + 8 * lane;
+        *reinterpret_cast<float4*>(to) = make_float4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<float4*>(to + 4) = make_float4(o[4], o[5], o[6], o[7]);
+      } else {
+        const float inv = l != 0.f ? 1.f / l : 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] *= inv;
+        store8(out_row(p, w, kvh, t) + 8 * lane, true, o);
+      }
+    }
+    if (p.splits > 1 && lane == 0) p.part_ml[part + t] = make_float2(m, l);
+  }
+}
+
+// What a thread of the softmax knows of its query.
+struct Query {
+  int lo, hi, pos;
+  float slope, m, l;
+};
+// Scores of 32 keys from j on, in base 2. BIAS scores of MOD kernels; seen: every one is.
+template <bool MOD>
+__device__ __forceinline__ void scores32(const PagedPrompt& p, const Query& q, uint32_t (&r)[32], int j, bool edge) {
+  const float scale = fabsf(p.scale2);
+  if (MOD && p.capl > 0.f) {
+    const float by = scale * p.cap_inv;
+#pragma unroll
+    for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(p.capl * soft_tanh(__uint_as_float(r[e]) * by));
+  } else {
+    const f32x2 by = both(scale);
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+      const float2 v = unpack(mul2(pack(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), by));
+      r[e] = __float_as_uint(v.x);
+      r[e + 1] = __float_as_uint(v.y);
+    }
+  }
+  if (MOD) {
+    const float d = (float)(q.pos - j);
+#pragma unroll
+    for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(fmaf(-q.slope, fabsf(d - (float)e), __uint_as_float(r[e])));
+  }
+  if (edge) {
+    const int from = q.lo - j;
+    const unsigned n = q.hi > q.lo ? q.hi - q.lo : 0;
+#pragma unroll
+    for (int e = 0; e < 32; ++e) r[e] = (unsigned)(e - from) < n ? r[e] : 0xff800000u;
+  }
+}
+
+template <int HD, Rows F, bool MOD>
+__global__ void __launch_bounds__(Shape<HD, F>::kThreads, 1) k_prompt_tc(const PagedPrompt p) {
+  using Sh = Shape<HD, F>;
+  constexpr int NS = Sh::NS, LW = Sh::LW, DB = HD / 64;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, kvh = blockIdx.y, hd = p.m.head_dim;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && warp == 0) prompt_report(p);
+  PromptTile w;
+  if (!prompt_tile(p, blockIdx.x, w)) {
+    pdl_trigger();
+    return;
+  }
+  uint64_t* full = (uint64_t*)smem;  // [NS] a slot's rows are there
+  uint64_t* empty = full + NS;       // [NS] the products have read it
+  uint64_t* s_full = empty + NS;     // [2] a half's scores
+  uint64_t* p_full = s_full + 2;     // [2] its weights
+  uint64_t* o_full = p_full + 2;     // [2] its last product
+  uint32_t* tmem_slot = (uint32_t*)(o_full + 2);
+  int* s_span = (int*)(tmem_slot + 1);  // [4] least lo, largest hi; largest lo, least hi (what every query sees)
+  int* s_odd = s_span + 4;              // the unit has to be computed row by row
+  int2* s_row = (int2*)(smem + 512);    // [LW / 4][kKeys] page (-1: not there) and row in it
+  unsigned char* sQ = smem + Sh::kHead;
+  sQ += (1024 - (smem_u32(sQ) & 1023)) & 1023;
+  unsigned char* ring = sQ + Sh::kQ;
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(smem_u32(full + i), 128);
+      mbar_init(smem_u32(empty + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(s_full + i), 1);
+      mbar_init(smem_u32(p_full + i), 128);
+      mbar_init(smem_u32(o_full + i), 1);
+    }
+    fence_mbar_init();
+    s_span[0] = s_span[3] = 0x7fffffff;
+    s_span[1] = s_span[2] = 0;
+    *s_odd = 0;
+  }
+  if (warp == 8 + LW) tmem_alloc(smem_u32(tmem_slot), 512);
+  __syncthreads();
+  pdl_trigger();
+  // ---- the queries: their spans, and their rows as an operand of two halves ----
+  Query q;
+  q.lo = q.hi = q.pos = 0;
+  q.slope = q.l = 0.f;
+  q.m = -INFINITY;
+  if (warp < 8) {
+    int least = 0x7fffffff, most = 0, late = 0, early = 0x7fffffff;
+    if (tid < w.count) {
+      const PromptQuery x = prompt_query(p, w, tid);
+      q.lo = x.lo;
+      q.hi = x.hi;
+      q.pos = x.pos;
+      if (MOD && p.a.scores.slopes) q.slope = __ldg(p.a.scores.slopes + kvh * p.group + x.head) * 1.4426950408889634f;
+      late = x.lo < x.hi ? x.lo : 0x7fffffff;  // (a row that sees nothing: no block is seen whole)
+      early = x.hi;
+      if (x.lo < x.hi) {
+        least = x.lo;
+        most = x.hi;
+      }
+    }
+    least = __reduce_min_sync(0xffffffffu, least);
+    most = __reduce_max_sync(0xffffffffu, most);
+    late = __reduce_max_sync(0xffffffffu, late);
+    early = __reduce_min_sync(0xffffffffu, early);
+    if (lane == 0) {
+      atomicMin(s_span, least);
+      atomicMax(s_span + 1, most);
+      atomicMax(s_span + 2, late);
+      atomicMin(s_span + 3, early);
+    }
+  }
+  {
+    const uint32_t flip = p.scale2 < 0.f ? 0x80008000u : 0u;  // (the softmax takes |scale|)
+    const int cpr = hd / 8;
+    for (int i = tid; i < kTile * cpr; i += Sh::kThreads) {
+      const int t = i / cpr, c = i - t * cpr;
+      uint4 u = make_uint4(0, 0, 0, 0);
+      if (t < w.count) {
+        const int r = (w.q0 + t) / p.group, head = kvh * p.group + (w.q0 + t - r * p.group);
+        u = __ldg(reinterpret_cast<const uint4*>((const bf16*)p.a.q + (int64_t)(w.row0 + r) * p.a.q_row +
+                                                 (int64_t)head * p.a.q_head) + c);
+      }
+      u = make_uint4(u.x ^ flip, u.y ^ flip, u.z ^ flip, u.w ^ flip);
+      *reinterpret_cast<uint4*>(sQ + (t >> 7) * (128 * HD * 2) + (c >> 3) * 16384 + sw128(t & 127, c & 7)) = u;
+    }
+  }
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int least = s_span[0], most = s_span[1], late = s_span[2], early = s_span[3];
+  const int j_first = least < most ? least / kKeys : 0;
+  const int blocks = least < most ? (most + kKeys - 1) / kKeys - j_first : 0;
+  const int t0 = (int)((int64_t)blocks * blockIdx.z / p.splits), nt = (int)((int64_t)blocks * (blockIdx.z + 1) / p.splits) - t0;
+  const int j_begin = (j_first + t0) * kKeys;
+  bool ok = true;
+
+  if (warp >= 8 && warp < 8 + LW) {
+    // ---------------- loaders ----------------
+    const int lt = tid & 127, wg = (warp - 8) >> 2;  // with two warpgroups one brings K, the other V
+    int2* rows = s_row + wg * kKeys;
+    bool odd = false;
+    auto look_up = [&](int t) {  // the rows of block t
+      const int j = j_begin + t * kKeys + lt;
+      int off = 0, page = -1;
+      if (j >= least && j < most) {
+        page = page_of(p.m, w.b, j, off, p.err);
+        odd = odd || page < 0;
+      }
+      rows[lt] = make_int2(page, off);
+    };
+    auto sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory"); };
+    auto whole = [&](int t) {  // every query sees all of block t
+      const int j = j_begin + t * kKeys;
+      return j >= late && j + kKeys <= early;
+    };
+    if constexpr (F == kRaw) {
+      constexpr int CPR = HD / 8, RPP = 128 / CPR;  // 16-byte chunks of a row, rows of a pass
+      const int c = lt % CPR, r0 = lt / CPR;
+      const bool on = 8 * c < hd;
+      int waiting = -1;  // number of the copy that is not yet announced
+      auto announce = [&]() {
+        const int n = waiting;
+        if (n & 1 && !whole(n >> 1) && on) {  // values that not every query sees
+          const unsigned char* slot = ring + (n % NS) * Sh::kSlot + (c >> 3) * 16384;
+#pragma unroll 4
+          for (int i = 0; i < kKeys / RPP; ++i) {
+            const uint4 u = *reinterpret_cast<const uint4*>(slot + sw128(r0 + i * RPP, c & 7));
+            odd = odd || odd_pair(u.x) || odd_pair(u.y) || odd_pair(u.z) || odd_pair(u.w);
+          }
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(smem_u32(full + n % NS));
+      };
+      // (a thread whose wait gave up still takes part in the barriers, and does nothing else)
+      for (int n = 0; n < 2 * nt; ++n) {
+        const int slot = n % NS;
+        const uint32_t gate = smem_u32(empty + slot), parity = ((n / NS) & 1) ^ 1;
+        if (ok && waiting >= 0 && !mbar_try_wait(gate, parity)) {
+          cp_async_wait<0>();
+          announce();
+          waiting = -1;
+        }
+        if (ok) ok = mbar_wait(gate, parity, p.err);
+        if (!(n & 1)) {
+          sync();  // the last block's rows have been read
+          look_up(n >> 1);
+          sync();
+        }
+        if (ok && on) {
+          const uint32_t to = smem_u32(ring + slot * Sh::kSlot + (c >> 3) * 16384);
+          const bf16* base = (const bf16*)((n & 1) ? p.v : p.k) + 8 * c;
+#pragma unroll 4
+          for (int i = 0; i < kKeys / RPP; ++i) {
+            const int r = r0 + i * RPP;
+            const int2 at = rows[r];
+            const int64_t line = (int64_t)kvh * p.m.page_size + at.y;
+            cp_async16(to + sw128(r, c & 7), at.x < 0 ? base : base + (int64_t)at.x * p.m.page_stride + line * hd,
+                       at.x < 0 ? 0 : 16);
+          }
+        }
+        cp_async_commit();
+        if (ok && waiting >= 0) {
+          cp_async_wait<1>();
+          announce();
+        }
+        waiting = n;
+      }
+      cp_async_wait<0>();
+      if (ok && waiting >= 0) announce();
+    } else {
+      // 16 columns of a row a thread: their bytes, the block's scale and the row's are asked for before
+      // the slot is free, and become bf16 on their way into it
+      constexpr int CPR = HD / 16, RPP = 128 / CPR, N = kKeys / RPP;
+      const int c = lt % CPR, r0 = lt / CPR;
+      const bool on = 16 * c < hd;
+      const unsigned char* base = (const unsigned char*)(wg ? p.v : p.k);
+      const float* scales = wg ? p.vs : p.ks;
+      const int64_t blk = F == kE2M1 ? e2m1_blocks(p.m) : 0;
+      for (int t = 0; t < nt; ++t) {
+        const int n = 2 * t + wg, slot = n % NS;
+        sync();
+        look_up(t);
+        sync();
+        uint4 u[N];
+        float s[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const int2 at = rows[r0 + i * RPP];
+          u[i] = make_uint4(0, 0, 0, 0);
+          s[i] = 0.f;
+          if (on && at.x >= 0) {
+            const int64_t line = (int64_t)kvh * p.m.page_size + at.y;
+            const unsigned char* pg = base + (int64_t)at.x * p.m.page_stride;
+            s[i] = __ldg(scales + (int64_t)at.x * p.m.scale_stride + line);
+            if (F == kE4M3) {
+              u[i] = __ldg(reinterpret_cast<const uint4*>(pg + line * hd) + c);
+            } else {
+              const uint2 v = __ldg(reinterpret_cast<const uint2*>(pg + line * (hd / 2)) + c);
+              u[i] = make_uint4(v.x, v.y, __ldg(pg + blk + line * (hd / 16) + c), 0);
+            }
+          }
+        }
+        if (ok) ok = mbar_wait(smem_u32(empty + slot), ((n / NS) & 1) ^ 1, p.err);
+        if (ok && on) {
+          unsigned char* to = ring + slot * Sh::kSlot + (c >> 2) * 16384;
+          const bool look = wg && !whole(t);
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            float f[16];
+            if (F == kE4M3) {
+              const uint32_t x[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float4 v = e4m3x4_to_f4(x[e]);
+                f[4 * e] = v.x * s[i], f[4 * e + 1] = v.y * s[i], f[4 * e + 2] = v.z * s[i], f[4 * e + 3] = v.w * s[i];
+              }
+            } else {
+              const float b = h2_to_f2(e4m3x2_to_h2(u[i].z)).x * s[i];
+              float v[8];
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                e2m1x8_to_f8(h ? u[i].y : u[i].x, v);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[8 * h + e] = v[e] * b;
+              }
+            }
+            uint32_t x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = pack_bf16(f[2 * e], f[2 * e + 1]);
+            if (look) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) odd = odd || odd_pair(x[e]);
+            }
+            const int r = r0 + i * RPP;
+            *reinterpret_cast<uint4*>(to + sw128(r, 2 * c & 7)) = make_uint4(x[0], x[1], x[2], x[3]);
+            *reinterpret_cast<uint4*>(to + sw128(r, (2 * c + 1) & 7)) = make_uint4(x[4], x[5], x[6], x[7]);
+          }
+        }
+        if (ok) {
+          fence_proxy_async_smem();
+          mbar_arrive(smem_u32(full + slot));
+        }
+      }
+    }
+    if (odd) *s_odd = 1;
+  } else if (warp == 8 + LW) {
+    // ---------------- the products ----------------
+    if (lane == 0 && nt > 0) {
+      const uint32_t id_s = umma_idesc_bf16(128, kKeys);
+      const uint32_t id_o = umma_idesc_bf16(128, hd) | 1u << 16;  // B is MN-major
+      const int ks = hd / 16;
+      auto scores = [&](int h, int t) {  // S of half h over block t
+        const unsigned char* k = ring + (2 * t % NS) * Sh::kSlot;
+        for (int i = 0; i < ks; ++i) {
+          const uint32_t at = (i >> 2) * 16384 + (i & 3) * 32;
+          umma_bf16(tmem + h * 128, umma_desc_sw128(smem_u32(sQ + h * (128 * HD * 2) + at)),
+                    umma_desc_sw128(smem_u32(k + at)), id_s, i ? 1u : 0u);
+        }
+        umma_commit(smem_u32(s_full + h));
+      };
+      auto wait_slot = [&](int n) { return mbar_wait(smem_u32(full + n % NS), (n / NS) & 1, p.err); };
+      ok = wait_slot(0);
+      if (ok) {
+        tc_fence_after();
+        scores(0, 0);
+        scores(1, 0);
+        umma_commit(smem_u32(empty));
+      }
+      for (int t = 0; t < nt && ok; ++t) {
+        const int nv = 2 * t + 1;
+        ok = wait_slot(nv);
+        const uint32_t v = smem_u32(ring + (nv % NS) * Sh::kSlot);
+        for (int h = 0; h < 2 && ok; ++h) {
+          ok = mbar_wait(smem_u32(p_full + h), t & 1, p.err);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int i = 0; i < kKeys / 16; ++i)
+            umma_bf16_ta(tmem + 256 + h * HD, tmem + h * 128 + 8 * i, umma_desc_mn(v + i * 2048), id_o, (t | i) ? 1u : 0u);
+          if (h == 1) umma_commit(smem_u32(empty + nv % NS));
+          if (t + 1 < nt) {
+            if (h == 0) {
+              ok = wait_slot(2 * t + 2);
+              if (!ok) break;
+              tc_fence_after();
+            }
+            scores(h, t + 1);
+            if (h == 1) umma_commit(smem_u32(empty + (2 * t + 2) % NS));
+          } else {
+            umma_commit(smem_u32(o_full + h));
+          }
+        }
+      }
+      if (!ok) {  // what was issued ends before TMEM is freed
+        umma_commit(smem_u32(o_full));
+        mbar_wait(smem_u32(o_full), 0, p.err);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---------------- softmax: warps 0-3 of half 0, 4-7 of half 1 ----------------
+    const int h = warp >> 2;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + h * 128 + lanes, tO = tmem + 256 + h * HD + lanes;
+    // what every query of the warp sees needs no mask
+    const bool mine = tid < w.count;
+    const int from = __reduce_max_sync(0xffffffffu, mine ? (q.lo < q.hi ? q.lo : 0x7fffffff) : 0);
+    const int to = __reduce_min_sync(0xffffffffu, mine ? q.hi : 0x7fffffff);
+    for (int t = 0; t < nt; ++t) {
+      const int j = j_begin + t * kKeys;
+      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(s_full + h), t & 1, p.err));
+      if (!ok) break;
+      tc_fence_after();
+      const bool edge = j < from || j + kKeys > to;
+      float top = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t r[32];
+        tmem_ld32(tS + 32 * c, r);
+        tmem_wait_ld(r);
+        scores32<MOD>(p, q, r, j + 32 * c, edge);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(r[e]));
+      }
+      if (t == 0) {
+        q.m = top;
+      } else if (__any_sync(0xffffffffu, top > q.m + 8.f)) {
+        const float n = top > q.m + 8.f ? top : q.m;
+        const float fix = n == q.m ? 1.f : ex2(q.m - n);  // (0 for the first)
+        q.m = n;
+        q.l *= fix;
+#pragma unroll 1
+        for (int c = 0; c < hd; c += 16) {
+          float v[16];
+          uint32_t r[16];
+          tmem_ld16(tO + c, v);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(v[e] * fix);
+          tmem_st16(tO + c, r);
+        }
+      }
+      const float ref = q.m == -INFINITY ? 0.f : q.m;
+      f32x2 sum = both(0.f);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t r[32], w16[16];
+        tmem_ld32(tS + 32 * c, r);
+        tmem_wait_ld(r);
+        scores32<MOD>(p, q, r, j + 32 * c, edge);
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          const float a = ex2(__uint_as_float(r[e]) - ref), b = ex2(__uint_as_float(r[e + 1]) - ref);
+          sum = add2(sum, pack(a, b));
+          w16[e / 2] = pack_bf16(a, b);
+        }
+        tmem_st16(tS + 16 * c, w16);
+      }
+      const float2 two = unpack(sum);
+      q.l += two.x + two.y;
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(smem_u32(p_full + h));
+    }
+    if (ok && nt > 0) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(o_full + h), 0, p.err));
+    tc_fence_after();
+  }
+  __syncthreads();
+  const int64_t part = (((int64_t)blockIdx.x * gridDim.y + kvh) * p.splits + blockIdx.z) * kTile;
+  if (*s_odd) {
+    row_by_row<F>(p, w, kvh, j_begin, j_begin + nt * kKeys, part, Sh::kThreads / 32);
+  } else if (warp < 8 && ok) {
+    const int h = warp >> 2;
+    const uint32_t tO = tmem + 256 + h * HD + ((uint32_t)((warp & 3) * 32) << 16);
+    const float inv = p.splits > 1 ? 1.f : q.l != 0.f ? 1.f / q.l : 0.f;
+    bf16* out = tid < w.count ? out_row(p, w, kvh, tid) : nullptr;
+    for (int c = 0; c < hd; c += 16) {
+      float v[16];
+      if (nt > 0) {
+        tmem_ld16(tO + c, v);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = 0.f;
+      }
+      if (tid < w.count) {
+        if (q.l == 0.f) {  // (a row that sees nothing)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] = 0.f;
+        }
+        if (p.splits > 1) {
+#pragma unroll
+          for (int e = 0; e < 16; e += 4)
+            *reinterpret_cast<float4*>(p.part_o + (part + tid) * hd + c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; e += 8) {
+            float x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = v[e + i] * inv;
+            store8(out + c + e, true, x);
+          }
+        }
+      }
+    }
+    if (p.splits > 1 && tid < w.count) p.part_ml[part + tid] = make_float2(q.m, q.l);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8 + LW) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int HD, Rows F, bool MOD>
+cudaError_t launch_hd(const PagedPrompt& p, const PromptPlan& pl, cudaStream_t st) {
+  using Sh = Shape<HD, F>;
+  static unsigned long long done = 0;
+  auto k = k_prompt_tc<HD, F, MOD>;
+  if (!smem_limit((const void*)k, Sh::kSmem, &done)) return cudaErrorInvalidValue;
+  const dim3 grid(pl.tiles, p.m.n_kv_heads, pl.splits);
+  return launch_op(k, grid, Sh::kThreads, Sh::kSmem, st, false, 1, p);
+}
+template <Rows F>
+cudaError_t launch_rows(const PagedPrompt& p, const PromptPlan& pl, bool mod, cudaStream_t st) {
+  if (p.m.head_dim <= 64) return mod ? launch_hd<64, F, true>(p, pl, st) : launch_hd<64, F, false>(p, pl, st);
+  return mod ? launch_hd<128, F, true>(p, pl, st) : launch_hd<128, F, false>(p, pl, st);
+}
+
+}  // namespace

@@ -664,6 +664,23 @@ int tc_make_tmap3s(CUtensorMap* tm, const void* base, uint64_t d0, uint64_t d1, 
   return r == CUDA_SUCCESS ? 0 : -3;
 }
 
+// 4-D bf16 view [d3][d2][d1][d0] with byte strides s1, s2, s3 and a box of 64 columns and b1 rows, as
+// tc_make_tmap lays it.
+int tc_make_tmap4s(CUtensorMap* tm, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t d3, uint64_t s1,
+                   uint64_t s2, uint64_t s3, uint32_t b1) {
+  PFN_encodeTiled_t enc = get_encode();
+  if (!enc) return -1;
+  if (((uintptr_t)base & 15) || s1 % 16 || s2 % 16 || s3 % 16) return -2;
+  cuuint64_t dims[4] = {d0, d1, d2, d3};
+  cuuint64_t strides[3] = {s1, s2, s3};
+  cuuint32_t box[4] = {(cuuint32_t)kBlockK, b1, 1, 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  CUresult r = enc(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, es,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? 0 : -3;
+}
+
 static size_t smem_bytes(int wide, int xrows, int stages) {
   size_t b = 1024 + (size_t)stages * (wide * kHalfBytes + (size_t)xrows * kBlockK * 2);
   b += (2 * stages + 3) * 8;

@@ -240,6 +240,8 @@ int tc_make_tmap3(CUtensorMap* tm, const void* base, uint64_t d0, uint64_t d1, u
                   uint32_t b1, uint32_t b2);
 // 3-D bf16 view with explicit byte strides s1 (dim 1) and s2 (dim 2), box {64, b1, b2},
 // 128-B swizzle: one TMA request moves b2 slabs of b1 rows x 128 B.
+int tc_make_tmap4s(CUtensorMap* tm, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t d3, uint64_t s1,
+                   uint64_t s2, uint64_t s3, uint32_t b1);
 int tc_make_tmap3s(CUtensorMap* tm, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
                    uint64_t s1, uint64_t s2, uint32_t b1, uint32_t b2);
 // Builds the tensor maps and launch shape for out[M,N] = X[M,K] . W[N,K]^T. split: X

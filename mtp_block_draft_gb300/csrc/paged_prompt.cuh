@@ -22,6 +22,7 @@ struct PagedPrompt {
   dmtp_paged_prompt a;
   unsigned* err;
   int group, tile, splits;
+  int box;              // rows of a TMA box (0: rows are copied one by one)
   float scale2;         // scale log2(e)
   float capl, cap_inv;  // cap log2(e) (0: scores are not capped), and 1 / that
   float* part_o;        // [units][splits][tile][head_dim]

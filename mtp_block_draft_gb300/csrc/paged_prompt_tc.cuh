@@ -24,16 +24,18 @@ using namespace dmtp;
 
 namespace {
 
-constexpr int kTile = 256, kKeys = 128;
+constexpr int kTile = 256, kKeys = 128, kLoaders = 224;
 
 template <int HD, Rows F>
 struct Shape {
-  static constexpr int LW = F == kRaw ? 4 : 8;               // loader warps
-  static constexpr int kThreads = 32 * (8 + LW + 1);
+  static constexpr int kThreads = 512;                       // softmax 256, loaders 224, products
+  // registers of a softmax thread and of the others: together what 512 threads are launched with
+  static constexpr int kMine = F == kRaw ? 184 : 168, kOther = F == kRaw ? 72 : 88;
+  static_assert(256 * (kMine + kOther) <= 65536, "registers");
   static constexpr uint32_t kSlot = kKeys * HD * 2;          // 128 rows of K or V
-  static constexpr int NS = HD == 64 ? 8 : F == kRaw ? 5 : 4;
+  static constexpr int NS = HD == 64 ? 8 : 5;
   static constexpr uint32_t kQ = 2 * 128 * HD * 2;
-  static constexpr uint32_t kHead = 512 + (LW / 4) * kKeys * 8;
+  static constexpr uint32_t kHead = 512 + 2 * kKeys * 6;     // barriers, rows of two blocks
   static constexpr uint32_t kSmem = kHead + 1024 + kQ + NS * kSlot;
   static_assert(kSmem <= 232448, "shared memory");
 };
@@ -73,10 +75,38 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[4][32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));  // no use moves above the wait
+  for (int c = 0; c < 4; ++c)
+#pragma unroll
+    for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[c][i]));  // no use moves above the wait
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+// 4-D tiled TMA load (x = inner coordinate); what lies outside the tensor becomes zeros.
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* tm, int x, int y, int z, int w, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"((uint64_t)tm), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
@@ -110,12 +140,12 @@ __device__ __forceinline__ bf16* out_row(const PagedPrompt& p, const PromptTile&
 }
 
 // The queries of a unit over the positions [j_lo, j_hi), row by row on the CUDA cores: a warp takes a
-// query, a lane a key of 32 and then eight columns.
+// query, a lane a key of 32 and then eight columns. Called by the 8 warps of the softmax.
 template <Rows F>
 __device__ __noinline__ void row_by_row(const PagedPrompt& p, const PromptTile& w, int kvh, int j_lo, int j_hi,
-                                        int64_t part, int warps) {
+                                        int64_t part) {
   const int lane = threadIdx.x & 31, hd = p.m.head_dim;
-  for (int t = threadIdx.x >> 5; t < w.count; t += warps) {
+  for (int t = threadIdx.x >> 5; t < w.count; t += 8) {
     const PromptQuery q = prompt_query(p, w, t);
     const int head = kvh * p.group + q.head;
     const bf16* src = (const bf16*)p.a.q + (int64_t)q.row * p.a.q_row + (int64_t)head * p.a.q_head;
@@ -184,11 +214,16 @@ struct Query {
   int lo, hi, pos;
   float slope, m, l;
 };
-// Scores of 32 keys from j on, in base 2. BIAS scores of MOD kernels; seen: every one is.
-template <bool MOD>
-__device__ __forceinline__ void scores32(const PagedPrompt& p, const Query& q, uint32_t (&r)[32], int j, bool edge) {
-  const float scale = fabsf(p.scale2);
-  if (MOD && p.capl > 0.f) {
+// Where the query does not see one of the 32 keys from j on: minus infinity.
+__device__ __forceinline__ void mask32(const Query& q, uint32_t (&r)[32], int j) {
+  const int from = q.lo - j;
+  const unsigned n = q.hi > q.lo ? q.hi - q.lo : 0;
+#pragma unroll
+  for (int e = 0; e < 32; ++e) r[e] = (unsigned)(e - from) < n ? r[e] : 0xff800000u;
+}
+// Capped and biased scores of 32 keys from j on, in base 2.
+__device__ __forceinline__ void scores32(const PagedPrompt& p, const Query& q, float scale, uint32_t (&r)[32], int j) {
+  if (p.capl > 0.f) {
     const float by = scale * p.cap_inv;
 #pragma unroll
     for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(p.capl * soft_tanh(__uint_as_float(r[e]) * by));
@@ -201,23 +236,16 @@ __device__ __forceinline__ void scores32(const PagedPrompt& p, const Query& q, u
       r[e + 1] = __float_as_uint(v.y);
     }
   }
-  if (MOD) {
-    const float d = (float)(q.pos - j);
+  const float d = (float)(q.pos - j);
 #pragma unroll
-    for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(fmaf(-q.slope, fabsf(d - (float)e), __uint_as_float(r[e])));
-  }
-  if (edge) {
-    const int from = q.lo - j;
-    const unsigned n = q.hi > q.lo ? q.hi - q.lo : 0;
-#pragma unroll
-    for (int e = 0; e < 32; ++e) r[e] = (unsigned)(e - from) < n ? r[e] : 0xff800000u;
-  }
+  for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(fmaf(-q.slope, fabsf(d - (float)e), __uint_as_float(r[e])));
 }
 
 template <int HD, Rows F, bool MOD>
-__global__ void __launch_bounds__(Shape<HD, F>::kThreads, 1) k_prompt_tc(const PagedPrompt p) {
+__global__ void __launch_bounds__(Shape<HD, F>::kThreads, 1)
+    k_prompt_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const PagedPrompt p) {
   using Sh = Shape<HD, F>;
-  constexpr int NS = Sh::NS, LW = Sh::LW, DB = HD / 64;
+  constexpr int NS = Sh::NS;
   extern __shared__ __align__(1024) unsigned char smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, kvh = blockIdx.y, hd = p.m.head_dim;
   if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && warp == 0) prompt_report(p);
@@ -234,13 +262,14 @@ __global__ void __launch_bounds__(Shape<HD, F>::kThreads, 1) k_prompt_tc(const P
   uint32_t* tmem_slot = (uint32_t*)(o_full + 2);
   int* s_span = (int*)(tmem_slot + 1);  // [4] least lo, largest hi; largest lo, least hi (what every query sees)
   int* s_odd = s_span + 4;              // the unit has to be computed row by row
-  int2* s_row = (int2*)(smem + 512);    // [LW / 4][kKeys] page (-1: not there) and row in it
+  int* s_page = (int*)(smem + 512);                // [2][kKeys] of the blocks in turn: a row's page (-1: it
+  uint16_t* s_off = (uint16_t*)(s_page + 2 * kKeys);  // is not there) and which row of that it is
   unsigned char* sQ = smem + Sh::kHead;
   sQ += (1024 - (smem_u32(sQ) & 1023)) & 1023;
   unsigned char* ring = sQ + Sh::kQ;
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
-      mbar_init(smem_u32(full + i), 128);
+      mbar_init(smem_u32(full + i), kLoaders);
       mbar_init(smem_u32(empty + i), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -253,7 +282,7 @@ __global__ void __launch_bounds__(Shape<HD, F>::kThreads, 1) k_prompt_tc(const P
     s_span[1] = s_span[2] = 0;
     *s_odd = 0;
   }
-  if (warp == 8 + LW) tmem_alloc(smem_u32(tmem_slot), 512);
+  if (warp == 12) tmem_alloc(smem_u32(tmem_slot), 512);
   __syncthreads();
   pdl_trigger();
   // ---- the queries: their spans, and their rows as an operand of two halves ----
@@ -314,132 +343,167 @@ __global__ void __launch_bounds__(Shape<HD, F>::kThreads, 1) k_prompt_tc(const P
   const int j_begin = (j_first + t0) * kKeys;
   bool ok = true;
 
-  if (warp >= 8 && warp < 8 + LW) {
-    // ---------------- loaders ----------------
-    const int lt = tid & 127, wg = (warp - 8) >> 2;  // with two warpgroups one brings K, the other V
-    int2* rows = s_row + wg * kKeys;
-    bool odd = false;
-    auto look_up = [&](int t) {  // the rows of block t
-      const int j = j_begin + t * kKeys + lt;
-      int off = 0, page = -1;
-      if (j >= least && j < most) {
-        page = page_of(p.m, w.b, j, off, p.err);
-        odd = odd || page < 0;
-      }
-      rows[lt] = make_int2(page, off);
-    };
-    auto sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory"); };
-    auto whole = [&](int t) {  // every query sees all of block t
-      const int j = j_begin + t * kKeys;
-      return j >= late && j + kKeys <= early;
-    };
-    if constexpr (F == kRaw) {
-      constexpr int CPR = HD / 8, RPP = 128 / CPR;  // 16-byte chunks of a row, rows of a pass
-      const int c = lt % CPR, r0 = lt / CPR;
-      const bool on = 8 * c < hd;
-      int waiting = -1;  // number of the copy that is not yet announced
-      auto announce = [&]() {
-        const int n = waiting;
-        if (n & 1 && !whole(n >> 1) && on) {  // values that not every query sees
-          const unsigned char* slot = ring + (n % NS) * Sh::kSlot + (c >> 3) * 16384;
-#pragma unroll 4
-          for (int i = 0; i < kKeys / RPP; ++i) {
-            const uint4 u = *reinterpret_cast<const uint4*>(slot + sw128(r0 + i * RPP, c & 7));
-            odd = odd || odd_pair(u.x) || odd_pair(u.y) || odd_pair(u.z) || odd_pair(u.w);
-          }
+  // all of a CTA's threads, from their different branches
+  auto meet = [&]() {
+    __syncwarp();
+    asm volatile("bar.sync 2, 512;" ::: "memory");
+  };
+
+  // (each branch is left only for the end: the registers that a thread has differ)
+  if (warp >= 8) {
+    fewer_registers<Sh::kOther>();
+    if (warp != 12) {
+      // ---------------- loaders ----------------
+      const int lt = tid - (warp < 12 ? 256 : 288);
+      bool odd = false;
+      int2 next = make_int2(-1, 0);
+      auto look_up = [&](int t) {  // this thread's row of block t
+        const int j = j_begin + t * kKeys + lt;
+        next = make_int2(-1, 0);
+        if (lt < kKeys && j >= least && j < most) {
+          next.x = page_of(p.m, w.b, j, next.y, p.err);
+          odd = odd || next.x < 0;
         }
-        fence_proxy_async_smem();
-        mbar_arrive(smem_u32(full + n % NS));
       };
-      // (a thread whose wait gave up still takes part in the barriers, and does nothing else)
-      for (int n = 0; n < 2 * nt; ++n) {
-        const int slot = n % NS;
-        const uint32_t gate = smem_u32(empty + slot), parity = ((n / NS) & 1) ^ 1;
-        if (ok && waiting >= 0 && !mbar_try_wait(gate, parity)) {
-          cp_async_wait<0>();
-          announce();
-          waiting = -1;
+      // The rows of block t for all loaders; those of the next are looked up meanwhile. (A thread whose
+      // wait gave up still takes part, and does nothing else.)
+      auto publish = [&](int t) {
+        if (lt < kKeys) {
+          s_page[(t & 1) * kKeys + lt] = next.x;
+          s_off[(t & 1) * kKeys + lt] = (uint16_t)next.y;
         }
-        if (ok) ok = mbar_wait(gate, parity, p.err);
-        if (!(n & 1)) {
-          sync();  // the last block's rows have been read
-          look_up(n >> 1);
-          sync();
-        }
-        if (ok && on) {
-          const uint32_t to = smem_u32(ring + slot * Sh::kSlot + (c >> 3) * 16384);
-          const bf16* base = (const bf16*)((n & 1) ? p.v : p.k) + 8 * c;
-#pragma unroll 4
-          for (int i = 0; i < kKeys / RPP; ++i) {
-            const int r = r0 + i * RPP;
-            const int2 at = rows[r];
-            const int64_t line = (int64_t)kvh * p.m.page_size + at.y;
-            cp_async16(to + sw128(r, c & 7), at.x < 0 ? base : base + (int64_t)at.x * p.m.page_stride + line * hd,
-                       at.x < 0 ? 0 : 16);
+        __syncwarp();
+        asm volatile("bar.sync 1, %0;" ::"n"(kLoaders) : "memory");
+        if (t + 1 < nt) look_up(t + 1);
+      };
+      auto whole = [&](int t) {  // every query sees all of block t
+        const int j = j_begin + t * kKeys;
+        return j >= late && j + kKeys <= early;
+      };
+      look_up(0);
+      if constexpr (F == kRaw) {
+        constexpr int CPR = HD / 8, N = (kKeys * CPR + kLoaders - 1) / kLoaders;  // 16-byte chunks of a row
+        for (int n = 0; n < 2 * nt; ++n) {
+          const int slot = n % NS, t = n >> 1;
+          const bool isv = n & 1;
+          if (!isv) publish(t);
+          if (ok) ok = mbar_wait(smem_u32(empty + slot), ((n / NS) & 1) ^ 1, p.err);
+          const int j = j_begin + t * kKeys;
+          const uint32_t to = smem_u32(ring + slot * Sh::kSlot), bar = smem_u32(full + slot);
+          const bf16* base = (const bf16*)(isv ? p.v : p.k) + (int64_t)kvh * p.m.page_size * hd;
+          const bool look = isv && !whole(t);
+          if (ok && p.box && j >= least && j + kKeys <= most) {
+            // a block of which all positions are seen by some query: a box of p.box rows and 64 columns
+            // a lane. (Of others the rows that none sees become zeros: their pages' contents may be
+            // anything.)
+            if (warp == 13) {
+              if (lane == 0) mbar_expect_tx(bar, Sh::kSlot);
+              __syncwarp();
+              for (int i = lane; i < kKeys / p.box * (HD / 64); i += 32) {
+                const int r = i / (HD / 64) * p.box, x = i % (HD / 64), page = s_page[(t & 1) * kKeys + r];
+                tma_load_4d(to + x * 16384 + r * 128, isv ? &tm_v : &tm_k, 64 * x, s_off[(t & 1) * kKeys + r], kvh,
+                            page < 0 ? p.m.n_pages : page, bar);
+              }
+              if (lane != 0) mbar_arrive(bar);
+            } else {
+              mbar_arrive(bar);
+            }
+            if (look) {  // values that not every query sees
+#pragma unroll 5
+              for (int i = 0; i < N; ++i) {
+                const int x = lt + i * kLoaders, r = x / CPR, c = x % CPR;
+                const int page = r < kKeys ? s_page[(t & 1) * kKeys + r] : -1;
+                if (page >= 0) {
+                  const uint4 u = __ldg(reinterpret_cast<const uint4*>(
+                      base + 8 * c + (int64_t)page * p.m.page_stride + (int)s_off[(t & 1) * kKeys + r] * hd));
+                  odd = odd || odd_pair(u.x) || odd_pair(u.y) || odd_pair(u.z) || odd_pair(u.w);
+                }
+              }
+            }
+          } else if (ok) {
+#pragma unroll 5
+            for (int i = 0; i < N; ++i) {
+              const int x = lt + i * kLoaders, r = x / CPR, c = x % CPR;
+              if (r < kKeys && 8 * c < hd) {
+                const int page = s_page[(t & 1) * kKeys + r];
+                const bf16* src = base + 8 * c;
+                if (page >= 0) src += (int64_t)page * p.m.page_stride + (int)s_off[(t & 1) * kKeys + r] * hd;
+                cp_async16(to + (c >> 3) * 16384 + sw128(r, c & 7), src, page < 0 ? 0 : 16);
+                if (look && page >= 0) {  // values that not every query sees
+                  const uint4 u = __ldg(reinterpret_cast<const uint4*>(src));
+                  odd = odd || odd_pair(u.x) || odd_pair(u.y) || odd_pair(u.z) || odd_pair(u.w);
+                }
+              }
+            }
+            // (arrives when this thread's copies have; the thread that starts the products orders them
+            // before those)
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
           }
         }
         cp_async_commit();
-        if (ok && waiting >= 0) {
-          cp_async_wait<1>();
-          announce();
+        cp_async_wait<0>();
+        if (!ok) {  // the copies on their way end before the CTA does
+          for (int i = 0; i < NS; ++i)
+            if (i < 2 * nt) mbar_wait_for(smem_u32(full + i), 0, p.err, 1000000), mbar_wait_for(smem_u32(full + i), 1, p.err, 1000000);
         }
-        waiting = n;
-      }
-      cp_async_wait<0>();
-      if (ok && waiting >= 0) announce();
-    } else {
-      // 16 columns of a row a thread: their bytes, the block's scale and the row's are asked for before
-      // the slot is free, and become bf16 on their way into it
-      constexpr int CPR = HD / 16, RPP = 128 / CPR, N = kKeys / RPP;
-      const int c = lt % CPR, r0 = lt / CPR;
-      const bool on = 16 * c < hd;
-      const unsigned char* base = (const unsigned char*)(wg ? p.v : p.k);
-      const float* scales = wg ? p.vs : p.ks;
-      const int64_t blk = F == kE2M1 ? e2m1_blocks(p.m) : 0;
-      for (int t = 0; t < nt; ++t) {
-        const int n = 2 * t + wg, slot = n % NS;
-        sync();
-        look_up(t);
-        sync();
-        uint4 u[N];
-        float s[N];
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const int2 at = rows[r0 + i * RPP];
-          u[i] = make_uint4(0, 0, 0, 0);
-          s[i] = 0.f;
-          if (on && at.x >= 0) {
-            const int64_t line = (int64_t)kvh * p.m.page_size + at.y;
-            const unsigned char* pg = base + (int64_t)at.x * p.m.page_stride;
-            s[i] = __ldg(scales + (int64_t)at.x * p.m.scale_stride + line);
-            if (F == kE4M3) {
-              u[i] = __ldg(reinterpret_cast<const uint4*>(pg + line * hd) + c);
-            } else {
-              const uint2 v = __ldg(reinterpret_cast<const uint2*>(pg + line * (hd / 2)) + c);
-              u[i] = make_uint4(v.x, v.y, __ldg(pg + blk + line * (hd / 16) + c), 0);
-            }
-          }
-        }
-        if (ok) ok = mbar_wait(smem_u32(empty + slot), ((n / NS) & 1) ^ 1, p.err);
-        if (ok && on) {
-          unsigned char* to = ring + slot * Sh::kSlot + (c >> 2) * 16384;
-          const bool look = wg && !whole(t);
+      } else {
+        // 16 columns of a row at a time: their bytes, the block's scale and the row's are asked for
+        // while the slot before is filled, and become bf16 on their way into theirs
+        constexpr int CPR = HD / 16, N = (kKeys * CPR + kLoaders - 1) / kLoaders;
+        const int64_t blk = F == kE2M1 ? e2m1_blocks(p.m) : 0;
+        struct Raws {
+          uint4 u[N];
+          float s[N];
+        };
+        auto ask = [&](int n, Raws& z) {
+          const bool isv = n & 1;
+          const unsigned char* base = (const unsigned char*)(isv ? p.v : p.k);
+          const float* scales = isv ? p.vs : p.ks;
 #pragma unroll
           for (int i = 0; i < N; ++i) {
+            const int x = lt + i * kLoaders, r = x / CPR, c = x % CPR;
+            z.u[i] = make_uint4(0, 0, 0, 0);
+            z.s[i] = 0.f;
+            if (r < kKeys && 16 * c < hd) {
+              const int page = s_page[(n >> 1 & 1) * kKeys + r];
+              if (page >= 0) {
+                const int64_t line = (int64_t)kvh * p.m.page_size + s_off[(n >> 1 & 1) * kKeys + r];
+                const unsigned char* pg = base + (int64_t)page * p.m.page_stride;
+                z.s[i] = __ldg(scales + (int64_t)page * p.m.scale_stride + line);
+                if (F == kE4M3) {
+                  z.u[i] = __ldg(reinterpret_cast<const uint4*>(pg + line * hd) + c);
+                } else {
+                  const uint2 v = __ldg(reinterpret_cast<const uint2*>(pg + line * (hd / 2)) + c);
+                  z.u[i] = make_uint4(v.x, v.y, __ldg(pg + blk + line * (hd / 16) + c), 0);
+                }
+              }
+            }
+          }
+        };
+        auto fill = [&](int n, const Raws& z) {
+          const int slot = n % NS;
+          if (ok) ok = mbar_wait(smem_u32(empty + slot), ((n / NS) & 1) ^ 1, p.err);
+          if (!ok) return;
+          unsigned char* to = ring + slot * Sh::kSlot;
+          const bool look = (n & 1) && !whole(n >> 1);
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            const int y = lt + i * kLoaders, r = y / CPR, c = y % CPR;
+            if (r >= kKeys || 16 * c >= hd) continue;
             float f[16];
             if (F == kE4M3) {
-              const uint32_t x[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+              const uint32_t x[4] = {z.u[i].x, z.u[i].y, z.u[i].z, z.u[i].w};
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 const float4 v = e4m3x4_to_f4(x[e]);
-                f[4 * e] = v.x * s[i], f[4 * e + 1] = v.y * s[i], f[4 * e + 2] = v.z * s[i], f[4 * e + 3] = v.w * s[i];
+                f[4 * e] = v.x * z.s[i], f[4 * e + 1] = v.y * z.s[i], f[4 * e + 2] = v.z * z.s[i], f[4 * e + 3] = v.w * z.s[i];
               }
             } else {
-              const float b = h2_to_f2(e4m3x2_to_h2(u[i].z)).x * s[i];
+              const float b = h2_to_f2(e4m3x2_to_h2(z.u[i].z)).x * z.s[i];
               float v[8];
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                e2m1x8_to_f8(h ? u[i].y : u[i].x, v);
+                e2m1x8_to_f8(h ? z.u[i].y : z.u[i].x, v);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) f[8 * h + e] = v[e] * b;
               }
@@ -451,75 +515,106 @@ __global__ void __launch_bounds__(Shape<HD, F>::kThreads, 1) k_prompt_tc(const P
 #pragma unroll
               for (int e = 0; e < 8; ++e) odd = odd || odd_pair(x[e]);
             }
-            const int r = r0 + i * RPP;
-            *reinterpret_cast<uint4*>(to + sw128(r, 2 * c & 7)) = make_uint4(x[0], x[1], x[2], x[3]);
-            *reinterpret_cast<uint4*>(to + sw128(r, (2 * c + 1) & 7)) = make_uint4(x[4], x[5], x[6], x[7]);
+            *reinterpret_cast<uint4*>(to + (c >> 2) * 16384 + sw128(r, 2 * c & 7)) = make_uint4(x[0], x[1], x[2], x[3]);
+            *reinterpret_cast<uint4*>(to + (c >> 2) * 16384 + sw128(r, (2 * c + 1) & 7)) = make_uint4(x[4], x[5], x[6], x[7]);
           }
-        }
-        if (ok) {
           fence_proxy_async_smem();
           mbar_arrive(smem_u32(full + slot));
+        };
+        Raws a, b;  // of K, of V
+        if (nt > 0) {
+          publish(0);
+          ask(0, a);
+        }
+        for (int t = 0; t < nt; ++t) {
+          ask(2 * t + 1, b);
+          fill(2 * t, a);
+          if (t + 1 < nt) {
+            publish(t + 1);
+            ask(2 * t + 2, a);
+          }
+          fill(2 * t + 1, b);
         }
       }
-    }
-    if (odd) *s_odd = 1;
-  } else if (warp == 8 + LW) {
+      if (odd) *s_odd = 1;
+    } else {
     // ---------------- the products ----------------
-    if (lane == 0 && nt > 0) {
+    // (the whole warp goes through this, so that addresses and descriptors are uniform; one thread
+    // starts the products and commits them)
+    if (nt > 0) {
+      const bool leader = elect_one();
       const uint32_t id_s = umma_idesc_bf16(128, kKeys);
       const uint32_t id_o = umma_idesc_bf16(128, hd) | 1u << 16;  // B is MN-major
       const int ks = hd / 16;
+      const uint64_t d_q = umma_desc_sw128(smem_u32(sQ)), d_k = umma_desc_sw128(smem_u32(ring)),
+                     d_v = umma_desc_mn(smem_u32(ring));
       auto scores = [&](int h, int t) {  // S of half h over block t
-        const unsigned char* k = ring + (2 * t % NS) * Sh::kSlot;
-        for (int i = 0; i < ks; ++i) {
-          const uint32_t at = (i >> 2) * 16384 + (i & 3) * 32;
-          umma_bf16(tmem + h * 128, umma_desc_sw128(smem_u32(sQ + h * (128 * HD * 2) + at)),
-                    umma_desc_sw128(smem_u32(k + at)), id_s, i ? 1u : 0u);
+        const uint64_t q0 = d_q + h * (128 * HD * 2 >> 4), k0 = d_k + (2 * t % NS) * (Sh::kSlot >> 4);
+        if (leader) {
+#pragma unroll
+          for (int i = 0; i < HD / 16; ++i) {
+            const uint32_t at = ((i >> 2) * 16384 + (i & 3) * 32) >> 4;
+            if (i < ks) umma_bf16(tmem + h * 128, q0 + at, k0 + at, id_s, i ? 1u : 0u);
+          }
+          umma_commit(smem_u32(s_full + h));
         }
-        umma_commit(smem_u32(s_full + h));
       };
-      auto wait_slot = [&](int n) { return mbar_wait(smem_u32(full + n % NS), (n / NS) & 1, p.err); };
+      auto wait = [&](uint64_t* bar, int parity) { return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, p.err)); };
+      auto wait_slot = [&](int n) {
+        const bool here = wait(full + n % NS, (n / NS) & 1);
+        fence_proxy_async_smem();  // the loaders' writes before the products' reads
+        tc_fence_after();
+        return here;
+      };
       ok = wait_slot(0);
       if (ok) {
-        tc_fence_after();
         scores(0, 0);
         scores(1, 0);
-        umma_commit(smem_u32(empty));
+        if (leader) umma_commit(smem_u32(empty));
       }
       for (int t = 0; t < nt && ok; ++t) {
         const int nv = 2 * t + 1;
         ok = wait_slot(nv);
-        const uint32_t v = smem_u32(ring + (nv % NS) * Sh::kSlot);
-        for (int h = 0; h < 2 && ok; ++h) {
-          ok = mbar_wait(smem_u32(p_full + h), t & 1, p.err);
+        const uint64_t v0 = d_v + (nv % NS) * (Sh::kSlot >> 4);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (ok) ok = wait(p_full + h, t & 1);
           if (!ok) break;
           tc_fence_after();
+          if (leader) {
 #pragma unroll
-          for (int i = 0; i < kKeys / 16; ++i)
-            umma_bf16_ta(tmem + 256 + h * HD, tmem + h * 128 + 8 * i, umma_desc_mn(v + i * 2048), id_o, (t | i) ? 1u : 0u);
-          if (h == 1) umma_commit(smem_u32(empty + nv % NS));
+            for (int i = 0; i < kKeys / 16; ++i)
+              umma_bf16_ta(tmem + 256 + h * HD, tmem + h * 128 + 8 * i, v0 + i * (2048 >> 4), id_o, (t | i) ? 1u : 0u);
+            if (h == 1) umma_commit(smem_u32(empty + nv % NS));
+          }
           if (t + 1 < nt) {
-            if (h == 0) {
-              ok = wait_slot(2 * t + 2);
-              if (!ok) break;
-              tc_fence_after();
-            }
+            if (h == 0) ok = wait_slot(2 * t + 2);
+            if (!ok) break;
             scores(h, t + 1);
-            if (h == 1) umma_commit(smem_u32(empty + (2 * t + 2) % NS));
-          } else {
+            if (h == 1 && leader) umma_commit(smem_u32(empty + (2 * t + 2) % NS));
+          } else if (leader) {
             umma_commit(smem_u32(o_full + h));
           }
         }
       }
       if (!ok) {  // what was issued ends before TMEM is freed
-        umma_commit(smem_u32(o_full));
+        if (leader) umma_commit(smem_u32(o_full));
         mbar_wait(smem_u32(o_full), 0, p.err);
       }
     }
     __syncwarp();
+    }
+    meet();
+    meet();
+    if (warp == 12) {
+      tc_fence_after();
+      tmem_dealloc(tmem, 512);
+    }
   } else {
+    more_registers<Sh::kMine>();
     // ---------------- softmax: warps 0-3 of half 0, 4-7 of half 1 ----------------
     const int h = warp >> 2;
+    const float scale = fmaxf(fabsf(p.scale2), 1.17549435e-38f);  // (of 0: masked scores stay minus infinity)
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + h * 128 + lanes, tO = tmem + 256 + h * HD + lanes;
     // what every query of the warp sees needs no mask
@@ -532,16 +627,21 @@ __global__ void __launch_bounds__(Shape<HD, F>::kThreads, 1) k_prompt_tc(const P
       if (!ok) break;
       tc_fence_after();
       const bool edge = j < from || j + kKeys > to;
-      float top = -INFINITY;
+      uint32_t r[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, r[c]);
+      tmem_wait_ld(r);
+      float tops[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        uint32_t r[32];
-        tmem_ld32(tS + 32 * c, r);
-        tmem_wait_ld(r);
-        scores32<MOD>(p, q, r, j + 32 * c, edge);
+        if (MOD) scores32(p, q, scale, r[c], j + 32 * c);
+        if (edge) mask32(q, r[c], j + 32 * c);
+        tops[c] = fmaxf(__uint_as_float(r[c][0]), __uint_as_float(r[c][1]));
 #pragma unroll
-        for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(r[e]));
+        for (int e = 2; e < 32; e += 2) tops[c] = max3(tops[c], __uint_as_float(r[c][e]), __uint_as_float(r[c][e + 1]));
       }
+      float top = max3(fmaxf(tops[0], tops[1]), tops[2], tops[3]);
+      if (!MOD) top *= scale;
       if (t == 0) {
         q.m = top;
       } else if (__any_sync(0xffffffffu, top > q.m + 8.f)) {
@@ -560,22 +660,22 @@ __global__ void __launch_bounds__(Shape<HD, F>::kThreads, 1) k_prompt_tc(const P
         }
       }
       const float ref = q.m == -INFINITY ? 0.f : q.m;
-      f32x2 sum = both(0.f);
+      const f32x2 by = both(scale), less = both(-ref);
+      f32x2 sum[2] = {both(0.f), both(0.f)};
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        uint32_t r[32], w16[16];
-        tmem_ld32(tS + 32 * c, r);
-        tmem_wait_ld(r);
-        scores32<MOD>(p, q, r, j + 32 * c, edge);
+        uint32_t w16[16];
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
-          const float a = ex2(__uint_as_float(r[e]) - ref), b = ex2(__uint_as_float(r[e + 1]) - ref);
-          sum = add2(sum, pack(a, b));
+          const f32x2 s2 = pack(__uint_as_float(r[c][e]), __uint_as_float(r[c][e + 1]));
+          const float2 x = unpack(MOD ? add2(s2, less) : fma2(s2, by, less));
+          const float a = ex2(x.x), b = ex2(x.y);
+          sum[e / 2 & 1] = add2(sum[e / 2 & 1], pack(a, b));
           w16[e / 2] = pack_bf16(a, b);
         }
         tmem_st16(tS + 16 * c, w16);
       }
-      const float2 two = unpack(sum);
+      const float2 two = unpack(add2(sum[0], sum[1]));
       q.l += two.x + two.y;
       tmem_wait_st();
       tc_fence_before();
@@ -583,52 +683,57 @@ __global__ void __launch_bounds__(Shape<HD, F>::kThreads, 1) k_prompt_tc(const P
     }
     if (ok && nt > 0) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(o_full + h), 0, p.err));
     tc_fence_after();
-  }
-  __syncthreads();
-  const int64_t part = (((int64_t)blockIdx.x * gridDim.y + kvh) * p.splits + blockIdx.z) * kTile;
-  if (*s_odd) {
-    row_by_row<F>(p, w, kvh, j_begin, j_begin + nt * kKeys, part, Sh::kThreads / 32);
-  } else if (warp < 8 && ok) {
-    const int h = warp >> 2;
-    const uint32_t tO = tmem + 256 + h * HD + ((uint32_t)((warp & 3) * 32) << 16);
-    const float inv = p.splits > 1 ? 1.f : q.l != 0.f ? 1.f / q.l : 0.f;
-    bf16* out = tid < w.count ? out_row(p, w, kvh, tid) : nullptr;
-    for (int c = 0; c < hd; c += 16) {
-      float v[16];
-      if (nt > 0) {
-        tmem_ld16(tO + c, v);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = 0.f;
-      }
-      if (tid < w.count) {
-        if (q.l == 0.f) {  // (a row that sees nothing)
+    meet();  // the loaders have seen all values
+    const int64_t part = (((int64_t)blockIdx.x * gridDim.y + kvh) * p.splits + blockIdx.z) * kTile;
+    if (*s_odd) {
+      row_by_row<F>(p, w, kvh, j_begin, j_begin + nt * kKeys, part);
+    } else if (ok) {
+      const float inv = p.splits > 1 ? 1.f : q.l != 0.f ? 1.f / q.l : 0.f;
+      bf16* out = tid < w.count ? out_row(p, w, kvh, tid) : nullptr;
+      for (int c = 0; c < hd; c += 16) {
+        float v[16];
+        if (nt > 0) {
+          tmem_ld16(tO + c, v);
+        } else {
 #pragma unroll
           for (int e = 0; e < 16; ++e) v[e] = 0.f;
         }
-        if (p.splits > 1) {
+        if (tid < w.count) {
+          if (q.l == 0.f) {  // (a row that sees nothing)
 #pragma unroll
-          for (int e = 0; e < 16; e += 4)
-            *reinterpret_cast<float4*>(p.part_o + (part + tid) * hd + c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-        } else {
+            for (int e = 0; e < 16; ++e) v[e] = 0.f;
+          }
+          if (p.splits > 1) {
 #pragma unroll
-          for (int e = 0; e < 16; e += 8) {
-            float x[8];
+            for (int e = 0; e < 16; e += 4)
+              *reinterpret_cast<float4*>(p.part_o + (part + tid) * hd + c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+          } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = v[e + i] * inv;
-            store8(out + c + e, true, x);
+            for (int e = 0; e < 16; e += 8) {
+              float x[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) x[i] = v[e + i] * inv;
+              store8(out + c + e, true, x);
+            }
           }
         }
       }
+      if (p.splits > 1 && tid < w.count) p.part_ml[part + tid] = make_float2(q.m, q.l);
     }
-    if (p.splits > 1 && tid < w.count) p.part_ml[part + tid] = make_float2(q.m, q.l);
+    tc_fence_before();
+    meet();
   }
-  tc_fence_before();
-  __syncthreads();
-  if (warp == 8 + LW) {
-    tc_fence_after();
-    tmem_dealloc(tmem, 512);
-  }
+}
+
+// Tensor maps of the pages, [n_pages][n_kv_heads][page_size][head_dim], with boxes of `box` rows.
+bool page_maps(const PagedPrompt& p, int box, CUtensorMap (&tm)[2]) {
+  const uint64_t row = (uint64_t)p.m.head_dim * 2, page = (uint64_t)p.m.page_stride * 2;
+  if (page >= 1ull << 40) return false;
+  for (int i = 0; i < 2; ++i)
+    if (tc_make_tmap4s(&tm[i], i ? p.v : p.k, p.m.head_dim, p.m.page_size, p.m.n_kv_heads, p.m.n_pages, row,
+                       row * p.m.page_size, page, box))
+      return false;
+  return true;
 }
 
 template <int HD, Rows F, bool MOD>
@@ -638,7 +743,16 @@ cudaError_t launch_hd(const PagedPrompt& p, const PromptPlan& pl, cudaStream_t s
   auto k = k_prompt_tc<HD, F, MOD>;
   if (!smem_limit((const void*)k, Sh::kSmem, &done)) return cudaErrorInvalidValue;
   const dim3 grid(pl.tiles, p.m.n_kv_heads, pl.splits);
-  return launch_op(k, grid, Sh::kThreads, Sh::kSmem, st, false, 1, p);
+  // Whole boxes of a page make up a block of keys: those come by TMA. (Other page sizes and heads row by row.)
+  PagedPrompt a = p;
+  CUtensorMap tm[2] = {};
+  a.box = 0;
+  if (F == kRaw && p.m.head_dim == HD) {
+    const int ps = p.m.page_size;
+    const int box = ps % kKeys == 0 ? kKeys : ps >= 8 && kKeys % ps == 0 ? ps : 0;
+    if (box && page_maps(p, box, tm)) a.box = box;
+  }
+  return launch_op(k, grid, Sh::kThreads, Sh::kSmem, st, false, 1, tm[0], tm[1], a);
 }
 template <Rows F>
 cudaError_t launch_rows(const PagedPrompt& p, const PromptPlan& pl, bool mod, cudaStream_t st) {

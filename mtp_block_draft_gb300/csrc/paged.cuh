@@ -269,20 +269,6 @@ __device__ __forceinline__ float rcp(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// tanh(y) to about 3e-7 of its value: near 0 y + y^3 P(y^2), P fitted to the least largest
-// relative error (4e-9) on |y| <= 0.625; further out 1 - 2 / (1 + e^2y), whose error of 2e-7 is no
-// longer large beside it.
-__device__ __forceinline__ float soft_tanh(float y) {
-  const float t = y * y;
-  float p = fmaf(t, -0.005704984068870544f, 0.0206390842795372f);
-  p = fmaf(t, p, -0.05373971536755562f);
-  p = fmaf(t, p, 0.13331441581249237f);
-  p = fmaf(t, p, -0.3333328068256378f);
-  const float near = fmaf(y * t, p, y);
-  const float far = fmaf(-2.f, rcp(1.f + ex2(y * 2.8853900817779268f)), 1.f);
-  return fabsf(y) <= 0.625f ? near : far;
-}
-
 // Two floats in one register pair: Blackwell's packed single-precision instructions, which halve
 // the issue slots of a pair of operations.
 typedef unsigned long long f32x2;
@@ -312,3 +298,23 @@ __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
   return r;
 }
 __device__ __forceinline__ f32x2 both(float a) { return pack(a, a); }
+// tanh(y) to about 3e-7 of its value: near 0 y + y^3 P(y^2), P fitted to the least largest
+// relative error (4e-9) on |y| <= kTanhNear; further out 1 - 2 / (1 + e^2y), whose error of 2e-7 is no
+// longer large beside it.
+constexpr float kTanhNear = 0.625f, kTanh3 = -0.3333328068256378f, kTanh5 = 0.13331441581249237f,
+                kTanh7 = -0.05373971536755562f, kTanh9 = 0.0206390842795372f, kTanh11 = -0.005704984068870544f;
+__device__ __forceinline__ float soft_tanh(float y) {
+  const float t = y * y;
+  const float p = fmaf(t, fmaf(t, fmaf(t, fmaf(t, kTanh11, kTanh9), kTanh7), kTanh5), kTanh3);
+  const float near = fmaf(y * t, p, y);
+  const float far = fmaf(-2.f, rcp(1.f + ex2(y * 2.8853900817779268f)), 1.f);
+  return fabsf(y) <= kTanhNear ? near : far;
+}
+// The same of two values near 0, t = y^2.
+__device__ __forceinline__ f32x2 tanh_near(f32x2 y, f32x2 t) {
+  f32x2 p = fma2(t, both(kTanh11), both(kTanh9));
+  p = fma2(t, p, both(kTanh7));
+  p = fma2(t, p, both(kTanh5));
+  p = fma2(t, p, both(kTanh3));
+  return fma2(mul2(y, t), p, y);
+}

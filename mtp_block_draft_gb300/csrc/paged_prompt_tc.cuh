@@ -33,10 +33,15 @@ struct Shape {
   static constexpr int kMine = F == kRaw ? 184 : 168, kOther = F == kRaw ? 72 : 88;
   static_assert(256 * (kMine + kOther) <= 65536, "registers");
   static constexpr uint32_t kSlot = kKeys * HD * 2;          // 128 rows of K or V
-  static constexpr int NS = HD == 64 ? 8 : 5;
+  static constexpr int NS = F == kRaw ? (HD == 64 ? 8 : 5) : HD == 64 ? 6 : F == kE2M1 ? 4 : 3;
+  // E4M3 and E2M1 rows as they lie, on their way: values, block scales, the rows' scales
+  static constexpr uint32_t kValues = F == kRaw ? 0 : kKeys * (F == kE4M3 ? HD : HD / 2);
+  static constexpr uint32_t kBlocks = F == kE2M1 ? kKeys * HD / 16 : 0;
+  static constexpr uint32_t kStage = F == kRaw ? 0 : kValues + kBlocks + kKeys * 4;
+  static constexpr int ST = F == kRaw ? 0 : 3;
   static constexpr uint32_t kQ = 2 * 128 * HD * 2;
   static constexpr uint32_t kHead = 512 + 2 * kKeys * 6;     // barriers, rows of two blocks
-  static constexpr uint32_t kSmem = kHead + 1024 + kQ + NS * kSlot;
+  static constexpr uint32_t kSmem = kHead + 1024 + kQ + NS * kSlot + ST * kStage;
   static_assert(kSmem <= 232448, "shared memory");
 };
 
@@ -91,6 +96,12 @@ __device__ __forceinline__ bool elect_one() {
   uint32_t r;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
   return r != 0;
+}
+// `bytes` bytes (a multiple of 16, both addresses too) from global to shared memory.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(__cvta_generic_to_global(src)), "r"(bytes), "r"(bar)
+               : "memory");
 }
 // 4-D tiled TMA load (x = inner coordinate); what lies outside the tensor becomes zeros.
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* tm, int x, int y, int z, int w, uint32_t bar) {
@@ -221,24 +232,45 @@ __device__ __forceinline__ void mask32(const Query& q, uint32_t (&r)[32], int j)
 #pragma unroll
   for (int e = 0; e < 32; ++e) r[e] = (unsigned)(e - from) < n ? r[e] : 0xff800000u;
 }
-// Capped and biased scores of 32 keys from j on, in base 2.
-__device__ __forceinline__ void scores32(const PagedPrompt& p, const Query& q, float scale, uint32_t (&r)[32], int j) {
+// Capped and biased scores of 32 keys from j on, in base 2. `behind`: none of them is past a query's
+// own position, in the whole warp.
+__device__ __forceinline__ void scores32(const PagedPrompt& p, const Query& q, float scale, uint32_t (&r)[32], int j,
+                                         bool behind) {
+  auto at = [&](int e) { return pack(__uint_as_float(r[e]), __uint_as_float(r[e + 1])); };
+  auto put = [&](int e, f32x2 v) {
+    const float2 x = unpack(v);
+    r[e] = __float_as_uint(x.x);
+    r[e + 1] = __float_as_uint(x.y);
+  };
   if (p.capl > 0.f) {
     const float by = scale * p.cap_inv;
+    float most = 0.f;
 #pragma unroll
-    for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(p.capl * soft_tanh(__uint_as_float(r[e]) * by));
-  } else {
-    const f32x2 by = both(scale);
+    for (int e = 0; e < 32; e += 2) most = max3(most, fabsf(__uint_as_float(r[e])), fabsf(__uint_as_float(r[e + 1])));
+    // (a NaN is no maximum, and comes through either form)
+    if (__all_sync(0xffffffffu, most * by <= kTanhNear)) {
 #pragma unroll
-    for (int e = 0; e < 32; e += 2) {
-      const float2 v = unpack(mul2(pack(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), by));
-      r[e] = __float_as_uint(v.x);
-      r[e + 1] = __float_as_uint(v.y);
+      for (int e = 0; e < 32; e += 2) {
+        const f32x2 y = mul2(at(e), both(by)), t = mul2(y, y);
+        put(e, mul2(both(p.capl), tanh_near(y, t)));
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(p.capl * soft_tanh(__uint_as_float(r[e]) * by));
     }
+    if (!p.a.scores.slopes) return;
+    scale = 1.f;
   }
   const float d = (float)(q.pos - j);
+  if (behind) {
+    const f32x2 by = both(scale), slope = both(q.slope), base = both(-q.slope * d);
 #pragma unroll
-  for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(fmaf(-q.slope, fabsf(d - (float)e), __uint_as_float(r[e])));
+    for (int e = 0; e < 32; e += 2) put(e, fma2(at(e), by, fma2(slope, pack((float)e, (float)(e + 1)), base)));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      r[e] = __float_as_uint(fmaf(-q.slope, fabsf(d - (float)e), __uint_as_float(r[e]) * scale));
+  }
 }
 
 template <int HD, Rows F, bool MOD>
@@ -259,7 +291,9 @@ __global__ void __launch_bounds__(Shape<HD, F>::kThreads, 1)
   uint64_t* s_full = empty + NS;     // [2] a half's scores
   uint64_t* p_full = s_full + 2;     // [2] its weights
   uint64_t* o_full = p_full + 2;     // [2] its last product
-  uint32_t* tmem_slot = (uint32_t*)(o_full + 2);
+  uint64_t* st_full = o_full + 2;    // [ST] rows as they lie are there
+  uint64_t* st_empty = st_full + Sh::ST;  // [ST] and have been turned into bf16
+  uint32_t* tmem_slot = (uint32_t*)(st_empty + Sh::ST);
   int* s_span = (int*)(tmem_slot + 1);  // [4] least lo, largest hi; largest lo, least hi (what every query sees)
   int* s_odd = s_span + 4;              // the unit has to be computed row by row
   int* s_page = (int*)(smem + 512);                // [2][kKeys] of the blocks in turn: a row's page (-1: it
@@ -267,10 +301,17 @@ __global__ void __launch_bounds__(Shape<HD, F>::kThreads, 1)
   unsigned char* sQ = smem + Sh::kHead;
   sQ += (1024 - (smem_u32(sQ) & 1023)) & 1023;
   unsigned char* ring = sQ + Sh::kQ;
+  unsigned char* stages = ring + NS * Sh::kSlot;
+  const bool bulk = F != kRaw && p.box;  // one warp brings the rows, the other loaders convert them
+  const int fillers = bulk ? kLoaders - 32 : kLoaders;
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
-      mbar_init(smem_u32(full + i), kLoaders);
+      mbar_init(smem_u32(full + i), fillers);
       mbar_init(smem_u32(empty + i), 1);
+    }
+    for (int i = 0; i < Sh::ST; ++i) {
+      mbar_init(smem_u32(st_full + i), 1);
+      mbar_init(smem_u32(st_empty + i), fillers);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(s_full + i), 1);
@@ -380,7 +421,7 @@ __global__ void __launch_bounds__(Shape<HD, F>::kThreads, 1)
         const int j = j_begin + t * kKeys;
         return j >= late && j + kKeys <= early;
       };
-      look_up(0);
+      if (!bulk) look_up(0);
       if constexpr (F == kRaw) {
         constexpr int CPR = HD / 8, N = (kKeys * CPR + kLoaders - 1) / kLoaders;  // 16-byte chunks of a row
         for (int n = 0; n < 2 * nt; ++n) {
@@ -454,6 +495,7 @@ __global__ void __launch_bounds__(Shape<HD, F>::kThreads, 1)
         struct Raws {
           uint4 u[N];
           float s[N];
+          uint32_t there;
         };
         auto ask = [&](int n, Raws& z) {
           const bool isv = n & 1;
@@ -461,24 +503,49 @@ __global__ void __launch_bounds__(Shape<HD, F>::kThreads, 1)
           const float* scales = isv ? p.vs : p.ks;
 #pragma unroll
           for (int i = 0; i < N; ++i) {
-            const int x = lt + i * kLoaders, r = x / CPR, c = x % CPR;
-            z.u[i] = make_uint4(0, 0, 0, 0);
-            z.s[i] = 0.f;
-            if (r < kKeys && 16 * c < hd) {
-              const int page = s_page[(n >> 1 & 1) * kKeys + r];
-              if (page >= 0) {
-                const int64_t line = (int64_t)kvh * p.m.page_size + s_off[(n >> 1 & 1) * kKeys + r];
-                const unsigned char* pg = base + (int64_t)page * p.m.page_stride;
-                z.s[i] = __ldg(scales + (int64_t)page * p.m.scale_stride + line);
-                if (F == kE4M3) {
-                  z.u[i] = __ldg(reinterpret_cast<const uint4*>(pg + line * hd) + c);
-                } else {
-                  const uint2 v = __ldg(reinterpret_cast<const uint2*>(pg + line * (hd / 2)) + c);
-                  z.u[i] = make_uint4(v.x, v.y, __ldg(pg + blk + line * (hd / 16) + c), 0);
-                }
-              }
+            // (without branches, so that the loads go out together: of a row that is not there those of
+            // page 0 are read and dropped)
+            const int x = lt + i * kLoaders, r = min(x / CPR, kKeys - 1), c = min(x % CPR, hd / 16 - 1);
+            const int page = s_page[(n >> 1 & 1) * kKeys + r], pg0 = max(page, 0);
+            const int64_t line = (int64_t)kvh * p.m.page_size + s_off[(n >> 1 & 1) * kKeys + r];
+            const unsigned char* pg = base + (int64_t)pg0 * p.m.page_stride;
+            z.s[i] = __ldg(scales + (int64_t)pg0 * p.m.scale_stride + line);
+            if (F == kE4M3) {
+              z.u[i] = __ldg(reinterpret_cast<const uint4*>(pg + line * hd) + c);
+            } else {
+              const uint2 v = __ldg(reinterpret_cast<const uint2*>(pg + line * (hd / 2)) + c);
+              z.u[i] = make_uint4(v.x, v.y, __ldg(pg + blk + line * (hd / 16) + c), 0);
+            }
+            z.there = i ? z.there : 0u;
+            z.there |= (page >= 0 ? 1u : 0u) << i;
+          }
+        };
+        // a block of 16 columns as bf16; u: its bytes (E2M1: and in z the block's scale), s: the row's scale
+        auto convert = [&](uint4 u, float s, bool there, uint32_t (&x)[8]) {
+          float f[16];
+          if (F == kE4M3) {
+            const uint32_t y[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float4 v = e4m3x4_to_f4(y[e]);
+              f[4 * e] = v.x * s, f[4 * e + 1] = v.y * s, f[4 * e + 2] = v.z * s, f[4 * e + 3] = v.w * s;
+            }
+          } else {
+            const float b = h2_to_f2(e4m3x2_to_h2(u.z)).x * s;
+            float v[8];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              e2m1x8_to_f8(h ? u.y : u.x, v);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) f[8 * h + e] = v[e] * b;
             }
           }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = there ? pack_bf16(f[2 * e], f[2 * e + 1]) : 0u;
+        };
+        auto put = [&](unsigned char* to, int r, int c, const uint32_t (&x)[8]) {
+          *reinterpret_cast<uint4*>(to + (c >> 2) * 16384 + sw128(r, 2 * c & 7)) = make_uint4(x[0], x[1], x[2], x[3]);
+          *reinterpret_cast<uint4*>(to + (c >> 2) * 16384 + sw128(r, (2 * c + 1) & 7)) = make_uint4(x[4], x[5], x[6], x[7]);
         };
         auto fill = [&](int n, const Raws& z) {
           const int slot = n % NS;
@@ -490,37 +557,95 @@ __global__ void __launch_bounds__(Shape<HD, F>::kThreads, 1)
           for (int i = 0; i < N; ++i) {
             const int y = lt + i * kLoaders, r = y / CPR, c = y % CPR;
             if (r >= kKeys || 16 * c >= hd) continue;
-            float f[16];
-            if (F == kE4M3) {
-              const uint32_t x[4] = {z.u[i].x, z.u[i].y, z.u[i].z, z.u[i].w};
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float4 v = e4m3x4_to_f4(x[e]);
-                f[4 * e] = v.x * z.s[i], f[4 * e + 1] = v.y * z.s[i], f[4 * e + 2] = v.z * z.s[i], f[4 * e + 3] = v.w * z.s[i];
-              }
-            } else {
-              const float b = h2_to_f2(e4m3x2_to_h2(z.u[i].z)).x * z.s[i];
-              float v[8];
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                e2m1x8_to_f8(h ? z.u[i].y : z.u[i].x, v);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) f[8 * h + e] = v[e] * b;
-              }
-            }
             uint32_t x[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = pack_bf16(f[2 * e], f[2 * e + 1]);
+            convert(z.u[i], z.s[i], z.there >> i & 1, x);
             if (look) {
 #pragma unroll
               for (int e = 0; e < 8; ++e) odd = odd || odd_pair(x[e]);
             }
-            *reinterpret_cast<uint4*>(to + (c >> 2) * 16384 + sw128(r, 2 * c & 7)) = make_uint4(x[0], x[1], x[2], x[3]);
-            *reinterpret_cast<uint4*>(to + (c >> 2) * 16384 + sw128(r, (2 * c + 1) & 7)) = make_uint4(x[4], x[5], x[6], x[7]);
+            put(to, r, c, x);
           }
           fence_proxy_async_smem();
           mbar_arrive(smem_u32(full + slot));
         };
+        if (bulk && warp == 13) {
+          // rows of a page lie side by side: a lane has a box of p.box rows
+          const int j0 = j_begin + lane * p.box;
+          int page = -1, off = 0, page1 = -1, off1 = 0;
+          auto box_of = [&](int t, int& pg, int& o) {
+            const int j = j0 + t * kKeys;
+            pg = -1;
+            if (lane < kKeys / p.box && j + p.box > least && j < most) {
+              pg = page_of(p.m, w.b, j, o, p.err);
+              odd = odd || pg < 0;
+            }
+          };
+          if (nt > 0) box_of(0, page1, off1);
+          int n = 0;
+          for (; n < 2 * nt; ++n) {
+            const int st = n % Sh::ST;
+            const bool isv = n & 1;
+            if (!isv) {
+              page = page1;
+              off = off1;
+              if (n / 2 + 1 < nt) box_of(n / 2 + 1, page1, off1);
+            }
+            ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(st_empty + st), ((n / Sh::ST) & 1) ^ 1, p.err));
+            if (!ok) break;
+            const uint32_t bar = smem_u32(st_full + st), to = smem_u32(stages + st * Sh::kStage);
+            const int boxes = __popc(__ballot_sync(0xffffffffu, page >= 0));
+            if (lane == 0) mbar_expect_tx(bar, boxes * p.box * (Sh::kStage / kKeys));
+            __syncwarp();
+            if (page >= 0) {
+              const int64_t line = (int64_t)kvh * p.m.page_size + off;
+              const unsigned char* pg = (const unsigned char*)(isv ? p.v : p.k) + (int64_t)page * p.m.page_stride;
+              const int r = lane * p.box;
+              constexpr int VB = Sh::kValues / kKeys, BB = HD / 16;
+              bulk_load(to + r * VB, pg + line * VB, p.box * VB, bar);
+              if (F == kE2M1) bulk_load(to + Sh::kValues + r * BB, pg + blk + line * BB, p.box * BB, bar);
+              bulk_load(to + Sh::kValues + Sh::kBlocks + r * 4, (isv ? p.vs : p.ks) + (int64_t)page * p.m.scale_stride + line,
+                        p.box * 4, bar);
+            }
+          }
+          if (!ok) {  // the copies on their way end before the CTA does
+            for (int i = max(0, n - Sh::ST); i < n; ++i)
+              mbar_wait_for(smem_u32(st_full + i % Sh::ST), (i / Sh::ST) & 1, p.err, 1000000);
+          }
+        } else if (bulk) {
+          constexpr int kFill = kLoaders - 32, M = (kKeys * CPR + kFill - 1) / kFill;
+          const int ft = warp < 12 ? lt : lt - 32;
+          for (int n = 0; n < 2 * nt; ++n) {
+            const int st = n % Sh::ST, slot = n % NS, t = n >> 1, j = j_begin + t * kKeys;
+            if (ok) ok = mbar_wait(smem_u32(st_full + st), (n / Sh::ST) & 1, p.err);
+            if (ok) ok = mbar_wait(smem_u32(empty + slot), ((n / NS) & 1) ^ 1, p.err);
+            if (!ok) break;
+            const unsigned char* from = stages + st * Sh::kStage;
+            unsigned char* to = ring + slot * Sh::kSlot;
+            const bool look = (n & 1) && !whole(t);
+#pragma unroll
+            for (int i = 0; i < M; ++i) {
+              const int y = ft + i * kFill, r = y / CPR, c = y % CPR;
+              if (r >= kKeys) break;
+              uint4 u;
+              if (F == kE4M3) {
+                u = *reinterpret_cast<const uint4*>(from + r * HD + 16 * c);
+              } else {
+                const uint2 v = *reinterpret_cast<const uint2*>(from + r * (HD / 2) + 8 * c);
+                u = make_uint4(v.x, v.y, from[Sh::kValues + r * CPR + c], 0);
+              }
+              uint32_t x[8];
+              convert(u, reinterpret_cast<const float*>(from + Sh::kValues + Sh::kBlocks)[r], j + r >= least && j + r < most, x);
+              if (look) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) odd = odd || odd_pair(x[e]);
+              }
+              put(to, r, c, x);
+            }
+            mbar_arrive(smem_u32(st_empty + st));
+            fence_proxy_async_smem();
+            mbar_arrive(smem_u32(full + slot));
+          }
+        } else {
         Raws a, b;  // of K, of V
         if (nt > 0) {
           publish(0);
@@ -534,6 +659,7 @@ __global__ void __launch_bounds__(Shape<HD, F>::kThreads, 1)
             ask(2 * t + 2, a);
           }
           fill(2 * t + 1, b);
+        }
         }
       }
       if (odd) *s_odd = 1;
@@ -621,12 +747,13 @@ __global__ void __launch_bounds__(Shape<HD, F>::kThreads, 1)
     const bool mine = tid < w.count;
     const int from = __reduce_max_sync(0xffffffffu, mine ? (q.lo < q.hi ? q.lo : 0x7fffffff) : 0);
     const int to = __reduce_min_sync(0xffffffffu, mine ? q.hi : 0x7fffffff);
+    const int nearest = __reduce_min_sync(0xffffffffu, mine ? q.pos : 0x7fffffff);
     for (int t = 0; t < nt; ++t) {
       const int j = j_begin + t * kKeys;
       ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(s_full + h), t & 1, p.err));
       if (!ok) break;
       tc_fence_after();
-      const bool edge = j < from || j + kKeys > to;
+      const bool edge = j < from || j + kKeys > to, behind = j + kKeys - 1 <= nearest;
       uint32_t r[4][32];
 #pragma unroll
       for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, r[c]);
@@ -634,7 +761,7 @@ __global__ void __launch_bounds__(Shape<HD, F>::kThreads, 1)
       float tops[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        if (MOD) scores32(p, q, scale, r[c], j + 32 * c);
+        if (MOD) scores32(p, q, scale, r[c], j + 32 * c, behind);
         if (edge) mask32(q, r[c], j + 32 * c);
         tops[c] = fmaxf(__uint_as_float(r[c][0]), __uint_as_float(r[c][1]));
 #pragma unroll
@@ -747,10 +874,13 @@ cudaError_t launch_hd(const PagedPrompt& p, const PromptPlan& pl, cudaStream_t s
   PagedPrompt a = p;
   CUtensorMap tm[2] = {};
   a.box = 0;
-  if (F == kRaw && p.m.head_dim == HD) {
+  if (p.m.head_dim == HD) {
     const int ps = p.m.page_size;
     const int box = ps % kKeys == 0 ? kKeys : ps >= 8 && kKeys % ps == 0 ? ps : 0;
-    if (box && page_maps(p, box, tm)) a.box = box;
+    if (F == kRaw)
+      a.box = box && page_maps(p, box, tm) ? box : 0;
+    else if (aligned_to(p.ks, 16) && aligned_to(p.vs, 16) && mult(p.m.scale_stride, 4))
+      a.box = box;
   }
   return launch_op(k, grid, Sh::kThreads, Sh::kSmem, st, false, 1, tm[0], tm[1], a);
 }

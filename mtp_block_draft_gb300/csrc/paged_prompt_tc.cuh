@@ -433,17 +433,19 @@ __global__ void __launch_bounds__(Shape<HD, F>::kThreads, 1)
           const uint32_t to = smem_u32(ring + slot * Sh::kSlot), bar = smem_u32(full + slot);
           const bf16* base = (const bf16*)(isv ? p.v : p.k) + (int64_t)kvh * p.m.page_size * hd;
           const bool look = isv && !whole(t);
-          if (ok && p.box && j >= least && j + kKeys <= most) {
-            // a block of which all positions are seen by some query: a box of p.box rows and 64 columns
-            // a lane. (Of others the rows that none sees become zeros: their pages' contents may be
-            // anything.)
+          // row `from` r up to r + p.box - 1 that some query sees, if there is one
+          auto seen_row = [&](int r) { return min(max(least - j, r), r + p.box - 1); };
+          if (ok && p.box && (!isv || j + kKeys <= w.len)) {
+            // a box of p.box rows and 64 columns a lane; what no query sees of the sequence comes along.
+            // (V rows behind its end may be anything, and become zeros: that block is copied row by row.)
             if (warp == 13) {
               if (lane == 0) mbar_expect_tx(bar, Sh::kSlot);
               __syncwarp();
               for (int i = lane; i < kKeys / p.box * (HD / 64); i += 32) {
-                const int r = i / (HD / 64) * p.box, x = i % (HD / 64), page = s_page[(t & 1) * kKeys + r];
-                tma_load_4d(to + x * 16384 + r * 128, isv ? &tm_v : &tm_k, 64 * x, s_off[(t & 1) * kKeys + r], kvh,
-                            page < 0 ? p.m.n_pages : page, bar);
+                const int r = i / (HD / 64) * p.box, x = i % (HD / 64), rr = seen_row(r);
+                const int page = s_page[(t & 1) * kKeys + rr];
+                tma_load_4d(to + x * 16384 + r * 128, isv ? &tm_v : &tm_k, 64 * x,
+                            page < 0 ? 0 : s_off[(t & 1) * kKeys + rr] - (rr - r), kvh, page < 0 ? p.m.n_pages : page, bar);
               }
               if (lane != 0) mbar_arrive(bar);
             } else {
@@ -453,10 +455,10 @@ __global__ void __launch_bounds__(Shape<HD, F>::kThreads, 1)
 #pragma unroll 5
               for (int i = 0; i < N; ++i) {
                 const int x = lt + i * kLoaders, r = x / CPR, c = x % CPR;
-                const int page = r < kKeys ? s_page[(t & 1) * kKeys + r] : -1;
+                const int rr = seen_row(r & -p.box), page = r < kKeys ? s_page[(t & 1) * kKeys + rr] : -1;
                 if (page >= 0) {
                   const uint4 u = __ldg(reinterpret_cast<const uint4*>(
-                      base + 8 * c + (int64_t)page * p.m.page_stride + (int)s_off[(t & 1) * kKeys + r] * hd));
+                      base + 8 * c + (int64_t)page * p.m.page_stride + ((int)s_off[(t & 1) * kKeys + rr] + r - rr) * hd));
                   odd = odd || odd_pair(u.x) || odd_pair(u.y) || odd_pair(u.z) || odd_pair(u.w);
                 }
               }
@@ -531,17 +533,24 @@ __global__ void __launch_bounds__(Shape<HD, F>::kThreads, 1)
               f[4 * e] = v.x * s, f[4 * e + 1] = v.y * s, f[4 * e + 2] = v.z * s, f[4 * e + 3] = v.w * s;
             }
           } else {
-            const float b = h2_to_f2(e4m3x2_to_h2(u.z)).x * s;
-            float v[8];
+            const f32x2 b = both(h2_to_f2(e4m3x2_to_h2(u.z)).x * s);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
+              float v[8];
               e2m1x8_to_f8(h ? u.y : u.x, v);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) f[8 * h + e] = v[e] * b;
+              for (int e = 0; e < 8; e += 2) {
+                const float2 y = unpack(mul2(pack(v[e], v[e + 1]), b));
+                f[8 * h + e] = y.x, f[8 * h + e + 1] = y.y;
+              }
             }
           }
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = there ? pack_bf16(f[2 * e], f[2 * e + 1]) : 0u;
+          for (int e = 0; e < 8; ++e) x[e] = pack_bf16(f[2 * e], f[2 * e + 1]);
+          if (!there) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = 0u;
+          }
         };
         auto put = [&](unsigned char* to, int r, int c, const uint32_t (&x)[8]) {
           *reinterpret_cast<uint4*>(to + (c >> 2) * 16384 + sw128(r, 2 * c & 7)) = make_uint4(x[0], x[1], x[2], x[3]);

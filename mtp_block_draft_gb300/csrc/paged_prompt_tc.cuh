@@ -263,9 +263,11 @@ __device__ __forceinline__ void scores32(const PagedPrompt& p, const Query& q, f
   }
   const float d = (float)(q.pos - j);
   if (behind) {
-    const f32x2 by = both(scale), slope = both(q.slope), base = both(-q.slope * d);
+    const f32x2 by = both(scale);
+    const float base = -q.slope * d;
 #pragma unroll
-    for (int e = 0; e < 32; e += 2) put(e, fma2(at(e), by, fma2(slope, pack((float)e, (float)(e + 1)), base)));
+    for (int e = 0; e < 32; e += 2)
+      put(e, fma2(at(e), by, pack(fmaf(q.slope, (float)e, base), fmaf(q.slope, (float)(e + 1), base))));
   } else {
 #pragma unroll
     for (int e = 0; e < 32; ++e)
@@ -289,8 +291,8 @@ __global__ void __launch_bounds__(Shape<HD, F>::kThreads, 1)
   uint64_t* full = (uint64_t*)smem;  // [NS] a slot's rows are there
   uint64_t* empty = full + NS;       // [NS] the products have read it
   uint64_t* s_full = empty + NS;     // [2] a half's scores
-  uint64_t* p_full = s_full + 2;     // [2] its weights
-  uint64_t* o_full = p_full + 2;     // [2] its last product
+  uint64_t* p_full = s_full + 2;     // [2][2] its weights of the block's first 64 keys, of the others
+  uint64_t* o_full = p_full + 4;     // [2] its last product
   uint64_t* st_full = o_full + 2;    // [ST] rows as they lie are there
   uint64_t* st_empty = st_full + Sh::ST;  // [ST] and have been turned into bf16
   uint32_t* tmem_slot = (uint32_t*)(st_empty + Sh::ST);
@@ -315,7 +317,8 @@ __global__ void __launch_bounds__(Shape<HD, F>::kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(s_full + i), 1);
-      mbar_init(smem_u32(p_full + i), 128);
+      mbar_init(smem_u32(p_full + 2 * i), 128);
+      mbar_init(smem_u32(p_full + 2 * i + 1), 128);
       mbar_init(smem_u32(o_full + i), 1);
     }
     fence_mbar_init();
@@ -678,6 +681,7 @@ __global__ void __launch_bounds__(Shape<HD, F>::kThreads, 1)
     // starts the products and commits them)
     if (nt > 0) {
       const bool leader = elect_one();
+      const int halves = w.count > 128 ? 2 : 1;
       const uint32_t id_s = umma_idesc_bf16(128, kKeys);
       const uint32_t id_o = umma_idesc_bf16(128, hd) | 1u << 16;  // B is MN-major
       const int ks = hd / 16;
@@ -704,7 +708,7 @@ __global__ void __launch_bounds__(Shape<HD, F>::kThreads, 1)
       ok = wait_slot(0);
       if (ok) {
         scores(0, 0);
-        scores(1, 0);
+        if (halves > 1) scores(1, 0);
         if (leader) umma_commit(smem_u32(empty));
       }
       for (int t = 0; t < nt && ok; ++t) {
@@ -713,20 +717,26 @@ __global__ void __launch_bounds__(Shape<HD, F>::kThreads, 1)
         const uint64_t v0 = d_v + (nv % NS) * (Sh::kSlot >> 4);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if (ok) ok = wait(p_full + h, t & 1);
-          if (!ok) break;
-          tc_fence_after();
-          if (leader) {
+          if (h >= halves) break;
 #pragma unroll
-            for (int i = 0; i < kKeys / 16; ++i)
-              umma_bf16_ta(tmem + 256 + h * HD, tmem + h * 128 + 8 * i, v0 + i * (2048 >> 4), id_o, (t | i) ? 1u : 0u);
-            if (h == 1) umma_commit(smem_u32(empty + nv % NS));
+          for (int x = 0; x < 2; ++x) {
+            if (ok) ok = wait(p_full + 2 * h + x, t & 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (leader) {
+#pragma unroll
+              for (int i = 4 * x; i < 4 * x + 4; ++i)
+                umma_bf16_ta(tmem + 256 + h * HD, tmem + h * 128 + 8 * i, v0 + i * (2048 >> 4), id_o, (t | i) ? 1u : 0u);
+            }
           }
+          if (!ok) break;
+          const bool last = h + 1 == halves;
+          if (last && leader) umma_commit(smem_u32(empty + nv % NS));
           if (t + 1 < nt) {
             if (h == 0) ok = wait_slot(2 * t + 2);
             if (!ok) break;
             scores(h, t + 1);
-            if (h == 1 && leader) umma_commit(smem_u32(empty + (2 * t + 2) % NS));
+            if (last && leader) umma_commit(smem_u32(empty + (2 * t + 2) % NS));
           } else if (leader) {
             umma_commit(smem_u32(o_full + h));
           }
@@ -757,7 +767,8 @@ __global__ void __launch_bounds__(Shape<HD, F>::kThreads, 1)
     const int from = __reduce_max_sync(0xffffffffu, mine ? (q.lo < q.hi ? q.lo : 0x7fffffff) : 0);
     const int to = __reduce_min_sync(0xffffffffu, mine ? q.hi : 0x7fffffff);
     const int nearest = __reduce_min_sync(0xffffffffu, mine ? q.pos : 0x7fffffff);
-    for (int t = 0; t < nt; ++t) {
+    const bool used = h == 0 || w.count > 128;  // (of a short tile there is no second half)
+    for (int t = 0; t < nt && used; ++t) {
       const int j = j_begin + t * kKeys;
       ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(s_full + h), t & 1, p.err));
       if (!ok) break;
@@ -810,14 +821,16 @@ __global__ void __launch_bounds__(Shape<HD, F>::kThreads, 1)
           w16[e / 2] = pack_bf16(a, b);
         }
         tmem_st16(tS + 16 * c, w16);
+        if (c & 1) {
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(smem_u32(p_full + 2 * h + c / 2));
+        }
       }
       const float2 two = unpack(add2(sum[0], sum[1]));
       q.l += two.x + two.y;
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(smem_u32(p_full + h));
     }
-    if (ok && nt > 0) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(o_full + h), 0, p.err));
+    if (ok && nt > 0 && used) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(o_full + h), 0, p.err));
     tc_fence_after();
     meet();  // the loaders have seen all values
     const int64_t part = (((int64_t)blockIdx.x * gridDim.y + kvh) * p.splits + blockIdx.z) * kTile;
@@ -828,7 +841,7 @@ __global__ void __launch_bounds__(Shape<HD, F>::kThreads, 1)
       bf16* out = tid < w.count ? out_row(p, w, kvh, tid) : nullptr;
       for (int c = 0; c < hd; c += 16) {
         float v[16];
-        if (nt > 0) {
+        if (nt > 0 && used) {
           tmem_ld16(tO + c, v);
         } else {
 #pragma unroll

@@ -220,6 +220,16 @@ __device__ __noinline__ void row_by_row(const PagedPrompt& p, const PromptTile& 
   }
 }
 
+// The largest of a block's scores.
+__device__ __forceinline__ float top_of(const uint32_t (&r)[4][32], float (&tops)[4]) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    tops[c] = fmaxf(__uint_as_float(r[c][0]), __uint_as_float(r[c][1]));
+#pragma unroll
+    for (int e = 2; e < 32; e += 2) tops[c] = max3(tops[c], __uint_as_float(r[c][e]), __uint_as_float(r[c][e + 1]));
+  }
+  return max3(fmaxf(tops[0], tops[1]), tops[2], tops[3]);
+}
 // What a thread of the softmax knows of its query.
 struct Query {
   int lo, hi, pos;
@@ -232,10 +242,26 @@ __device__ __forceinline__ void mask32(const Query& q, uint32_t (&r)[32], int j)
 #pragma unroll
   for (int e = 0; e < 32; ++e) r[e] = (unsigned)(e - from) < n ? r[e] : 0xff800000u;
 }
-// Capped and biased scores of 32 keys from j on, in base 2. `behind`: none of them is past a query's
-// own position, in the whole warp.
-__device__ __forceinline__ void scores32(const PagedPrompt& p, const Query& q, float scale, uint32_t (&r)[32], int j,
-                                         bool behind) {
+// Capped and biased scores of 32 keys from j on, in base 2, less `ref`. `behind`: none of them is past a
+// query's own position, in the whole warp. Two packed instructions take the time of four others here,
+// so the cap's polynomial has the cap and the scale in its coefficients: cap tanh(s by) is
+// s (a0 + a1 s^2 + ..), 6 of them a pair.
+struct Cap {
+  float near, a[5];  // |s| up to `near` takes the polynomial (tanh(y) / y to 2e-8 for |y| <= 1/2)
+};
+__device__ __forceinline__ Cap cap_of(const PagedPrompt& p, float scale) {
+  const float by = scale * p.cap_inv, t = by * by;
+  Cap c;
+  c.near = 0.5f / by;
+  c.a[0] = p.capl * by;
+  c.a[1] = c.a[0] * t * -0.333331435918808f;
+  c.a[2] = c.a[0] * (t * t) * 0.13325878977775574f;
+  c.a[3] = c.a[0] * (t * t * t) * -0.05304549261927605f;
+  c.a[4] = c.a[0] * (t * t * t * t) * 0.01724148541688919f;
+  return c;
+}
+__device__ __forceinline__ void scores32(const PagedPrompt& p, const Query& q, const Cap& cap, float scale, float ref,
+                                         uint32_t (&r)[32], int j, bool behind) {
   auto at = [&](int e) { return pack(__uint_as_float(r[e]), __uint_as_float(r[e + 1])); };
   auto put = [&](int e, f32x2 v) {
     const float2 x = unpack(v);
@@ -243,20 +269,25 @@ __device__ __forceinline__ void scores32(const PagedPrompt& p, const Query& q, f
     r[e + 1] = __float_as_uint(x.y);
   };
   if (p.capl > 0.f) {
-    const float by = scale * p.cap_inv;
+    const float less = p.a.scores.slopes ? 0.f : -ref;
     float most = 0.f;
 #pragma unroll
     for (int e = 0; e < 32; e += 2) most = max3(most, fabsf(__uint_as_float(r[e])), fabsf(__uint_as_float(r[e + 1])));
-    // (a NaN is no maximum, and comes through either form)
-    if (__all_sync(0xffffffffu, most * by <= kTanhNear)) {
+    // (a NaN is no maximum, and comes through either form; a scale that leaves no polynomial has none)
+    if (__all_sync(0xffffffffu, most <= cap.near && cap.a[4] != 0.f)) {
 #pragma unroll
       for (int e = 0; e < 32; e += 2) {
-        const f32x2 y = mul2(at(e), both(by)), t = mul2(y, y);
-        put(e, mul2(both(p.capl), tanh_near(y, t)));
+        const f32x2 x = at(e), t = mul2(x, x);
+        f32x2 v = fma2(t, both(cap.a[4]), both(cap.a[3]));
+        v = fma2(t, v, both(cap.a[2]));
+        v = fma2(t, v, both(cap.a[1]));
+        v = fma2(t, v, both(cap.a[0]));
+        put(e, fma2(x, v, both(less)));
       }
     } else {
+      const float by = scale * p.cap_inv;
 #pragma unroll
-      for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(p.capl * soft_tanh(__uint_as_float(r[e]) * by));
+      for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(fmaf(p.capl, soft_tanh(__uint_as_float(r[e]) * by), less));
     }
     if (!p.a.scores.slopes) return;
     scale = 1.f;
@@ -264,14 +295,14 @@ __device__ __forceinline__ void scores32(const PagedPrompt& p, const Query& q, f
   const float d = (float)(q.pos - j);
   if (behind) {
     const f32x2 by = both(scale);
-    const float base = -q.slope * d;
+    const float base = fmaf(-q.slope, d, -ref);
 #pragma unroll
     for (int e = 0; e < 32; e += 2)
       put(e, fma2(at(e), by, pack(fmaf(q.slope, (float)e, base), fmaf(q.slope, (float)(e + 1), base))));
   } else {
 #pragma unroll
     for (int e = 0; e < 32; ++e)
-      r[e] = __float_as_uint(fmaf(-q.slope, fabsf(d - (float)e), __uint_as_float(r[e]) * scale));
+      r[e] = __float_as_uint(fmaf(-q.slope, fabsf(d - (float)e), __uint_as_float(r[e]) * scale) - ref);
   }
 }
 
@@ -385,6 +416,11 @@ __global__ void __launch_bounds__(Shape<HD, F>::kThreads, 1)
   const int blocks = least < most ? (most + kKeys - 1) / kKeys - j_first : 0;
   const int t0 = (int)((int64_t)blocks * blockIdx.z / p.splits), nt = (int)((int64_t)blocks * (blockIdx.z + 1) / p.splits) - t0;
   const int j_begin = (j_first + t0) * kKeys;
+  // First position of block t. With a bias the nearest scores are the largest: from the last block to
+  // the first the reference seldom moves (a prompt of 16384 rows 2.06 ms; the other way O was rescaled in
+  // most blocks of the steeper heads, 2.48). Without, the masked blocks come better at the end (1.47
+  // and 1.52).
+  auto block = [&](int t) { return j_begin + (MOD ? nt - 1 - t : t) * kKeys; };
   bool ok = true;
 
   // all of a CTA's threads, from their different branches
@@ -402,7 +438,7 @@ __global__ void __launch_bounds__(Shape<HD, F>::kThreads, 1)
       bool odd = false;
       int2 next = make_int2(-1, 0);
       auto look_up = [&](int t) {  // this thread's row of block t
-        const int j = j_begin + t * kKeys + lt;
+        const int j = block(t) + lt;
         next = make_int2(-1, 0);
         if (lt < kKeys && j >= least && j < most) {
           next.x = page_of(p.m, w.b, j, next.y, p.err);
@@ -421,7 +457,7 @@ __global__ void __launch_bounds__(Shape<HD, F>::kThreads, 1)
         if (t + 1 < nt) look_up(t + 1);
       };
       auto whole = [&](int t) {  // every query sees all of block t
-        const int j = j_begin + t * kKeys;
+        const int j = block(t);
         return j >= late && j + kKeys <= early;
       };
       if (!bulk) look_up(0);
@@ -432,7 +468,7 @@ __global__ void __launch_bounds__(Shape<HD, F>::kThreads, 1)
           const bool isv = n & 1;
           if (!isv) publish(t);
           if (ok) ok = mbar_wait(smem_u32(empty + slot), ((n / NS) & 1) ^ 1, p.err);
-          const int j = j_begin + t * kKeys;
+          const int j = block(t);
           const uint32_t to = smem_u32(ring + slot * Sh::kSlot), bar = smem_u32(full + slot);
           const bf16* base = (const bf16*)(isv ? p.v : p.k) + (int64_t)kvh * p.m.page_size * hd;
           const bool look = isv && !whole(t);
@@ -582,10 +618,9 @@ __global__ void __launch_bounds__(Shape<HD, F>::kThreads, 1)
         };
         if (bulk && warp == 13) {
           // rows of a page lie side by side: a lane has a box of p.box rows
-          const int j0 = j_begin + lane * p.box;
           int page = -1, off = 0, page1 = -1, off1 = 0;
           auto box_of = [&](int t, int& pg, int& o) {
-            const int j = j0 + t * kKeys;
+            const int j = block(t) + lane * p.box;
             pg = -1;
             if (lane < kKeys / p.box && j + p.box > least && j < most) {
               pg = page_of(p.m, w.b, j, o, p.err);
@@ -627,7 +662,7 @@ __global__ void __launch_bounds__(Shape<HD, F>::kThreads, 1)
           constexpr int kFill = kLoaders - 32, M = (kKeys * CPR + kFill - 1) / kFill;
           const int ft = warp < 12 ? lt : lt - 32;
           for (int n = 0; n < 2 * nt; ++n) {
-            const int st = n % Sh::ST, slot = n % NS, t = n >> 1, j = j_begin + t * kKeys;
+            const int st = n % Sh::ST, slot = n % NS, t = n >> 1, j = block(t);
             if (ok) ok = mbar_wait(smem_u32(st_full + st), (n / Sh::ST) & 1, p.err);
             if (ok) ok = mbar_wait(smem_u32(empty + slot), ((n / NS) & 1) ^ 1, p.err);
             if (!ok) break;
@@ -766,10 +801,15 @@ __global__ void __launch_bounds__(Shape<HD, F>::kThreads, 1)
     const bool mine = tid < w.count;
     const int from = __reduce_max_sync(0xffffffffu, mine ? (q.lo < q.hi ? q.lo : 0x7fffffff) : 0);
     const int to = __reduce_min_sync(0xffffffffu, mine ? q.hi : 0x7fffffff);
+    // scores that a cap keeps within 2^+-60 need no reference but 0
+    const bool fixed = MOD && p.capl > 0.f && p.capl <= 60.f && !p.a.scores.slopes;
+    if (fixed) q.m = 0.f;
+    Cap cap = {};
+    if (MOD) cap = cap_of(p, scale);
     const int nearest = __reduce_min_sync(0xffffffffu, mine ? q.pos : 0x7fffffff);
     const bool used = h == 0 || w.count > 128;  // (of a short tile there is no second half)
     for (int t = 0; t < nt && used; ++t) {
-      const int j = j_begin + t * kKeys;
+      const int j = block(t);
       ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(s_full + h), t & 1, p.err));
       if (!ok) break;
       tc_fence_after();
@@ -778,32 +818,55 @@ __global__ void __launch_bounds__(Shape<HD, F>::kThreads, 1)
 #pragma unroll
       for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, r[c]);
       tmem_wait_ld(r);
-      float tops[4];
+      float tops[4], fix = 1.f;
+      bool rises = false;
+      if constexpr (MOD) {
+        // the scores come relative to the reference of the blocks before
+        const float was = q.m == -INFINITY ? 0.f : q.m;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        if (MOD) scores32(p, q, scale, r[c], j + 32 * c, behind);
-        if (edge) mask32(q, r[c], j + 32 * c);
-        tops[c] = fmaxf(__uint_as_float(r[c][0]), __uint_as_float(r[c][1]));
+        for (int c = 0; c < 4; ++c) {
+          scores32(p, q, cap, scale, was, r[c], j + 32 * c, behind);
+          if (edge) mask32(q, r[c], j + 32 * c);
+        }
+        if (!fixed) {
+          const float top = top_of(r, tops);
+          const bool up = q.m == -INFINITY ? top > -INFINITY : top > 8.f;
+          rises = __any_sync(0xffffffffu, up);
+          if (rises) {
+            const float by = up ? top : 0.f;
+            fix = !up ? 1.f : q.m == -INFINITY ? 0.f : ex2(-by);
+            if (up) q.m = was + by;
 #pragma unroll
-        for (int e = 2; e < 32; e += 2) tops[c] = max3(tops[c], __uint_as_float(r[c][e]), __uint_as_float(r[c][e + 1]));
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int e = 0; e < 32; ++e) r[c][e] = __float_as_uint(__uint_as_float(r[c][e]) - by);
+          }
+        }
+      } else {
+        if (edge) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) mask32(q, r[c], j + 32 * c);
+        }
+        const float top = top_of(r, tops) * scale;
+        const bool up = q.m == -INFINITY ? top > -INFINITY : top > q.m + 8.f;
+        rises = __any_sync(0xffffffffu, up);
+        if (rises) {
+          fix = up ? ex2(q.m - top) : 1.f;  // (0 for the first)
+          if (up) q.m = top;
+        }
       }
-      float top = max3(fmaxf(tops[0], tops[1]), tops[2], tops[3]);
-      if (!MOD) top *= scale;
-      if (t == 0) {
-        q.m = top;
-      } else if (__any_sync(0xffffffffu, top > q.m + 8.f)) {
-        const float n = top > q.m + 8.f ? top : q.m;
-        const float fix = n == q.m ? 1.f : ex2(q.m - n);  // (0 for the first)
-        q.m = n;
+      if (rises) {
         q.l *= fix;
+        if (t > 0) {
 #pragma unroll 1
-        for (int c = 0; c < hd; c += 16) {
-          float v[16];
-          uint32_t r[16];
-          tmem_ld16(tO + c, v);
+          for (int c = 0; c < hd; c += 16) {
+            float v[16];
+            uint32_t o[16];
+            tmem_ld16(tO + c, v);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(v[e] * fix);
-          tmem_st16(tO + c, r);
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(v[e] * fix);
+            tmem_st16(tO + c, o);
+          }
         }
       }
       const float ref = q.m == -INFINITY ? 0.f : q.m;
@@ -815,7 +878,7 @@ __global__ void __launch_bounds__(Shape<HD, F>::kThreads, 1)
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
           const f32x2 s2 = pack(__uint_as_float(r[c][e]), __uint_as_float(r[c][e + 1]));
-          const float2 x = unpack(MOD ? add2(s2, less) : fma2(s2, by, less));
+          const float2 x = unpack(MOD ? s2 : fma2(s2, by, less));
           const float a = ex2(x.x), b = ex2(x.y);
           sum[e / 2 & 1] = add2(sum[e / 2 & 1], pack(a, b));
           w16[e / 2] = pack_bf16(a, b);

@@ -211,12 +211,13 @@ int dmtp_paged_attention_scores(const dmtp_paged_kv* c, const dmtp_paged_query* 
  * sequence are left as they were. kv heads serve query heads as in dmtp_paged_attention, and
  * lengths past the table's reach, bad pages, NaN and infinities are treated as there. Row starts
  * that do not ascend or lie outside [0, n_rows] set DMTP_OPS_ERR_ROWS and are taken as the nearest
- * that fit (of sequences whose rows overlap either may be the one that is computed).
+ * that fit (of sequences whose rows overlap either may be the one that is computed, or neither).
  * Scores, softmax statistics and sums are fp32. bf16 rows of head_dim <= 128 run on the tensor
  * cores: the cached values as bf16 (of E4M3 and E2M1 rows whose scales are powers of two exactly, of
- * others rounded to it) and the weights, relative to about the largest so far, as bf16; other
- * rows on the CUDA cores in fp32. Types, alignment, strides and limits of q and out as in
- * dmtp_paged_attention. Results do not depend on timing. */
+ * others rounded to it), the weights as bf16, relative to about the largest so far or, capped at
+ * 41 or less with no bias, to that of a score of 0; the sum of weights times values must stay below
+ * 2^120. Other rows run on the CUDA cores in fp32. Types, alignment, strides and limits of q and out as
+ * in dmtp_paged_attention; n_rows <= 2^24. Results do not depend on timing. */
 typedef struct {
   const void* q;
   void* out;

@@ -18,6 +18,9 @@
 // 130 us. With a lane per key and the rows staged for the CTA, one stage at a time, those took 147,
 // 954, 70, 33 and 220 us. Bf16 heads of 128 take 92 us and with 64 queries 520 us that way, on the
 // tensor cores 30 and 72: they are left to those.
+//
+// E2M1 rows: two bytes a lane, brought four at a time by every other lane; a row's block scales come as
+// the whole words that hold them.
 #pragma once
 
 #include <cuda_fp16.h>

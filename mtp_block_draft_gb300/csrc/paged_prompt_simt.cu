@@ -3,7 +3,9 @@
 //
 // A CTA of 256 threads has a tile of 64 queries and goes through the keys 64 (heads over 128
 // columns: 32) at a time, Q, K and V as fp32 in shared memory. A thread has 4 queries: of the
-// scores with 4 keys, of the output with a sixteenth of the columns.
+// scores with 4 keys, of the output with a sixteenth of the columns: per four columns and key pair of
+// loads 64 fused operations, so the fp32 pipes bound it (16384 bf16 rows of 32 / 4 heads of 128, which
+// the tensor cores take, took 66 ms here: 33 TFLOP/s).
 #include <type_traits>
 
 #include "paged_prompt.cuh"

@@ -8,9 +8,27 @@
 //   O += P V    tcgen05, A = P from TMEM, B = V as its rows lie (keys by columns, MN-major)
 // S and O of both halves fill TMEM's 512 columns; while one half's softmax runs, the tensor cores
 // work for the other. The reference m of a query moves only when a score passes it by 2^8, so that O
-// is hardly ever rescaled. Loader warps bring K and V (of E4M3 and E2M1 rows as bf16) into a ring of
-// shared-memory slots by the page, row for row, which leaves page sizes and strides free; one
-// thread issues the products.
+// is hardly ever rescaled. A thread holds the 128 scores of its query and block in registers, which
+// the softmax's warps get from the others (184 and 72 a thread; 128 for all spilled, and a second
+// reading from TMEM instead took 3.06 ms where this takes 1.47). The products of a block begin with the
+// weights of its first 64 keys. One warp, uniform, starts them all: as one thread of a diverged warp it
+// needed 4200 cycles for the 32 products of a block, which take 2048.
+//
+// Keys and values come into a ring of shared-memory slots:
+//   bf16, whole boxes of a page (page sizes that 128 divides or that divide 128, heads of 64 or 128)
+//     by TMA, a box a lane, outside the tensor where a page is not looked up (zeros);
+//   other bf16 rows, and V at a sequence's end (its rows past the end may be anything) row by row by
+//     16-byte copies (a prompt of 16384 rows 3.07 ms so, 1.46 by TMA);
+//   E4M3 and E2M1 rows as they lie, by bulk copies of the same boxes, three ahead, which six warps
+//     turn into bf16 (over 16384 4-bit positions 465 us; through registers, for other pages, 548).
+//
+// What bounds it: 16384 rows of 32 / 4 heads of 128, causal: 1.47 ms, 1490 TFLOP/s, 0.87 of what cuBLAS
+// sustains at the power limit; a block of keys costs about 3000 cycles where its products take 2048,
+// the chain of one half's softmax (1400), products (1024) and barriers. With a bias 2.06 ms, capped
+// 2.57: packed fp32 instructions take two cycles a warp, and those of two warps an SM quarter add up.
+// 4-bit rows without a bias 277 us (bf16 209): the conversions. Short prompts pay about 5 us a unit
+// for its queries, first block and output (4 prompts of 1021 to 2047 rows, uncapped: 160 us, 0.34 of
+// the burst rate).
 //
 // A row may see any interval of positions: a block that not every query of a warp sees whole is
 // masked there. In such a block a weight is 0 where a value may be infinite or NaN, and the tensor

@@ -1,8 +1,14 @@
 // dmtp_paged_write_rope, and E2M1 rows into and out of the pages of a K/V cache.
 //
-// Write. A group of lanes takes one head of one row, a lane 16 consecutive columns of it: a block of
-// an E2M1 row, whole pairs of an interleaved rotation; the partners of a rotate-half pair are read
-// once more from the row, which its first reader has just brought to L1.
+// Write. A group of lanes takes one head of one row, a lane two chunks of eight columns of it: side by
+// side, or (PAIR) where rotate-half pairs meet eight of each half of what is rotated. A block of an E2M1
+// row is then two neighbours' business; where the half is no whole number of blocks, chunks stay
+// side by side and the partners are read once more. The bytes moved are the rows
+// once in and once out: 8188 rows of 32 + 2 x 4 heads of 128, half of each rotated, into E4M3 pages
+// take 44 us (160 MB, 0.53 of the copy rate), 32 rows into bf16 pages 3.8 us, which is latency; 4096 rows
+// into E2M1 pages and back 29 us (89 MB in two launches). Issue bounds the many-row form: two rounded
+// quotients a 4-bit value, the second reading of partners (k_paged_write, which holds both halves of
+// a head in one lane, takes 32 us for the 8188 rows in bf16, and stays for what it can do).
 #include <math.h>
 #include <string.h>
 
@@ -28,7 +34,7 @@ struct RopeArgs {
 };
 
 // A CTA takes ROWS rows (see k_paged_write).
-template <typename T, Rows F, int ROWS>
+template <typename T, Rows F, int ROWS, bool PAIR>
 __global__ void __launch_bounds__(256) k_paged_write_rope(const RopeArgs a, const Turns turns) {
   __shared__ __align__(16) float cs[ROWS][2][DMTP_OPS_MAX_HEAD_DIM / 2];
   __shared__ int s_page[ROWS], s_off[ROWS], s_pos[ROWS];
@@ -39,6 +45,8 @@ __global__ void __launch_bounds__(256) k_paged_write_rope(const RopeArgs a, cons
   const bool on = gl < a.lanes;
   // a group's loop count is the CTA's: the shuffles below see every lane
   const int step = gridDim.y * ng, mine = threadIdx.x / a.group;
+  const bool pair = PAIR && 16 * gl < a.rot;
+  const int col[2] = {pair ? 8 * gl : 16 * gl, pair ? half + 8 * gl : 16 * gl + 8};
   Raw<T> x[2], y[2];  // this lane's columns, and their partners
   auto ask = [&](int it) {
     if (on && it < all) {
@@ -49,9 +57,9 @@ __global__ void __launch_bounds__(256) k_paged_write_rope(const RopeArgs a, cons
                                     : (const T*)a.r.v + row * a.r.v_row + (int64_t)(i - nq - hkv) * a.r.v_head;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int c = 16 * gl + 8 * h;
+        const int c = col[h];
         fetch(src + c, a.wide, x[h]);
-        if (!a.inter && c < a.rot && i < nq + hkv) fetch(src + (c < half ? c + half : c - half), a.wide, y[h]);
+        if (!PAIR && !a.inter && c < a.rot && i < nq + hkv) fetch(src + (c < half ? c + half : c - half), a.wide, y[h]);
       }
     }
   };
@@ -90,13 +98,36 @@ __global__ void __launch_bounds__(256) k_paged_write_rope(const RopeArgs a, cons
     const int r = ROWS == 1 ? 0 : it / items, i = it - r * items;
     const int page = it < all ? s_page[r] : -1;
     const bool live = on && page >= 0, isq = i < nq, isv = i >= nq + hkv;
-    if (live) {
+    if (pair && live) {
+      float v[8], w[8];
+      values(x[0], v);
+      values(x[1], w);
+      if (!isv) {
+#pragma unroll
+        for (int e = 0; e < 8; e += 4) {
+          const float4 co = *reinterpret_cast<const float4*>(&cs[r][0][8 * gl + e]);
+          const float4 si = *reinterpret_cast<const float4*>(&cs[r][1][8 * gl + e]);
+          const float cc[4] = {co.x, co.y, co.z, co.w}, ss[4] = {si.x, si.y, si.z, si.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float p = v[e + j], q = w[e + j];
+            v[e + j] = p * cc[j] - q * ss[j];
+            w[e + j] = q * cc[j] + p * ss[j];
+          }
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        f[e] = v[e];
+        f[8 + e] = w[e];
+      }
+    } else if (live) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int c = 16 * gl + 8 * h;
+        const int c = col[h];
         float v[8];
         values(x[h], v);
-        if (c < a.rot && !isv) {
+        if (!pair && c < a.rot && !isv) {
           if (a.inter) {
             const float4 co = *reinterpret_cast<const float4*>(&cs[r][0][c / 2]);
             const float4 si = *reinterpret_cast<const float4*>(&cs[r][1][c / 2]);
@@ -129,26 +160,42 @@ __global__ void __launch_bounds__(256) k_paged_write_rope(const RopeArgs a, cons
     __syncwarp();  // q_out may be q: no lane writes before its partners have read
     ask(it + step);
     if (live && isq) {
-      T* dst = (T*)a.r.q_out + (int64_t)(row0 + r) * a.r.qo_row + (int64_t)i * a.r.qo_head + 16 * gl;
+      T* dst = (T*)a.r.q_out + (int64_t)(row0 + r) * a.r.qo_row + (int64_t)i * a.r.qo_head;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         float v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = f[8 * h + e];
-        store8(dst + 8 * h, a.wide, v);
+        store8(dst + col[h], a.wide, v);
       }
     }
-    float block = 0.f, amax = 0.f;
-    bool odd = false;
+    float block[2] = {0.f, 0.f}, amax = 0.f;  // of the blocks that the chunks lie in
+    bool odd[2] = {false, false};
     if (F != kRaw) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
         const float m = fabsf(f[e]);
         const bool fine = m <= 3.402823466e38f;
-        odd = odd || !fine;
-        block = fmaxf(block, fine ? m : 0.f);
+        odd[e / 8] = odd[e / 8] || !fine;
+        block[e / 8] = fmaxf(block[e / 8], fine ? m : 0.f);
       }
-      amax = block;
+      amax = fmaxf(block[0], block[1]);
+      if (F == kE2M1) {
+        const float both = amax;
+        const bool any = odd[0] || odd[1];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (PAIR) {  // (every lane takes part)
+            const float other = __shfl_xor_sync(0xffffffffu, block[h], 1);
+            const bool theirs = __shfl_xor_sync(0xffffffffu, (int)odd[h], 1);
+            block[h] = pair ? fmaxf(block[h], other) : both;
+            odd[h] = pair ? odd[h] || theirs : any;
+          } else {
+            block[h] = both;
+            odd[h] = any;
+          }
+        }
+      }
       for (int o = a.group >> 1; o > 0; o >>= 1)
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     }
@@ -159,22 +206,33 @@ __global__ void __launch_bounds__(256) k_paged_write_rope(const RopeArgs a, cons
         const int e = e2m1_exponent(amax);
         const float inv = pow2f(-e);
         uint8_t* pg = (uint8_t*)(isv ? a.v : a.k) + at;
-        uint32_t b = e4m3_byte(__fdiv_rn(block * inv, 6.f));
-        const float bf = h2_to_f2(e4m3x2_to_h2(b)).x;
-        uint32_t w[2] = {0u, 0u};
-        if (odd) {
-          b = 0x7fu;
-        } else if (bf > 0.f) {
+        uint32_t b[2], w[2] = {0u, 0u};
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < 2; ++h) {
+          if (h && !pair) {
+            b[1] = b[0];
+          } else {
+            b[h] = e4m3_byte(__fdiv_rn(block[h] * inv, 6.f));
+            if (odd[h]) b[h] = 0x7fu;
+          }
+          const float bf = h2_to_f2(e4m3x2_to_h2(b[h])).x;
+          if (bf > 0.f) {  // (no NaN)
             float v[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] = __fdiv_rn(f[8 * h + j] * inv, bf);
             w[h] = e2m1x8(v);
           }
         }
-        *reinterpret_cast<uint2*>(pg + line * (hd / 2) + 8 * gl) = make_uint2(w[0], w[1]);
-        pg[e2m1_blocks(a.m) + line * (hd / 16) + gl] = (uint8_t)b;
+        if (pair) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            *reinterpret_cast<uint32_t*>(pg + line * (hd / 2) + col[h] / 2) = w[h];
+            if (gl % 2 == 0) pg[e2m1_blocks(a.m) + line * (hd / 16) + col[h] / 16] = (uint8_t)b[h];
+          }
+        } else {
+          *reinterpret_cast<uint2*>(pg + line * (hd / 2) + 8 * gl) = make_uint2(w[0], w[1]);
+          pg[e2m1_blocks(a.m) + line * (hd / 16) + gl] = (uint8_t)b[0];
+        }
         if (gl == 0) (isv ? a.vs : a.ks)[(int64_t)page * a.m.scale_stride + line] = pow2f(e);
       } else if (F == kE4M3) {
         const int e = e4m3_exponent(amax);
@@ -183,16 +241,18 @@ __global__ void __launch_bounds__(256) k_paged_write_rope(const RopeArgs a, cons
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           w[j] = e4m3_row4(make_float4(f[4 * j] * inv, f[4 * j + 1] * inv, f[4 * j + 2] * inv, f[4 * j + 3] * inv));
-        *reinterpret_cast<uint4*>((uint8_t*)(isv ? a.v : a.k) + at + line * hd + 16 * gl) = make_uint4(w[0], w[1], w[2], w[3]);
+        uint8_t* dst = (uint8_t*)(isv ? a.v : a.k) + at + line * hd;
+        *reinterpret_cast<uint2*>(dst + col[0]) = make_uint2(w[0], w[1]);
+        *reinterpret_cast<uint2*>(dst + col[1]) = make_uint2(w[2], w[3]);
         if (gl == 0) (isv ? a.vs : a.ks)[(int64_t)page * a.m.scale_stride + line] = pow2f(e);
       } else {
-        T* dst = (T*)(isv ? a.v : a.k) + at + line * hd + 16 * gl;
+        T* dst = (T*)(isv ? a.v : a.k) + at + line * hd;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           float v[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) v[e] = f[8 * h + e];
-          store8(dst + 8 * h, true, v);
+          store8(dst + col[h], true, v);
         }
       }
     }
@@ -314,14 +374,14 @@ const Turns& turns_of(const dmtp_rope& p) {
   return t;
 }
 
-template <typename T>
+template <typename T, bool PAIR>
 auto write_kernel(Rows f, bool few) {
-  return few ? (f == kE2M1   ? k_paged_write_rope<T, kE2M1, 1>
-                : f == kE4M3 ? k_paged_write_rope<T, kE4M3, 1>
-                             : k_paged_write_rope<T, kRaw, 1>)
-             : (f == kE2M1   ? k_paged_write_rope<T, kE2M1, 4>
-                : f == kE4M3 ? k_paged_write_rope<T, kE4M3, 4>
-                             : k_paged_write_rope<T, kRaw, 4>);
+  return few ? (f == kE2M1   ? k_paged_write_rope<T, kE2M1, 1, PAIR>
+                : f == kE4M3 ? k_paged_write_rope<T, kE4M3, 1, PAIR>
+                             : k_paged_write_rope<T, kRaw, 1, PAIR>)
+             : (f == kE2M1   ? k_paged_write_rope<T, kE2M1, 4, PAIR>
+                : f == kE4M3 ? k_paged_write_rope<T, kE4M3, 4, PAIR>
+                             : k_paged_write_rope<T, kRaw, 4, PAIR>);
 }
 
 }  // namespace
@@ -382,7 +442,9 @@ extern "C" int dmtp_paged_write_rope(const dmtp_paged_kv* c, const dmtp_paged_ro
   const dim3 grid(few ? r->n_rows : quads, few ? blocks : spread < rounds ? spread : rounds);
   static const Turns none = {};
   const Turns& t = p.dims ? turns_of(p) : none;
-  auto k = c->dtype ? write_kernel<bf16>(rows_of(*c), few) : write_kernel<float>(rows_of(*c), few);
+  const bool pair = a.rot && !a.inter && (c->e4m3 != DMTP_OPS_E2M1 || a.rot % 32 == 0);
+  auto k = c->dtype ? (pair ? write_kernel<bf16, true>(rows_of(*c), few) : write_kernel<bf16, false>(rows_of(*c), few))
+                    : (pair ? write_kernel<float, true>(rows_of(*c), few) : write_kernel<float, false>(rows_of(*c), few));
   return launch_op(k, grid, 256, 0, (cudaStream_t)stream, false, 1, a, t) == cudaSuccess
              ? DMTP_OK
              : (cudaGetLastError(), DMTP_ECUDA);

@@ -354,8 +354,8 @@ def reference(q, kv, spans, scale, hd, weights, cap=0.0, slopes=None, kbits=0.0)
                 ds += 4e-7 * np.abs(s).max()
             if slopes is not None:
                 s = s - slopes[h] * far
-                ds += 4 * U * (slopes[h] * far).max()
-                mag += (slopes[h] * far).max()
+                ds += 4 * U * (abs(slopes[h]) * far).max()
+                mag += (abs(slopes[h]) * far).max()
             w = np.exp(s - s.max())
             w /= w.sum()
             out[r, h] = w @ vv
@@ -744,3 +744,105 @@ def test_a_prompt_then_decode_steps():
             one = check_attention(c, q.view(2, 1, hq, hd), at, kv, cap=cap, slopes=slopes)
             # both are within their bounds: 2^-8 of the weights of one, 2^-11 of the other's
             assert np.abs(np64(one)[:, 0] - np64(out)).max() <= 2.0 ** -6 * 4
+
+
+# ---- what the larger pieces of the kernels could get wrong ------------------------------
+
+@pytest.mark.parametrize("dtype,rows", KINDS)
+@pytest.mark.parametrize("ps", [8, 64, 128, 256])
+@pytest.mark.parametrize("window", [3, 10, 129, 700])
+def test_prompt_windows_inside_pages(dtype, rows, ps, window):
+    """Intervals that begin and end inside a page, pages that no row sees not named at all."""
+    count, lens = [1, 40, 100], [777, 1000, 100]
+    g = gen(ps + window)
+    c = new_cache(3, -(-1024 // ps), ps, 1, 128, dtype, rows)
+    kv = fill_cache(c, lens, g)
+    table = c.table.cpu()
+    for b, (n, r) in enumerate(zip(lens, count)):
+        table[b, :max(0, n - r - window + 1) // ps] = -1
+        table[b, -(-n // ps):] = 10 ** 6
+    c.table.copy_(table)
+    st = starts(count)
+    q = randn((st[-1], 6, 128), g, dtype)
+    check_prompt(c, q, st, lens, kv, window=window)
+    check_prompt(c, q, st, lens, kv, window=window, slopes=slopes_of(6), cap=15.0)
+
+
+@pytest.mark.parametrize("dtype,rows", KINDS)
+@pytest.mark.parametrize("hd,ps", [(128, 128), (64, 32), (128, 24)])
+def test_prompt_of_several_tiles(dtype, rows, hd, ps):
+    """A prompt over several tiles and blocks of keys, scores of every kind."""
+    n = 700
+    g = gen(hd + ps)
+    c = new_cache(2, -(-900 // ps), ps, 1, hd, dtype, rows)
+    lens = [n, 900]
+    kv = fill_cache(c, lens, g)
+    st = starts([n, 130])
+    q = randn((st[-1], 3, hd), g, dtype, 2.0)
+    for kw in (dict(), dict(cap=8.0), dict(slopes=slopes_of(3)), dict(cap=60.0), dict(scale=-0.05, cap=3.0, slopes=-slopes_of(3))):
+        check_prompt(c, q, st, lens, kv, **kw)
+
+
+@pytest.mark.parametrize("dtype,rows", KINDS)
+def test_prompt_with_a_bias_that_leaves_only_near_positions(dtype, rows):
+    c = new_cache(1, 30, 32, 2, 64, dtype, rows)
+    g = gen(2)
+    kv = fill_cache(c, [900], g)
+    q = randn((900, 2, 64), g, dtype)
+    for slopes in ([50.0, 0.0], [1000.0, -0.5], [0.01, 3.0]):
+        check_prompt(c, q, [0, 900], [900], kv, slopes=torch.tensor(slopes, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype,rows", [(d, r) for d in (BF, FP) for r in ("e4m3", "e2m1")])
+def test_scales_that_are_no_powers_of_two(dtype, rows):
+    """Prompts on the tensor cores take such rows rounded to bf16."""
+    c = new_cache(2, 10, 32, 2, 128, dtype, rows)
+    g = gen(1)
+    fill_cache(c, [300, 300], g)
+    for s in (c.k_scale, c.v_scale):
+        s.mul_(0.5 + torch.rand(s.shape, device="cuda", generator=g))
+    kv = stored(c, [300, 300])
+    q = randn((310, 4, 128), g, dtype)
+    out = c.prompt_attention(q, i32([0, 300, 310]), i32([300, 300]))
+    spans = [(0, i, 0, i + 1) for i in range(300)] + [(1, 290 + i, 0, 291 + i) for i in range(10)]
+    tc = tensor_cores(c)
+    ref, tol = reference(np64(q), kv, spans, 128 ** -0.5, 128, 2.0 ** -8 if tc else 2.0 ** -24, kbits=2.0 ** -8 if tc else 0.0)
+    close(out, ref, tol, dtype)
+    check_attention(c, randn((2, 3, 4, 128), g, dtype), [300, 300], kv)
+
+
+@pytest.mark.parametrize("dtype,rows", KINDS)
+def test_few_rows_over_a_long_cache_with_values_that_are_not_finite(dtype, rows):
+    """Split keys: the range with such a value is computed row by row, the rest as ever."""
+    c = new_cache(1, 100, 64, 1, 128, dtype, rows)
+    g = gen(5)
+    fill_cache(c, [6000], g)
+    q = randn((6, 4, 128), g, dtype)
+    want = c.prompt_attention(q, i32([0, 6]), i32([6000]), first=i32([3100] * 6))
+    bad = torch.full((1, 1, 128), float("nan"), dtype=dtype, device="cuda")
+    c.write(bad, bad, i32([0]), i32([3090]))        # in the first block of keys, seen by none
+    got = c.prompt_attention(q, i32([0, 6]), i32([6000]), first=i32([3100] * 6))
+    c.check()
+    d = np.abs(np64(got) - np64(want))
+    assert (d <= 2 * HALF[dtype] * np.abs(np64(want)) + 2.0 ** -8 * 0.5).all()
+    assert np.isnan(np64(c.prompt_attention(q, i32([0, 6]), i32([6000])))).all()
+
+
+@pytest.mark.parametrize("dtype,rows", KINDS)
+@pytest.mark.parametrize("cap,bias", [(0.0, False), (10.0, True)])
+def test_decode_rows_that_do_not_see_what_is_not_finite(dtype, rows, cap, bias):
+    c = new_cache(2, 20, 16, 2, 64, dtype, rows)
+    g = gen(0)
+    lens = [300, 100]
+    fill_cache(c, lens, g)
+    q = randn((2, 8, 4, 64), g, dtype)
+    sl = slopes_of(4) if bias else None
+    want = np64(c.attention(q, i32(lens), cap=cap, slopes=sl, window=50))
+    z = torch.full((3, 2, 64), float("nan"), dtype=dtype, device="cuda")
+    c.write(z, z, i32([0, 0, 1]), i32([296, 200, 97]))      # seen by rows 4.., by none, by rows 5..
+    got = np64(c.attention(q, i32(lens), cap=cap, slopes=sl, window=50))
+    c.check()
+    assert np.isnan(got[0, 4:]).all() and np.isnan(got[1, 5:]).all()
+    for b, n in ((0, 4), (1, 5)):
+        d = np.abs(got[b, :n] - want[b, :n])
+        assert (d <= 2 * HALF[dtype] * np.abs(want[b, :n]) + 2.0 ** -10 * 4).all()

@@ -5,10 +5,10 @@
 // row is then two neighbours' business; where the half is no whole number of blocks, chunks stay
 // side by side and the partners are read once more. The bytes moved are the rows
 // once in and once out: 8188 rows of 32 + 2 x 4 heads of 128, half of each rotated, into E4M3 pages
-// take 44 us (160 MB, 0.53 of the copy rate), 32 rows into bf16 pages 3.8 us, which is latency; 4096 rows
-// into E2M1 pages and back 29 us (89 MB in two launches). Issue bounds the many-row form: two rounded
-// quotients a 4-bit value, the second reading of partners (k_paged_write, which holds both halves of
-// a head in one lane, takes 32 us for the 8188 rows in bf16, and stays for what it can do).
+// take 37 us (160 MB, 0.63 of the copy rate; with partners read twice 44), whole heads into bf16 pages 36
+// (interleaved 39; k_paged_write, which knows its pairs beforehand, 32), 32 rows 3.8 us, which is
+// latency; 4096 rows into E2M1 pages and back 29 us (89 MB in two launches). Issue bounds the many-row
+// form, of 4-bit rows two rounded quotients a value.
 #include <math.h>
 #include <string.h>
 

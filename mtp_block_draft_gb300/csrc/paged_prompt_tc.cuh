@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(Shape<HD, F>::kThreads, 1)
           const int slot = n % NS, t = n >> 1;
           const bool isv = n & 1;
           if (!isv) publish(t);
-          if (ok) ok = mbar_wait(smem_u32(empty + slot), ((n / NS) & 1) ^ 1, p.err);
+          if (ok) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(empty + slot), ((n / NS) & 1) ^ 1, p.err));
           const int j = block(t);
           const uint32_t to = smem_u32(ring + slot * Sh::kSlot), bar = smem_u32(full + slot);
           const bf16* base = (const bf16*)(isv ? p.v : p.k) + (int64_t)kvh * p.m.page_size * hd;

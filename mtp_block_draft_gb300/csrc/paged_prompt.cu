@@ -63,7 +63,7 @@ int plan(const dmtp_paged_kv* c, const dmtp_paged_prompt* a, PromptPlan* pl) {
   // Few units: their keys are split so that all together fill the SMs once (the CUDA-core kernel's two
   // CTAs an SM), into ranges of 512 positions of the table's reach at least. 32 / 4 heads of 128, us, whole /
   // split: 8 rows over 32768 bf16 positions 267 / 42, 64 rows 299 / 51, over 2048 33 / 26, 256 rows over
-  // 2048 38 / 31, 4 x 16 rows over 4096 53 / 26; fp32, 64 rows over 16384 2635 / 505. Ranges of 256: 512
+  // 2048 38 / 31, 4 x 16 rows over 4096 53 / 26; fp32, 64 rows over 16384 2635 / 505 (469 now). Ranges of 256: 512
   // rows over nothing 27.5 instead of 20.3, 64 rows over 2048 24.4 instead of 25.8.
   int64_t s = units ? (pl->tc ? 152 : 304) / units : 1;
   const int64_t most = reach / 512;

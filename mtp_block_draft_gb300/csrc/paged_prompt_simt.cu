@@ -4,8 +4,10 @@
 // A CTA of 256 threads has a tile of 64 queries and goes through the keys 64 (heads over 128
 // columns: 32) at a time, Q, K and V as fp32 in shared memory. A thread has 4 queries: of the
 // scores with 4 keys, of the output with a sixteenth of the columns: per four columns and key pair of
-// loads 64 fused operations, so the fp32 pipes bound it (16384 bf16 rows of 32 / 4 heads of 128, which
-// the tensor cores take, took 66 ms here: 33 TFLOP/s).
+// loads 64 fused operations, two an instruction (sums over even and odd columns, two columns of the
+// output), so the fp32 pipes bound it: 64 fp32 rows of 32 / 4 heads of 128 over 16384 positions 469 us
+// (one an instruction 505), 2048 rows 1.08 ms, 32 TFLOP/s with what the causal blocks waste. (16384
+// bf16 rows, which the tensor cores take, took 66 ms here.)
 #include <type_traits>
 
 #include "paged_prompt.cuh"
@@ -94,13 +96,14 @@ __global__ void __launch_bounds__(kThreads, HDM > 128 ? 1 : 2) k_prompt_simt(con
   const int j_first = least < most ? least / TK : 0, tiles = least < most ? (most + TK - 1) / TK - j_first : 0;
   const int t0 = (int)((int64_t)tiles * blockIdx.z / p.splits), t1 = (int)((int64_t)tiles * (blockIdx.z + 1) / p.splits);
 
-  float o[4][CJ][4], m[4], l[4];
+  f32x2 o[4][CJ][2];  // two columns each
+  float m[4], l[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     m[i] = -INFINITY;
     l[i] = 0.f;
 #pragma unroll
-    for (int c = 0; c < CJ; ++c) o[i][c][0] = o[i][c][1] = o[i][c][2] = o[i][c][3] = 0.f;
+    for (int c = 0; c < CJ; ++c) o[i][c][0] = o[i][c][1] = 0ull;
   }
   for (int t = t0; t < t1; ++t) {
     const int j0 = (j_first + t) * TK;
@@ -133,22 +136,31 @@ __global__ void __launch_bounds__(kThreads, HDM > 128 ? 1 : 2) k_prompt_simt(con
     }
     odd = __syncthreads_or(odd);
     float s[4][KJ];
+    {
+      f32x2 s2[4][KJ];  // the sums over even and over odd columns
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < KJ; ++j) s[i][j] = 0.f;
+        for (int j = 0; j < KJ; ++j) s2[i][j] = 0ull;
 #pragma unroll 2
-    for (int d = 0; d < hd; d += 4) {
-      float4 a[4];
+      for (int d = 0; d < hd; d += 4) {
+        ulonglong2 a[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(sQ + (4 * ty + i) * pitch + d);
+        for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const ulonglong2*>(sQ + (4 * ty + i) * pitch + d);
 #pragma unroll
-      for (int j = 0; j < KJ; ++j) {
-        const float4 b = *reinterpret_cast<const float4*>(sK + (tx + 16 * j) * pitch + d);
+        for (int j = 0; j < KJ; ++j) {
+          const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(sK + (tx + 16 * j) * pitch + d);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          s[i][j] = fmaf(a[i].w, b.w, fmaf(a[i].z, b.z, fmaf(a[i].y, b.y, fmaf(a[i].x, b.x, s[i][j]))));
+          for (int i = 0; i < 4; ++i) s2[i][j] = fma2(a[i].y, b.y, fma2(a[i].x, b.x, s2[i][j]));
+        }
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < KJ; ++j) {
+          const float2 x = unpack(s2[i][j]);
+          s[i][j] = x.x + x.y;
+        }
     }
     __syncthreads();  // K has been read: its place takes the weights
 #pragma unroll
@@ -172,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, HDM > 128 ? 1 : 2) k_prompt_simt(con
 #pragma unroll
       for (int c = 0; c < CJ; ++c)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[i][c][e] *= fix;
+        for (int e = 0; e < 2; ++e) o[i][c][e] = mul2(o[i][c][e], both(fix));
 #pragma unroll
       for (int j = 0; j < KJ; ++j) {
         const float x = ex2(s[i][j] - ref);
@@ -196,13 +208,11 @@ __global__ void __launch_bounds__(kThreads, HDM > 128 ? 1 : 2) k_prompt_simt(con
           for (int c = 0; c < CJ; ++c) {
             const int d = 64 * c + 4 * tx;
             if (d >= hd) break;
-            const float4 v = *reinterpret_cast<const float4*>(sV + (k + y) * pitch + d);
+            const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(sV + (k + y) * pitch + d);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              o[i][c][0] = fmaf(x[i][y], v.x, o[i][c][0]);
-              o[i][c][1] = fmaf(x[i][y], v.y, o[i][c][1]);
-              o[i][c][2] = fmaf(x[i][y], v.z, o[i][c][2]);
-              o[i][c][3] = fmaf(x[i][y], v.w, o[i][c][3]);
+              o[i][c][0] = fma2(both(x[i][y]), v.x, o[i][c][0]);
+              o[i][c][1] = fma2(both(x[i][y]), v.y, o[i][c][1]);
             }
           }
       }
@@ -217,8 +227,9 @@ __global__ void __launch_bounds__(kThreads, HDM > 128 ? 1 : 2) k_prompt_simt(con
           for (int i = 0; i < 4; ++i) {
             const float x = sP[(4 * ty + i) * PP + k];
             if (x != 0.f) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) o[i][c][e] = fmaf(x, sV[k * pitch + d + e], o[i][c][e]);
+              const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(sV + k * pitch + d);
+              o[i][c][0] = fma2(both(x), v.x, o[i][c][0]);
+              o[i][c][1] = fma2(both(x), v.y, o[i][c][1]);
             }
           }
         }
@@ -237,8 +248,7 @@ __global__ void __launch_bounds__(kThreads, HDM > 128 ? 1 : 2) k_prompt_simt(con
 #pragma unroll
       for (int c = 0; c < CJ; ++c)
         if (64 * c + 4 * tx < hd)
-          *reinterpret_cast<float4*>(p.part_o + (part + t) * hd + 64 * c + 4 * tx) =
-              make_float4(o[i][c][0], o[i][c][1], o[i][c][2], o[i][c][3]);
+          *reinterpret_cast<ulonglong2*>(p.part_o + (part + t) * hd + 64 * c + 4 * tx) = make_ulonglong2(o[i][c][0], o[i][c][1]);
       continue;
     }
     const int r = (w.q0 + t) / p.group, head = kvh * p.group + (w.q0 + t - r * p.group);
@@ -246,9 +256,10 @@ __global__ void __launch_bounds__(kThreads, HDM > 128 ? 1 : 2) k_prompt_simt(con
     const float inv = l[i] != 0.f ? 1.f / l[i] : 0.f;
 #pragma unroll
     for (int c = 0; c < CJ; ++c)
-      if (64 * c + 4 * tx < hd)
-        store_act4(out + 64 * c + 4 * tx, 0,
-                   make_float4(o[i][c][0] * inv, o[i][c][1] * inv, o[i][c][2] * inv, o[i][c][3] * inv));
+      if (64 * c + 4 * tx < hd) {
+        const float2 x = unpack(mul2(o[i][c][0], both(inv))), y = unpack(mul2(o[i][c][1], both(inv)));
+        store_act4(out + 64 * c + 4 * tx, 0, make_float4(x.x, x.y, y.x, y.y));
+      }
   }
 }
 
